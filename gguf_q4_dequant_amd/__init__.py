@@ -14,13 +14,19 @@ CPU fallback.
     h = matmul_swiglu(w_gate, w_up, x)  # silu(x.Wg^T) * (x.Wu^T), the down projection's input
     ws = load_q4k("model.gguf")         # Q4_K tensors of a GGUF file, bytes unchanged, on the device
 
-Names and semantics mirror include/q4k.h.
+    r = moe_route(router_logits, top_k)  # experts, weights and the groups of a mixture-of-experts layer
+    h = matmul_grouped_swiglu(w_gate, w_up, x, r.offsets, r.rows, x_div=top_k)  # w: uint8 [E, N, K/256*144]
+    y = matmul_grouped_combine(w_down, h, r)   # each token's weighted sum over its experts
+    a = Adjustment(history=recent, repetition=r, mask=grammar)  # penalties, biases, allowed tokens
+    index, value = matmul_argmax(w, x, adjustment=a)  # greedy selection under them
+
+Names and semantics mirror include/q4k.h, include/q4k_moe.h, include/q4k_select.h and include/q4a.h.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Iterable, Optional, Sequence, Tuple
+from typing import Iterable, NamedTuple, Optional, Sequence, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_PKG, "libq4k.so")
@@ -51,7 +57,8 @@ PATH_GEMV = 3
 EXPORTED = ("q4k_matmul", "q4k_matmul_batched", "q4k_matmul_path", "q4k_matmul_batched_path",
             "q4k_matmul_batched_noalloc", "q4a_matmul", "q4a_matmul_batched",
             "q4k_matmul_argmax", "q4k_matmul_swiglu", "q4k_gguf_list", "q4k_select_path", "q4k_strerror",
-            "q4k_version")
+            "q4k_version", "q4k_moe_route", "q4k_moe_group", "q4k_matmul_grouped", "q4k_matmul_grouped_swiglu",
+            "q4k_matmul_grouped_combine", "q4k_logits_adjust", "q4k_logits_argmax", "q4k_matmul_argmax_adjusted")
 
 
 class Q4KError(RuntimeError):
@@ -63,6 +70,12 @@ class Q4KError(RuntimeError):
 class _Problem(ctypes.Structure):
     _fields_ = [("w_packed", ctypes.c_void_p), ("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("N", ctypes.c_int), ("K", ctypes.c_int)]
+
+
+class _Adjustment(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_id", ctypes.c_void_p), ("bias_value", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("history_len", ctypes.c_int), ("bias_len", ctypes.c_int)]
 
 
 class GgufTensor(ctypes.Structure):
@@ -101,6 +114,23 @@ def library() -> ctypes.CDLL:
     lib.q4a_matmul.restype = ci
     lib.q4a_matmul_batched.argtypes = [ctypes.POINTER(_QaProblem), ci, ci, vp]
     lib.q4a_matmul_batched.restype = ci
+    cf, adj = ctypes.c_float, ctypes.POINTER(_Adjustment)
+    lib.q4k_moe_route.argtypes = [vp, vp, ci, ci, ci, ci, cf, vp, vp, vp, vp, vp]
+    lib.q4k_moe_route.restype = ci
+    lib.q4k_moe_group.argtypes = [vp, ci, ci, vp, vp, vp]
+    lib.q4k_moe_group.restype = ci
+    lib.q4k_matmul_grouped.argtypes = [vp, vp, ci, vp, vp, vp, ci, ci, ci, ci, vp]
+    lib.q4k_matmul_grouped.restype = ci
+    lib.q4k_matmul_grouped_swiglu.argtypes = [vp, vp, vp, ci, vp, vp, vp, ci, ci, ci, ci, vp]
+    lib.q4k_matmul_grouped_swiglu.restype = ci
+    lib.q4k_matmul_grouped_combine.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
+    lib.q4k_matmul_grouped_combine.restype = ci
+    lib.q4k_logits_adjust.argtypes = [vp, vp, adj, ci, ci, vp]
+    lib.q4k_logits_adjust.restype = ci
+    lib.q4k_logits_argmax.argtypes = [vp, adj, ci, ci, vp, vp, vp]
+    lib.q4k_logits_argmax.restype = ci
+    lib.q4k_matmul_argmax_adjusted.argtypes = [vp, vp, adj, ci, ci, ci, vp, vp, vp]
+    lib.q4k_matmul_argmax_adjusted.restype = ci
     lib.q4k_gguf_list.argtypes = [ctypes.c_char_p, ctypes.POINTER(GgufTensor), ci, ctypes.POINTER(ci)]
     lib.q4k_gguf_list.restype = ci
     lib.q4k_select_path.argtypes = [ci, ci, ci]
@@ -189,10 +219,12 @@ def _check_outputs(x, index, value, M):
             raise ValueError(f"{name} must be contiguous")
 
 
-def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=None):
+def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=None, adjustment=None):
     """(index int32 [M], value float32 [M]): for each row of x, the lowest n with
     the largest y[m, n] of y = x . dequant(w)^T, and that value.  The logits stay
-    on the device (library workspace).  N defaults to w's leading dimension."""
+    on the device (library workspace).  N defaults to w's leading dimension.
+    With an ``Adjustment`` the choice is made under its penalties, biases and
+    mask (as by logits_argmax)."""
     import torch
     if N is None:
         if w.dim() != 2:
@@ -213,11 +245,277 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
     if value is None:
         value = torch.empty(M, dtype=torch.float32, device=x.device)
     _check_outputs(x, index, value, M)
+    if adjustment is not None:
+        rc = library().q4k_matmul_argmax_adjusted(w.data_ptr(), x.data_ptr(), adjustment._checked(x, M, N), M, N, K,
+                                                  index.data_ptr(), value.data_ptr(), _stream_handle(stream))
+        if rc != OK:
+            raise Q4KError(rc, "q4k_matmul_argmax_adjusted")
+        return index, value
     rc = library().q4k_matmul_argmax(w.data_ptr(), x.data_ptr(), M, N, K, index.data_ptr(),
                                      value.data_ptr(), _stream_handle(stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_argmax")
     return index, value
+
+
+def _checked_tensor(name, t, dtype, shape, like):
+    """t is a contiguous tensor of this dtype and shape on like's device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be shaped {list(shape)}, not {list(t.shape)}")
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a device tensor on {like.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class Adjustment:
+    """What is applied to logits [M, N] before a token is chosen (include/q4k_select.h);
+    every part is optional, all are device tensors:
+
+    history int32 [M, L]: recent tokens of each sequence, entries outside [0, N)
+        (padding) count for nothing; with it, float32 [M] each:
+        repetition: z > 0 ? z / r : z * r for tokens that occur in the history,
+        frequency: z - f * (number of occurrences), presence: z - p;
+    bias_id int32 [M, B], bias_value float32 [M, B]: added to the named tokens
+        (several for one token add up; ids outside [0, N) are skipped);
+    mask int32 or uint32 [M, ceil(N / 32)]: token n is allowed where bit n % 32
+        of word n / 32 is set, else its logit is -inf.
+
+    The tensors are read by the calls that are given the object, not before."""
+
+    __slots__ = ("history", "repetition", "frequency", "presence", "bias_id", "bias_value", "mask")
+
+    def __init__(self, history=None, repetition=None, frequency=None, presence=None, bias_id=None, bias_value=None,
+                 mask=None):
+        if (bias_id is None) != (bias_value is None):
+            raise ValueError("bias_id and bias_value come together")
+        if history is None and not (repetition is None and frequency is None and presence is None):
+            raise ValueError("repetition, frequency and presence need a history")
+        self.history, self.repetition, self.frequency, self.presence = history, repetition, frequency, presence
+        self.bias_id, self.bias_value, self.mask = bias_id, bias_value, mask
+
+    def _checked(self, like, M, N):
+        """The C struct for logits [M, N] on like's device."""
+        import torch
+        c = _Adjustment()
+        if self.history is not None:
+            if self.history.dim() != 2:
+                raise ValueError("history must be int32 [M, L]")
+            c.history_len = self.history.shape[1]
+            c.history = _checked_tensor("history", self.history, torch.int32, (M, c.history_len), like)
+            for name in ("repetition", "frequency", "presence"):
+                t = getattr(self, name)
+                if t is not None:
+                    setattr(c, name, _checked_tensor(name, t, torch.float32, (M,), like))
+        if self.bias_id is not None:
+            if self.bias_id.dim() != 2:
+                raise ValueError("bias_id must be int32 [M, B]")
+            c.bias_len = self.bias_id.shape[1]
+            c.bias_id = _checked_tensor("bias_id", self.bias_id, torch.int32, (M, c.bias_len), like)
+            c.bias_value = _checked_tensor("bias_value", self.bias_value, torch.float32, (M, c.bias_len), like)
+        if self.mask is not None:
+            dtype = torch.uint32 if self.mask.dtype == torch.uint32 else torch.int32
+            c.mask = _checked_tensor("mask", self.mask, dtype, (M, (N + 31) // 32), like)
+        return c
+
+
+def _checked_logits(logits):
+    import torch
+    if logits.dim() != 2 or logits.dtype != torch.float32:
+        raise TypeError("logits must be float32 [M, N]")
+    if not logits.is_cuda or not logits.is_contiguous():
+        raise ValueError("logits must be a contiguous device tensor")
+    return logits.shape
+
+
+def logits_adjust(logits, adjustment, out=None, stream=None):
+    """The logits float32 [M, N] under an ``Adjustment`` (penalties, biases, -inf
+    where the mask forbids), in a new tensor or in ``out`` (which may be logits)."""
+    import torch
+    M, N = _checked_logits(logits)
+    if out is None:
+        out = torch.empty_like(logits)
+    elif out is not logits:
+        _checked_tensor("out", out, torch.float32, (M, N), logits)
+    rc = library().q4k_logits_adjust(logits.data_ptr(), out.data_ptr(), adjustment._checked(logits, M, N), M, N,
+                                     _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_logits_adjust")
+    return out
+
+
+def logits_argmax(logits, adjustment, index=None, value=None, stream=None):
+    """(index int32 [M], value float32 [M]): for each row of logits [M, N] the lowest
+    allowed token with the largest adjusted logit, and that logit; index -1 and
+    value -inf where the mask (or NaN) leaves nothing.  The adjusted logits are
+    not written."""
+    import torch
+    M, N = _checked_logits(logits)
+    if index is None:
+        index = torch.empty(M, dtype=torch.int32, device=logits.device)
+    if value is None:
+        value = torch.empty(M, dtype=torch.float32, device=logits.device)
+    _check_outputs(logits, index, value, M)
+    rc = library().q4k_logits_argmax(logits.data_ptr(), adjustment._checked(logits, M, N), M, N, index.data_ptr(),
+                                     value.data_ptr(), _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_logits_argmax")
+    return index, value
+
+
+MAX_EXPERTS = 1024
+MAX_TOP_K = 64
+ROUTE_SIGMOID = 1
+ROUTE_NORMALIZE = 2
+
+
+class Routing(NamedTuple):
+    """A routed batch: expert int32 [M, top_k] (-1: none), weight float32 [M, top_k],
+    and the groups of its pairs p = m * top_k + j: offsets int32 [E + 1] and
+    rows int32 [M * top_k], group e being rows[offsets[e]:offsets[e + 1]]."""
+    expert: object
+    weight: object
+    offsets: object
+    rows: object
+
+
+def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, normalize: bool = True, scale: float = 1.0,
+              out: Optional[Routing] = None, stream=None) -> Routing:
+    """Each token's top_k experts, their weights, and the pairs grouped by expert
+    (q4k_moe_route).  logits float32 [M, E]; scores are their softmax, or with
+    ``sigmoid`` their sigmoid; ``bias`` float32 [E] takes part in the choice
+    only; ``normalize`` divides a token's weights by their sum."""
+    import torch
+    M, E = _checked_logits(logits)
+    k = int(top_k)
+    if not (1 <= E <= MAX_EXPERTS and 1 <= k <= min(E, MAX_TOP_K)):
+        raise Q4KError(ERR_BAD_DIM, f"E={E} top_k={k}")
+    bias_ptr = None if bias is None else _checked_tensor("bias", bias, torch.float32, (E,), logits)
+    if out is None:
+        dev = logits.device
+        out = Routing(torch.empty((M, k), dtype=torch.int32, device=dev),
+                      torch.empty((M, k), dtype=torch.float32, device=dev),
+                      torch.empty(E + 1, dtype=torch.int32, device=dev),
+                      torch.empty(M * k, dtype=torch.int32, device=dev))
+    else:
+        _checked_tensor("expert", out.expert, torch.int32, (M, k), logits)
+        _checked_tensor("weight", out.weight, torch.float32, (M, k), logits)
+        _checked_tensor("offsets", out.offsets, torch.int32, (E + 1,), logits)
+        _checked_tensor("rows", out.rows, torch.int32, (M * k,), logits)
+    flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_NORMALIZE if normalize else 0)
+    rc = library().q4k_moe_route(logits.data_ptr(), bias_ptr, M, E, k, flags, float(scale), out.expert.data_ptr(),
+                                 out.weight.data_ptr(), out.offsets.data_ptr(), out.rows.data_ptr(),
+                                 _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_moe_route")
+    return out
+
+
+def moe_group(expert, E: int, stream=None):
+    """(offsets int32 [E + 1], rows int32 [P]): the groups of an existing table of
+    choices, int32 of any shape with P entries (outside [0, E): in no group)."""
+    import torch
+    if expert.dtype != torch.int32:
+        raise TypeError("expert must be int32")
+    if not expert.is_cuda or not expert.is_contiguous():
+        raise ValueError("expert must be a contiguous device tensor")
+    P, E = expert.numel(), int(E)
+    if not 1 <= E <= MAX_EXPERTS:
+        raise Q4KError(ERR_BAD_DIM, f"E={E}")
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
+    rows = torch.empty(P, dtype=torch.int32, device=expert.device)
+    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(), _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_moe_group")
+    return offsets, rows
+
+
+def _grouped_checked(ws, x, offsets, rows, x_div):
+    """Validate the operands of a grouped product; returns (P, E, N, K, rows pointer)."""
+    import torch
+    if x.dtype != torch.float32 or x.dim() != 2 or any(w.dtype != torch.uint8 or w.dim() != 3 for w in ws):
+        raise TypeError("expected w uint8 [E, N, K/256*144] and x float32 [rows, K]")
+    if not (x.is_cuda and x.is_contiguous()):
+        raise ValueError("x must be a contiguous device tensor")
+    E, N, row_bytes = ws[0].shape
+    K = x.shape[1]
+    if K % BLOCK_WEIGHTS != 0 or K == 0:
+        raise Q4KError(ERR_BAD_DIM, f"K={K}")
+    if not 1 <= E <= MAX_EXPERTS:
+        raise Q4KError(ERR_BAD_DIM, f"E={E}")
+    for w in ws:
+        _checked_tensor("w", w, torch.uint8, (E, N, K // BLOCK_WEIGHTS * BLOCK_BYTES), x)
+    _checked_tensor("offsets", offsets, torch.int32, (E + 1,), x)
+    if x_div < 1:
+        raise Q4KError(ERR_BAD_DIM, f"x_div={x_div}")
+    if rows is None:
+        return x.shape[0] * x_div, E, N, K, None
+    P = rows.numel()
+    ptr = _checked_tensor("rows", rows, torch.int32, (P,), x)
+    if (P + x_div - 1) // x_div != x.shape[0]:
+        raise ValueError(f"x has {x.shape[0]} rows, expected {P} pairs / x_div {x_div}")
+    return P, E, N, K, ptr
+
+
+def matmul_grouped(w, x, offsets, rows=None, y=None, x_div: int = 1, stream=None):
+    """y[p] = x[p // x_div] . dequant(w[e])^T for every pair p = rows[i] of group e
+    (offsets[e] <= i < offsets[e + 1]); w uint8 [E, N, K/256*144], y float32
+    [P, N].  Rows of pairs in no group are left as they were (in a ``y`` made
+    here they hold nothing meaningful).  rows None: pairs already in expert order."""
+    import torch
+    P, E, N, K, rows_ptr = _grouped_checked((w,), x, offsets, rows, x_div)
+    if y is None:
+        y = torch.empty((P, N), dtype=torch.float32, device=x.device)
+    else:
+        _checked_tensor("y", y, torch.float32, (P, N), x)
+    rc = library().q4k_matmul_grouped(w.data_ptr(), x.data_ptr(), x_div, offsets.data_ptr(), rows_ptr, y.data_ptr(),
+                                      E, P, N, K, _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_matmul_grouped")
+    return y
+
+
+def matmul_grouped_swiglu(w_gate, w_up, x, offsets, rows=None, out=None, x_div: int = 1, stream=None):
+    """out[p] = silu(x[p // x_div] . dequant(w_gate[e])^T) * (x[p // x_div] . dequant(w_up[e])^T)
+    for every pair p of group e; arguments as for matmul_grouped."""
+    import torch
+    P, E, N, K, rows_ptr = _grouped_checked((w_gate, w_up), x, offsets, rows, x_div)
+    if out is None:
+        out = torch.empty((P, N), dtype=torch.float32, device=x.device)
+    else:
+        _checked_tensor("out", out, torch.float32, (P, N), x)
+    rc = library().q4k_matmul_grouped_swiglu(w_gate.data_ptr(), w_up.data_ptr(), x.data_ptr(), x_div,
+                                             offsets.data_ptr(), rows_ptr, out.data_ptr(), E, P, N, K,
+                                             _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_matmul_grouped_swiglu")
+    return out
+
+
+def matmul_grouped_combine(w, x, routing: Routing, out=None, stream=None):
+    """out[m] = sum_j weight[m, j] * (x[m * top_k + j] . dequant(w[expert[m, j]])^T),
+    the experts' down projections and each token's weighted sum; x float32
+    [M * top_k, K], out float32 [M, N]."""
+    import torch
+    P, E, N, K, rows_ptr = _grouped_checked((w,), x, routing.offsets, routing.rows, 1)
+    if routing.expert.dim() != 2 or routing.expert.numel() != P:
+        raise ValueError(f"expert must be [M, top_k] with {P} entries")
+    M, top_k = routing.expert.shape
+    _checked_tensor("expert", routing.expert, torch.int32, (M, top_k), x)
+    _checked_tensor("weight", routing.weight, torch.float32, (M, top_k), x)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    else:
+        _checked_tensor("out", out, torch.float32, (M, N), x)
+    rc = library().q4k_matmul_grouped_combine(w.data_ptr(), x.data_ptr(), routing.expert.data_ptr(),
+                                              routing.weight.data_ptr(), routing.offsets.data_ptr(), rows_ptr,
+                                              out.data_ptr(), E, M, top_k, N, K, _stream_handle(stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_matmul_grouped_combine")
+    return out
 
 
 def matmul_swiglu(w_gate, w_up, x, out=None, stream=None):

@@ -1,0 +1,392 @@
+// Products grouped by expert over packed Q4_K weights: y[p] = x[row of p] .
+// dequant(W[e])^T for every pair p of group e (include/q4k_moe.h), the gate/up
+// form with its SwiGLU epilogue, and the weighted sum over a token's experts.
+//
+// What is computed.  A Q4_K weight is w = d * sc_j * q - dmin * m_j with the
+// 6-bit sc_j, m_j of its 32-weight sub-block j and the 4-bit quant q, so for a
+// token t, a row n of W and one super-block
+//   y += d * (sum_k x_k * (sc q)_k) - dmin * (sum_j m_j X_j),   X_j = sum of x over sub-block j.
+//   * sc * q <= 945 is an integer below 2^11: exact as a binary16.  A nibble in
+//     the low bits of a 16-bit lane is the binary16 subnormal q * 2^-24 (one AND
+//     for two weights), times sc in binary16 (v_pk_mul_f16) the subnormal
+//     sc * q * 2^-24, still exact; the matrix cores keep subnormals.  Both
+//     scales d and dmin stay out of the operand and are applied to the fp32
+//     sums once per super-block of 256, so nothing of W is ever rounded.
+//   * x is scaled by a power of two per row, 2^e, that puts the row's largest
+//     magnitude in [2^14, 2^15), and split into two binary16 values, hi =
+//     rn(x'), lo = rn(x' - hi): about 22 bits of every value, and an absolute
+//     error below 2^-40 of the row's maximum where lo is subnormal.  Both
+//     enter the same fp32 accumulator: two v_mfma_f32_16x16x32_f16 per 32
+//     weights, half the binary16 matrix rate at fp32 accuracy.
+//   * The min term is one more MFMA per super-block: the eight X_j (hi and lo
+//     in k-quarters 0 and 1) times the eight m_j as subnormals.
+//
+// k order.  The order of k inside an MFMA is free as long as both operands
+// agree.  Lane quarter c of a wave (lanes 16c .. 16c + 15, one row of W each)
+// takes group c of the super-block, 32 contiguous quant bytes = sub-blocks 2c
+// (low nibbles) and 2c + 1 (high): a lane reads 32 bytes of its row in two
+// 16-byte loads and needs two of the eight scales.  Step s = 2i + h uses bytes
+// 8i .. 8i + 7 of every group, nibble h; inside a step a lane's eight k are
+// 8i + {0, 2, 1, 3, 4, 6, 5, 7} (bytes 0, 2 and 1, 3 of a dword come out of one
+// AND each).  The staged x is laid out in that order once per call.
+#include <limits.h>
+#include <math.h>
+
+#include "../../include/q4k_moe.h"
+#include "q4k_internal.h"
+
+namespace q4k {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+constexpr int kImageBlock = 1024;  // staged bytes per super-block of a row: 8 steps x (hi, lo) x 4 quarters x 16
+constexpr int kSumsBlock = 32;     // eight sub-block sums, hi then lo
+
+struct Staged {
+    const uint8_t *img;   // [rows][K / 256][kImageBlock]
+    const uint8_t *sums;  // [rows][K / 256][kSumsBlock]
+    const float *back;    // [rows]: 2^(24 - e)
+};
+
+// Stages one row of x per workgroup (see above): thread u takes eight
+// consecutive values at a time.
+__global__ __launch_bounds__(256) void stage_rows_kernel(const float *x, int K, uint8_t *img, uint8_t *sums,
+                                                         float *back) {
+    __shared__ float wave_mx[4];
+    const size_t row = blockIdx.x;
+    const float *xr = x + row * K;
+    float mx = 0.f;
+    for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
+        const float4 a = *reinterpret_cast<const float4 *>(xr + k), b = *reinterpret_cast<const float4 *>(xr + k + 4);
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))));
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    if ((threadIdx.x & 63) == 0) wave_mx[threadIdx.x >> 6] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(wave_mx[0], wave_mx[1]), fmaxf(wave_mx[2], wave_mx[3]));
+    // 2^e with e = 14 - floor(log2 mx), limited so that 2^e and 2^(24-e) are normal
+    const int E = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
+    int e = E == 0 ? 127 : (E == 255 ? 0 : 141 - E);
+    e = max(-103, min(127, e));
+    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    if (threadIdx.x == 0) back[row] = __uint_as_float(static_cast<uint32_t>(24 - e + 127) << 23);
+    uint8_t *im = img + row * (K / kBlockWeights) * kImageBlock;
+    uint8_t *sm = sums + row * (K / kBlockWeights) * kSumsBlock;
+    for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
+        const float4 a = *reinterpret_cast<const float4 *>(xr + k), b = *reinterpret_cast<const float4 *>(xr + k + 4);
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        constexpr int order[8] = {0, 2, 1, 3, 4, 6, 5, 7};
+        half8 hi, lo;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = v[order[i]] * up;
+            hi[i] = static_cast<_Float16>(t);
+            lo[i] = static_cast<_Float16>(t - static_cast<float>(hi[i]));
+            s += v[i] * up;
+        }
+        const int blk = k / kBlockWeights, in = k % kBlockWeights;
+        const int quarter = in >> 6, h = (in >> 5) & 1, i = (in >> 3) & 3;
+        uint8_t *o = im + blk * kImageBlock + (2 * i + h) * 128 + quarter * 16;
+        *reinterpret_cast<half8 *>(o) = hi;
+        *reinterpret_cast<half8 *>(o + 64) = lo;
+        // the sub-block's sum over its four threads (32 values below 2^15
+        // each), times 2^-6 to stay in binary16's range
+        s += __shfl_xor(s, 1);
+        s += __shfl_xor(s, 2);
+        s *= 0.015625f;
+        if (i == 0) {
+            const _Float16 sh = static_cast<_Float16>(s);
+            _Float16 *so = reinterpret_cast<_Float16 *>(sm + blk * kSumsBlock) + (in >> 5);
+            so[0] = sh;
+            so[8] = static_cast<_Float16>(s - static_cast<float>(sh));
+        }
+    }
+}
+
+struct Grouped {
+    const uint8_t *w, *w2;  // [E][N][K/256*144]; w2: the up matrices (SwiGLU) or null
+    Staged x;
+    const int *offsets, *rows;
+    float *y;
+    int E, P, N, K, x_div;
+};
+
+struct Tile {
+    int e, first, count;  // rows[first .. first + count) of expert e
+};
+
+// Tile number t of the groups cut into tiles of TM rows (count 0: no such
+// tile).  Every wave scans the offsets by itself, 64 experts at a time.
+template <int TM>
+__device__ __forceinline__ Tile find_tile(const int *offsets, int E, int P, int t, int lane) {
+    int done = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        int b = 0, c = 0;
+        if (e0 + lane < E) {
+            b = min(max(offsets[e0 + lane], 0), P);
+            c = max(min(offsets[e0 + lane + 1], P) - b, 0);
+        }
+        const int tiles = (c + TM - 1) / TM;
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int up = __shfl_up(incl, o);
+            incl += lane >= o ? up : 0;
+        }
+        const uint64_t past = __ballot(done + incl > t);
+        if (past != 0) {
+            const int owner = __builtin_ctzll(past);
+            const int begin = __builtin_amdgcn_readlane(b, owner), all = __builtin_amdgcn_readlane(c, owner);
+            const int at = t - done - (__builtin_amdgcn_readlane(incl, owner) - __builtin_amdgcn_readlane(tiles, owner));
+            return {e0 + owner, begin + at * TM, min(TM, all - at * TM)};
+        }
+        done += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return {0, 0, 0};
+}
+
+// One lane's part of one super-block of its row of W.
+struct WBlock {
+    uint4 head, q0, q1;
+};
+__device__ __forceinline__ WBlock load_block(const uint8_t *row, int b, int quarter) {
+    const uint8_t *p = row + static_cast<size_t>(b) * kBlockBytes;
+    return {*reinterpret_cast<const uint4 *>(p), *reinterpret_cast<const uint4 *>(p + 16 + 32 * quarter),
+            *reinterpret_cast<const uint4 *>(p + 32 + 32 * quarter)};
+}
+
+struct WScales {
+    float d, nm;    // d, -64 * dmin
+    half2v s0, s1;  // the lane's two scales, the second / 16 (its nibbles are 16q)
+    half8 mins;     // m_0..m_7 as subnormals m * 2^-24
+};
+__device__ __forceinline__ WScales block_scales(const uint4 hd, int quarter) {
+    WScales s;
+    s.d = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(hd.x & 0xFFFFu)));
+    s.nm = -64.f * static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(hd.x >> 16)));
+    const uint32_t scA = hd.y & 0x3F3F3F3Fu, mnA = hd.z & 0x3F3F3F3Fu;
+    const uint32_t scB = (hd.w & 0x0F0F0F0Fu) | ((hd.y >> 2) & 0x30303030u);
+    const uint32_t mnB = ((hd.w >> 4) & 0x0F0F0F0Fu) | ((hd.z >> 2) & 0x30303030u);
+    const uint32_t two = (quarter & 2 ? scB : scA) >> (16 * (quarter & 1));
+    const _Float16 a = static_cast<_Float16>(static_cast<float>(two & 0xFFu));
+    const _Float16 b = static_cast<_Float16>(0.0625f * static_cast<float>((two >> 8) & 0xFFu));
+    s.s0 = half2v{a, a};
+    s.s1 = half2v{b, b};
+    uint4 m;
+    m.x = (mnA & 0xFFu) | ((mnA & 0xFF00u) << 8);
+    m.y = ((mnA >> 16) & 0xFFu) | ((mnA >> 8) & 0xFF0000u);
+    m.z = (mnB & 0xFFu) | ((mnB & 0xFF00u) << 8);
+    m.w = ((mnB >> 16) & 0xFFu) | ((mnB >> 8) & 0xFF0000u);
+    s.mins = __builtin_bit_cast(half8, m);
+    return s;
+}
+
+// The operands of steps 2i (low nibbles) and 2i + 1 (high) from two dwords.
+__device__ __forceinline__ half2v scaled(uint32_t bits, half2v s) { return __builtin_bit_cast(half2v, bits) * s; }
+__device__ __forceinline__ half8 join(half2v a, half2v b, half2v c, half2v d) {
+    return half8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+__device__ __forceinline__ void operands(uint32_t u, uint32_t v, const WScales &s, half8 &low, half8 &high) {
+    const uint32_t LM = 0x000F000Fu, HM = 0x00F000F0u;
+    const uint32_t u8 = u >> 8, v8 = v >> 8;
+    low = join(scaled(u & LM, s.s0), scaled(u8 & LM, s.s0), scaled(v & LM, s.s0), scaled(v8 & LM, s.s0));
+    high = join(scaled(u & HM, s.s1), scaled(u8 & HM, s.s1), scaled(v & HM, s.s1), scaled(v8 & HM, s.s1));
+}
+
+__device__ __forceinline__ float4v mfma(half8 a, half8 b, float4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// 16 rows of x times 32 rows of W (SwiGLU: 16 gate and the same 16 up rows)
+// per wave, four waves side by side; operands straight from memory.
+template <bool kSwiglu>
+__global__ __launch_bounds__(256) void grouped_kernel(Grouped g) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, quarter = lane >> 4;
+    const Tile t = find_tile<16>(g.offsets, g.E, g.P, blockIdx.y, lane);
+    if (t.count == 0) return;
+    constexpr int kWaveN = kSwiglu ? 16 : 32;
+    const int n0 = (blockIdx.x * 4 + wave) * kWaveN;
+    if (n0 >= g.N) return;
+    const int KB = g.K / kBlockWeights;
+    const size_t row_bytes = static_cast<size_t>(KB) * kBlockBytes;
+    const uint8_t *wrow[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int n = min(n0 + (kSwiglu ? 0 : 16 * c) + c16, g.N - 1);
+        wrow[c] = (kSwiglu && c ? g.w2 : g.w) + (static_cast<size_t>(t.e) * g.N + n) * row_bytes;
+    }
+    // this lane's row of x as the A operand: row c16 of the tile (the last one again behind the end)
+    const auto pair_at = [&](int i) {
+        const int at = t.first + min(i, t.count - 1);
+        return g.rows ? g.rows[at] : at;
+    };
+    int pair = pair_at(c16);
+    pair = static_cast<unsigned>(pair) < static_cast<unsigned>(g.P) ? pair : 0;
+    const size_t xr = pair / g.x_div;
+    const uint8_t *img = g.x.img + xr * KB * kImageBlock + quarter * 16;
+    const uint8_t *sums = g.x.sums + xr * KB * kSumsBlock + (quarter & 1) * 16;
+    float4v acc[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < KB; ++b) {
+        WBlock wb[2];
+        WScales ws[2];
+        float4v blk[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            wb[c] = load_block(wrow[c], b, quarter);
+            blk[c] = float4v{0.f, 0.f, 0.f, 0.f};
+        }
+        half8 a[16];
+#pragma unroll
+        for (int s = 0; s < 16; ++s) a[s] = *reinterpret_cast<const half8 *>(img + b * kImageBlock + s * 64);
+        const uint4 sm = *reinterpret_cast<const uint4 *>(sums + b * kSumsBlock);
+        const half8 am = __builtin_bit_cast(half8, quarter < 2 ? sm : uint4{0, 0, 0, 0});
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            ws[c] = block_scales(wb[c].head, quarter);
+            const uint32_t q[8] = {wb[c].q0.x, wb[c].q0.y, wb[c].q0.z, wb[c].q0.w,
+                                   wb[c].q1.x, wb[c].q1.y, wb[c].q1.z, wb[c].q1.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                half8 low, high;
+                operands(q[2 * i], q[2 * i + 1], ws[c], low, high);
+                blk[c] = mfma(a[4 * i + 0], low, blk[c]);
+                blk[c] = mfma(a[4 * i + 1], low, blk[c]);
+                blk[c] = mfma(a[4 * i + 2], high, blk[c]);
+                blk[c] = mfma(a[4 * i + 3], high, blk[c]);
+            }
+            const float4v cm = mfma(am, ws[c].mins, float4v{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[c][r] = __builtin_fmaf(ws[c].nm, cm[r], __builtin_fmaf(ws[c].d, blk[c][r], acc[c][r]));
+        }
+    }
+    // lane l holds rows 4 * (l / 16) + r of the tile for column l % 16
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = 4 * quarter + r;
+        const int p = pair_at(i);
+        if (i >= t.count || static_cast<unsigned>(p) >= static_cast<unsigned>(g.P)) continue;
+        const float back = g.x.back[p / g.x_div];
+        float *yr = g.y + static_cast<size_t>(p) * g.N;
+        if (kSwiglu) {
+            if (n0 + c16 < g.N) yr[n0 + c16] = swiglu(acc[0][r] * back, acc[1][r] * back);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                if (n0 + 16 * c + c16 < g.N) yr[n0 + 16 * c + c16] = acc[c][r] * back;
+        }
+    }
+}
+
+// out[m, n] = sum_j weight[m, j] * y[m * top_k + j, n] over the choices with a
+// valid expert, in ascending j.
+__global__ __launch_bounds__(256) void combine_kernel(const float *y, const int *expert, const float *weight,
+                                                      float *out, int E, int top_k, int N) {
+    const int m = blockIdx.y;
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= N) return;
+    float acc = 0.f;
+    for (int j = 0; j < top_k; ++j) {
+        const size_t p = static_cast<size_t>(m) * top_k + j;
+        if (static_cast<unsigned>(expert[p]) >= static_cast<unsigned>(E)) continue;
+        acc = __builtin_fmaf(weight[p], y[p * N + n], acc);
+    }
+    out[static_cast<size_t>(m) * N + n] = acc;
+}
+
+bool misaligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+int status(hipError_t err) {
+    if (err == hipErrorOutOfMemory || err == hipErrorMemoryAllocation) return Q4K_ERR_ALLOC;
+    return err == hipSuccess ? Q4K_OK : Q4K_ERR_LAUNCH;
+}
+
+int check_grouped(const void *w, const void *w2, const float *x, int x_div, const int *offsets, const int *rows,
+                  const float *y, int E, int P, int N, int K) {
+    if (E < 1 || E > Q4K_MAX_EXPERTS || P < 0 || N < 0 || K < 0 || x_div < 1) return Q4K_ERR_BAD_DIM;
+    if (P == 0 || N == 0) return Q4K_OK;
+    if (K == 0 || K % kBlockWeights != 0) return Q4K_ERR_BAD_DIM;
+    if (!w || !w2 || !x || !offsets || !y) return Q4K_ERR_NULL;
+    if (misaligned(w, 16) || misaligned(w2, 16) || misaligned(x, 16) || misaligned(y, 16) || misaligned(offsets, 4) ||
+        misaligned(rows, 4))
+        return Q4K_ERR_ALIGN;
+    return Q4K_OK;
+}
+
+// Stages x, then the products.  g.x is filled in here.
+hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
+    const size_t xrows = (static_cast<size_t>(g.P) + g.x_div - 1) / g.x_div, KB = g.K / kBlockWeights;
+    float *ws = nullptr;
+    hipError_t err = workspace(stream, xrows * (KB * (kImageBlock + kSumsBlock) + 16), &ws);
+    if (err != hipSuccess) return err;
+    uint8_t *img = reinterpret_cast<uint8_t *>(ws), *sums = img + xrows * KB * kImageBlock;
+    float *back = reinterpret_cast<float *>(sums + xrows * KB * kSumsBlock);
+    g.x = {img, sums, back};
+    hipLaunchKernelGGL(stage_rows_kernel, dim3(static_cast<unsigned>(xrows)), dim3(256), 0, stream, x, g.K, img, sums,
+                       back);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const int tiles = g.P / 16 + (g.E < g.P ? g.E : g.P);
+    const int cols = g.w2 ? 64 : 128;
+    const dim3 grid((g.N + cols - 1) / cols, tiles);
+    if (g.w2) hipLaunchKernelGGL(grouped_kernel<true>, grid, dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL(grouped_kernel<false>, grid, dim3(256), 0, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace q4k
+
+extern "C" int q4k_matmul_grouped(const void *w_packed, const float *x, int x_div, const int *offsets,
+                                  const int *rows, float *y, int E, int P, int N, int K, hipStream_t stream) {
+    using namespace q4k;
+    int rc = check_grouped(w_packed, w_packed, x, x_div, offsets, rows, y, E, P, N, K);
+    if (rc != Q4K_OK || P == 0 || N == 0) return rc;
+    rc = check_device();
+    if (rc != Q4K_OK) return rc;
+    return status(run_grouped({static_cast<const uint8_t *>(w_packed), nullptr, {}, offsets, rows, y, E, P, N, K, x_div},
+                              x, stream));
+}
+
+extern "C" int q4k_matmul_grouped_swiglu(const void *w_gate, const void *w_up, const float *x, int x_div,
+                                         const int *offsets, const int *rows, float *out, int E, int P, int N,
+                                         int K, hipStream_t stream) {
+    using namespace q4k;
+    int rc = check_grouped(w_gate, w_up, x, x_div, offsets, rows, out, E, P, N, K);
+    if (rc != Q4K_OK || P == 0 || N == 0) return rc;
+    rc = check_device();
+    if (rc != Q4K_OK) return rc;
+    return status(run_grouped({static_cast<const uint8_t *>(w_gate), static_cast<const uint8_t *>(w_up), {}, offsets,
+                               rows, out, E, P, N, K, x_div},
+                              x, stream));
+}
+
+extern "C" int q4k_matmul_grouped_combine(const void *w_packed, const float *x, const int *expert,
+                                          const float *weight, const int *offsets, const int *rows, float *out,
+                                          int E, int M, int top_k, int N, int K, hipStream_t stream) {
+    using namespace q4k;
+    if (M < 0 || top_k < 1 || static_cast<int64_t>(M) * top_k > INT_MAX) return Q4K_ERR_BAD_DIM;
+    const int P = M * top_k;
+    int rc = check_grouped(w_packed, w_packed, x, 1, offsets, rows, out, E, P, N, K);
+    if (rc != Q4K_OK || P == 0 || N == 0) return rc;
+    if (!rows || !expert || !weight) return Q4K_ERR_NULL;
+    if (misaligned(expert, 4) || misaligned(weight, 4)) return Q4K_ERR_ALIGN;
+    rc = check_device();
+    if (rc != Q4K_OK) return rc;
+    float *y = nullptr;
+    if (workspace(stream, static_cast<size_t>(P) * N * sizeof(float), &y, 1) != hipSuccess) return Q4K_ERR_ALLOC;
+    hipError_t err = run_grouped({static_cast<const uint8_t *>(w_packed), nullptr, {}, offsets, rows, y, E, P, N, K, 1},
+                                 x, stream);
+    if (err != hipSuccess) return status(err);
+    hipLaunchKernelGGL(combine_kernel, dim3((N + 255) / 256, M), dim3(256), 0, stream, y, expert, weight, out, E,
+                       top_k, N);
+    return status(hipGetLastError());
+}

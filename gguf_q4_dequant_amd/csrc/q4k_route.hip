@@ -1,0 +1,420 @@
+// Top-k routing and the grouping of (token, choice) pairs by expert.
+//
+// Routing.  One wave per token; lane l holds the logits of experts l, 64 + l,
+// 128 + l, ... in registers.  The k choices are k rounds of a wave maximum
+// (DPP moves inside the vector unit, no LDS round trip) followed by a ballot
+// that finds the lowest expert holding it: a round costs about a hundred
+// cycles, against the three thousand of comparing every pair of 128 scores.
+//
+// Grouping is a stable counting sort, without atomics whose order could
+// change a result: pairs are taken 64 at a time by a wave, each lane finds
+// the lanes with its own expert by one ballot per bit of the expert number
+// (its rank is the number of them below it), and per-wave counts per expert,
+// summed over waves (and workgroups) in order, give every wave its first
+// place in every group.  Up to kSingleTokens tokens one workgroup of sixteen
+// waves does all of it in one launch; above, the routing workgroups leave
+// their counts in the workspace and a second launch places the pairs.
+#include <math.h>
+
+#include "../../include/q4k_moe.h"
+#include "q4k_internal.h"
+
+namespace q4k {
+namespace {
+
+constexpr int kSingleTokens = 64;   // tokens routed and grouped by one workgroup
+constexpr int kSinglePairs = 8192;  // pairs grouped by one workgroup (q4k_moe_group)
+constexpr int kMaxBlocks = 256;     // workgroups of the two-launch forms
+constexpr int kSingleThreads = 1024;
+constexpr int kThreads = 256;
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v, float identity) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(identity), __float_as_int(v), kCtrl, 0xF, 0xF,
+                                                      false));
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp(double v, double identity) {
+    const int2 a = __builtin_bit_cast(int2, v), i = __builtin_bit_cast(int2, identity);
+    int2 r;
+    r.x = __builtin_amdgcn_update_dpp(i.x, a.x, kCtrl, 0xF, 0xF, false);
+    r.y = __builtin_amdgcn_update_dpp(i.y, a.y, kCtrl, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, r);
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    int2 a = __builtin_bit_cast(int2, v);
+    a.x = __builtin_amdgcn_readlane(a.x, lane);
+    a.y = __builtin_amdgcn_readlane(a.y, lane);
+    return __builtin_bit_cast(double, a);
+}
+
+// op over the 64 lanes, uniform: row shifts by 1, 2, 4 and 8 leave each row
+// of 16 in its last lane, the two row broadcasts join the rows in lane 63.
+template <class T, class Op>
+__device__ __forceinline__ T wave_reduce(T v, T identity, Op op) {
+    v = op(v, dpp<0x111>(v, identity));
+    v = op(v, dpp<0x112>(v, identity));
+    v = op(v, dpp<0x114>(v, identity));
+    v = op(v, dpp<0x118>(v, identity));
+    v = op(v, dpp<0x142>(v, identity));
+    v = op(v, dpp<0x143>(v, identity));
+    return lane_value(v, 63);
+}
+template <class T>
+__device__ __forceinline__ T wave_max(T v) {
+    return wave_reduce(v, static_cast<T>(-INFINITY), [](T a, T b) { return a > b ? a : b; });
+}
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
+    return wave_reduce(v, static_cast<T>(0), [](T a, T b) { return a + b; });
+}
+
+// The softmax's numerator: 1 at the largest logit also where that is +inf.
+__device__ __forceinline__ float softmax_term(float l, float mx) { return l == mx ? 1.f : expf(l - mx); }
+__device__ __forceinline__ double softmax_term(double l, double mx) { return l == mx ? 1.0 : exp(l - mx); }
+
+// Routes one token; lane j < top_k ends with choice j.  T is float where the
+// logits themselves decide (no bias), else double.
+template <int VPL, class T>
+__device__ __forceinline__ void route_token(const float *logits, const float *bias, int E, int top_k, int flags,
+                                            float scale, int lane, int &expert, float &weight) {
+    constexpr bool kBias = sizeof(T) == 8;
+    const bool sigmoid = (flags & Q4K_ROUTE_SIGMOID) != 0;
+    float l[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        const int e = v * 64 + lane;
+        l[v] = e < E ? logits[e] : -INFINITY;
+        if (!(l[v] > -INFINITY)) l[v] = -INFINITY;  // NaN too
+    }
+    float mx = l[0];
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) mx = fmaxf(mx, l[v]);
+    mx = wave_max(mx);
+    T sum = 0;
+    T s[kBias ? VPL : 1], key[VPL];
+    if constexpr (kBias) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const double z = l[v];
+            s[v] = !(l[v] > -INFINITY) ? 0.0 : sigmoid ? 1.0 / (1.0 + exp(-z)) : softmax_term(z, static_cast<double>(mx));
+            sum += s[v];
+        }
+        sum = sigmoid ? 1.0 : wave_sum(sum);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int e = v * 64 + lane;
+            s[v] = s[v] / sum;
+            key[v] = l[v] > -INFINITY ? s[v] + static_cast<double>(bias[e]) : -INFINITY;
+            if (!(key[v] > -INFINITY)) key[v] = -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            key[v] = l[v];
+            if (!sigmoid && !(flags & Q4K_ROUTE_NORMALIZE)) sum += l[v] > -INFINITY ? softmax_term(l[v], mx) : 0.f;
+        }
+        sum = sigmoid ? 1.f : wave_sum(sum);
+    }
+    expert = -1;
+    T mine = 0;  // the choice's score (bias) or logit (no bias)
+    for (int j = 0; j < top_k; ++j) {
+        T best = key[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) best = key[v] > best ? key[v] : best;
+        best = wave_max(best);
+        if (!(best > static_cast<T>(-INFINITY))) break;  // uniform: nothing left to choose
+        bool found = false;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const uint64_t at = __ballot(key[v] == best);
+            if (!found && at != 0) {
+                found = true;
+                const int owner = __builtin_ctzll(at);
+                const T val = kBias ? lane_value(s[kBias ? v : 0], owner) : best;
+                if (lane == j) {
+                    expert = v * 64 + owner;
+                    mine = val;
+                }
+                if (lane == owner) key[v] = -INFINITY;
+            }
+        }
+    }
+    // One value per lane from here: in double, where a sigmoid does not
+    // underflow before -745 and the shares of very low scores stay exact.
+    double w = 0.0;
+    if (expert >= 0) {
+        if constexpr (kBias) w = mine;
+        else w = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(mine))) : static_cast<double>(softmax_term(mine, mx));
+    }
+    if (flags & Q4K_ROUTE_NORMALIZE) {
+        const double total = wave_sum(w);
+        w = total > 0.0 ? w / total : 0.0;
+    } else if constexpr (!kBias) {
+        w = expert >= 0 ? w / static_cast<double>(sum) : 0.0;
+    }
+    weight = expert >= 0 ? scale * static_cast<float>(w) : 0.f;
+}
+
+__device__ __forceinline__ int expert_bits(int E) { return E <= 1 ? 0 : 32 - __builtin_clz(E - 1); }
+
+// The lanes of the wave that hold this lane's expert (0 for a lane without).
+__device__ __forceinline__ uint64_t same_expert(int e, bool valid, int bits) {
+    uint64_t mask = __ballot(valid);
+    for (int b = 0; b < bits; ++b) {
+        const bool bit = (e >> b) & 1;
+        const uint64_t with = __ballot(bit);
+        mask &= bit ? with : ~with;
+    }
+    return valid ? mask : 0;
+}
+
+__device__ __forceinline__ uint64_t lanes_below(int lane) { return (1ull << lane) - 1; }
+
+// hist[wave][e] += pairs of expert e among this wave's share of [0, count).
+template <class F>
+__device__ __forceinline__ void count_pairs(F expert_of, int count, int E, int *hist) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int chunks = (count + 63) / 64, per = (chunks + waves - 1) / waves, bits = expert_bits(E);
+    for (int c = wave * per; c < min(chunks, (wave + 1) * per); ++c) {
+        const int i = c * 64 + lane;
+        const int e = i < count ? expert_of(i) : -1;
+        const bool valid = static_cast<unsigned>(e) < static_cast<unsigned>(E);
+        const uint64_t same = same_expert(e, valid, bits);
+        if (valid && (same & lanes_below(lane)) == 0) atomicAdd(&hist[wave * E + e], __builtin_popcountll(same));
+    }
+}
+
+// Places the workgroup's pairs first + [0, count): hist [waves][E] holds
+// the counts of count_pairs, tot [E + 1] is scratch, both in LDS.  counts
+// [blocks][E] are all workgroups' counts (one workgroup: null, its own).
+template <class F>
+__device__ __forceinline__ void place_pairs(F expert_of, int first, int count, int E, int P, int *hist, int *tot,
+                                            const int *counts, int block, int blocks, int *offsets, int *rows) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int before = 0, all = 0;
+        if (counts) {
+            for (int g = 0; g < blocks; ++g) {
+                const int c = counts[g * E + e];
+                before += g < block ? c : 0;
+                all += c;
+            }
+        }
+        int run = before;
+        for (int w = 0; w < waves; ++w) {
+            const int c = hist[w * E + e];
+            hist[w * E + e] = run;
+            run += c;
+        }
+        tot[e] = counts ? all : run;
+    }
+    __syncthreads();
+    if (wave == 0) {  // exclusive scan of the totals over the experts
+        int carry = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int c = e0 + lane < E ? tot[e0 + lane] : 0;
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int up = __shfl_up(incl, o);
+                incl += lane >= o ? up : 0;
+            }
+            if (e0 + lane < E) tot[e0 + lane] = carry + incl - c;
+            carry += __shfl(incl, 63);
+        }
+        if (lane == 0) tot[E] = carry;
+    }
+    __syncthreads();
+    if (block == 0)
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = tot[e];
+    const int chunks = (count + 63) / 64, per = (chunks + waves - 1) / waves, bits = expert_bits(E);
+    for (int c = wave * per; c < min(chunks, (wave + 1) * per); ++c) {
+        const int i = c * 64 + lane;
+        const int e = i < count ? expert_of(i) : -1;
+        const bool valid = static_cast<unsigned>(e) < static_cast<unsigned>(E);
+        const uint64_t same = same_expert(e, valid, bits);
+        const uint64_t below = same & lanes_below(lane);
+        if (valid) {
+            rows[tot[e] + hist[wave * E + e] + __builtin_popcountll(below)] = first + i;
+            if (below == 0) atomicAdd(&hist[wave * E + e], __builtin_popcountll(same));
+        }
+    }
+    for (int64_t i = static_cast<int64_t>(tot[E]) + block * blockDim.x + threadIdx.x; i < P; i += blocks * blockDim.x)
+        rows[i] = -1;
+}
+
+struct RouteArgs {
+    const float *logits, *bias;
+    int *expert;
+    float *weight;
+    int *offsets, *rows, *counts;  // counts: workspace [blocks][E] (two launches) or null
+    int M, E, top_k, flags, per;   // per: tokens of a workgroup
+    float scale;
+};
+
+// LDS: hist [waves][E], tot [E + 1], and the workgroup's choices [per][top_k].
+template <int VPL, class T>
+__global__ __launch_bounds__(kSingleThreads) void route_kernel(RouteArgs a) {
+    extern __shared__ int lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    int *hist = lds, *tot = hist + waves * a.E, *chosen = tot + a.E + 1;
+    for (int i = threadIdx.x; i < waves * a.E; i += blockDim.x) hist[i] = 0;
+    const int m0 = blockIdx.x * a.per, tokens = min(a.per, a.M - m0);
+    for (int t = wave; t < tokens; t += waves) {
+        const size_t m = m0 + t;
+        int e;
+        float w;
+        route_token<VPL, T>(a.logits + m * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
+        if (lane < a.top_k) {
+            chosen[t * a.top_k + lane] = e;
+            a.expert[m * a.top_k + lane] = e;
+            a.weight[m * a.top_k + lane] = w;
+        }
+    }
+    __syncthreads();
+    const int count = tokens * a.top_k;
+    const auto expert_of = [&](int i) { return chosen[i]; };
+    count_pairs(expert_of, count, a.E, hist);
+    if (a.counts) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+            int c = 0;
+            for (int w = 0; w < waves; ++w) c += hist[w * a.E + e];
+            a.counts[blockIdx.x * a.E + e] = c;
+        }
+        return;
+    }
+    place_pairs(expert_of, 0, count, a.E, count, hist, tot, nullptr, 0, 1, a.offsets, a.rows);
+}
+
+// Counts of each workgroup's share of a table of choices.
+__global__ __launch_bounds__(kThreads) void count_kernel(const int *expert, int P, int E, int per, int *counts) {
+    extern __shared__ int lds[];
+    const int waves = blockDim.x >> 6;
+    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) lds[i] = 0;
+    __syncthreads();
+    const int first = blockIdx.x * per, count = min(per, P - first);
+    count_pairs([&](int i) { return expert[first + i]; }, count, E, lds);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int c = 0;
+        for (int w = 0; w < waves; ++w) c += lds[w * E + e];
+        counts[blockIdx.x * E + e] = c;
+    }
+}
+
+// Places each workgroup's share; counts as left by the launch before, or null
+// for a single workgroup.
+__global__ __launch_bounds__(kSingleThreads) void place_kernel(const int *expert, int P, int E, int per,
+                                                               const int *counts, int *offsets, int *rows) {
+    extern __shared__ int lds[];
+    const int waves = blockDim.x >> 6;
+    int *hist = lds, *tot = hist + waves * E;
+    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    const int first = blockIdx.x * per, count = min(per, P - first);
+    const auto expert_of = [&](int i) { return expert[first + i]; };
+    count_pairs(expert_of, count, E, hist);
+    place_pairs(expert_of, first, count, E, P, hist, tot, counts, blockIdx.x, gridDim.x, offsets, rows);
+}
+
+template <int VPL, class T>
+hipError_t launch_route(const RouteArgs &a, int blocks, int threads, hipStream_t stream) {
+    const int bytes = ((threads / 64) * a.E + a.E + 1 + a.per * a.top_k) * 4;
+    hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_kernel<VPL, T>), 128 << 10);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((route_kernel<VPL, T>), dim3(blocks), dim3(threads), bytes, stream, a);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_route_for(const RouteArgs &a, int blocks, int threads, hipStream_t stream) {
+    if (a.E <= 64) return launch_route<1, T>(a, blocks, threads, stream);
+    if (a.E <= 128) return launch_route<2, T>(a, blocks, threads, stream);
+    if (a.E <= 256) return launch_route<4, T>(a, blocks, threads, stream);
+    if (a.E <= 512) return launch_route<8, T>(a, blocks, threads, stream);
+    return launch_route<16, T>(a, blocks, threads, stream);
+}
+
+hipError_t launch_place(const int *expert, int P, int E, int per, int blocks, int threads, const int *counts,
+                        int *offsets, int *rows, hipStream_t stream) {
+    const int bytes = ((threads / 64) * E + E + 1) * 4;
+    hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(place_kernel), 128 << 10);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(threads), bytes, stream, expert, P, E, per, counts, offsets,
+                       rows);
+    return hipGetLastError();
+}
+
+bool misaligned4(const void *a, const void *b = nullptr, const void *c = nullptr, const void *d = nullptr,
+                 const void *e = nullptr, const void *f = nullptr) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
+             reinterpret_cast<uintptr_t>(d) | reinterpret_cast<uintptr_t>(e) | reinterpret_cast<uintptr_t>(f)) & 3u) != 0;
+}
+
+int status(hipError_t err) {
+    if (err == hipErrorOutOfMemory || err == hipErrorMemoryAllocation) return Q4K_ERR_ALLOC;
+    return err == hipSuccess ? Q4K_OK : Q4K_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace q4k
+
+extern "C" int q4k_moe_route(const float *logits, const float *bias, int M, int E, int top_k, int flags,
+                             float scale, int *expert, float *weight, int *offsets, int *rows, hipStream_t stream) {
+    using namespace q4k;
+    if (M < 0 || E < 1 || E > Q4K_MAX_EXPERTS || top_k < 1 || top_k > E || top_k > Q4K_MAX_TOP_K ||
+        static_cast<int64_t>(M) * top_k > INT_MAX || (flags & ~(Q4K_ROUTE_SIGMOID | Q4K_ROUTE_NORMALIZE)) != 0)
+        return Q4K_ERR_BAD_DIM;
+    if (!offsets || (M > 0 && (!logits || !expert || !weight || !rows))) return Q4K_ERR_NULL;
+    if (misaligned4(logits, bias, expert, weight, offsets, rows)) return Q4K_ERR_ALIGN;
+    const int dev_rc = check_device();
+    if (dev_rc != Q4K_OK) return dev_rc;
+    if (M == 0) return status(launch_place(nullptr, 0, E, 0, 1, kThreads, nullptr, offsets, rows, stream));
+    RouteArgs a = {logits, bias, expert, weight, offsets, rows, nullptr, M, E, top_k, flags, M, scale};
+    int blocks = 1, threads = kSingleThreads;
+    if (M > kSingleTokens) {
+        // one wave per token in flight, at most kMaxBlocks workgroups of four
+        a.per = (M - 1) / kMaxBlocks + 1;
+        a.per = a.per < 4 ? 4 : a.per;
+        // the choices share the LDS with the counts
+        if (static_cast<int64_t>(a.per) * top_k * 4 > (64 << 10)) a.per = (64 << 10) / (4 * top_k);
+        blocks = (M - 1) / a.per + 1;
+        threads = kThreads;
+        float *ws = nullptr;
+        if (workspace(stream, static_cast<size_t>(blocks) * E * 4, &ws) != hipSuccess) return Q4K_ERR_ALLOC;
+        a.counts = reinterpret_cast<int *>(ws);
+    }
+    hipError_t err = bias ? launch_route_for<double>(a, blocks, threads, stream)
+                          : launch_route_for<float>(a, blocks, threads, stream);
+    if (err == hipSuccess && a.counts)
+        err = launch_place(expert, M * top_k, E, a.per * top_k, blocks, kThreads, a.counts, offsets, rows, stream);
+    return status(err);
+}
+
+extern "C" int q4k_moe_group(const int *expert, int P, int E, int *offsets, int *rows, hipStream_t stream) {
+    using namespace q4k;
+    if (P < 0 || E < 1 || E > Q4K_MAX_EXPERTS) return Q4K_ERR_BAD_DIM;
+    if (!offsets || (P > 0 && (!expert || !rows))) return Q4K_ERR_NULL;
+    if (misaligned4(expert, offsets, rows)) return Q4K_ERR_ALIGN;
+    const int dev_rc = check_device();
+    if (dev_rc != Q4K_OK) return dev_rc;
+    if (P <= kSinglePairs)
+        return status(launch_place(expert, P, E, P, 1, kSingleThreads, nullptr, offsets, rows, stream));
+    const int per = (((P - 1) / kMaxBlocks + 1) + 255) & ~255;
+    const int blocks = (P - 1) / per + 1;
+    float *ws = nullptr;
+    if (workspace(stream, static_cast<size_t>(blocks) * E * 4, &ws) != hipSuccess) return Q4K_ERR_ALLOC;
+    int *counts = reinterpret_cast<int *>(ws);
+    hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(kThreads), (kThreads / 64) * E * 4, stream, expert, P, E, per,
+                       counts);
+    hipError_t err = hipGetLastError();
+    if (err == hipSuccess) err = launch_place(expert, P, E, per, blocks, kThreads, counts, offsets, rows, stream);
+    return status(err);
+}
