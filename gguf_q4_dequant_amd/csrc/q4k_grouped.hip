@@ -199,6 +199,13 @@ __device__ __forceinline__ void operands(uint32_t u, uint32_t v, const WScales &
     high = join(scaled(u & HM, s.s1), scaled(u8 & HM, s.s1), scaled(v & HM, s.s1), scaled(v8 & HM, s.s1));
 }
 
+// The operand of one of the two steps.
+__device__ __forceinline__ void operand(uint32_t u, uint32_t v, const WScales &s, int h, half8 &op) {
+    const uint32_t mask = h ? 0x00F000F0u : 0x000F000Fu;
+    const half2v sc = h ? s.s1 : s.s0;
+    op = join(scaled(u & mask, sc), scaled((u >> 8) & mask, sc), scaled(v & mask, sc), scaled((v >> 8) & mask, sc));
+}
+
 __device__ __forceinline__ float4v mfma(half8 a, half8 b, float4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -286,6 +293,233 @@ __global__ __launch_bounds__(256) void grouped_kernel(Grouped g) {
     }
 }
 
+// ---- many rows per expert: tiles of RT * 16 rows times 256 columns ----------
+
+// LDS of a workgroup: two buffers of x (a quarter of a super-block: two steps,
+// 256 bytes a row), two of its sub-block sums, one super-block of each wave's
+// own 64 rows of W, and the tile's pair numbers.
+template <int RT>
+struct TileLds {
+    static constexpr int kRows = RT * 16;
+    static constexpr int kX = kRows * 256, kSums = kRows * kSumsBlock, kW = 64 * kBlockBytes;
+    static constexpr int kSumsAt = 2 * kX, kWAt = kSumsAt + 2 * kSums, kPairsAt = kWAt + 4 * kW;
+    static constexpr int kBytes = kPairsAt + kRows * 4;
+};
+
+typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// LDS byte address of a uniform pointer.
+__device__ __forceinline__ uint32_t lds_address(uint8_t *p) {
+    return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8 *)p)));
+}
+
+// 16 bytes per lane from memory to LDS at dst + 16 * lane.  Written in
+// assembly because the compiler waits for every such copy before the next LDS
+// read, whichever buffer that reads; no register is written, and the kernel
+// waits for vmcnt and the barrier before it reads a buffer.
+__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+}
+// The same from a buffer (offsets behind its end read zeros).
+__device__ __forceinline__ void copy_to_lds(rsrc_t buffer, uint32_t offset, uint32_t base, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(offset), "s"(buffer),
+                 "s"(base), "s"(dst)
+                 : "memory");
+}
+// A raw buffer of bytes at p (both uniform).
+__device__ __forceinline__ rsrc_t buffer_at(const uint8_t *p, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    rsrc_t r;
+    r.x = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    r.y = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32) & 0xFFFFu);
+    r.z = __builtin_amdgcn_readfirstlane(bytes);
+    r.w = 0x00020000u;
+    return r;
+}
+
+// At most VM vector-memory operations of this wave outstanding and no LDS
+// operation, then the workgroup's barrier.
+template <int VM>
+__device__ __forceinline__ void wait_and_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (VM & 15));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int RT, bool kSwiglu>
+__global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
+    using L = TileLds<RT>;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c16 = lane & 15, quarter = lane >> 4;
+    const Tile t = find_tile<L::kRows>(g.offsets, g.E, g.P, blockIdx.y, lane);
+    if (t.count == 0) return;
+    int *pairs = reinterpret_cast<int *>(lds + L::kPairsAt);
+    if (threadIdx.x < L::kRows) {
+        const int at = t.first + min(static_cast<int>(threadIdx.x), t.count - 1);
+        const int p = g.rows ? g.rows[at] : at;
+        pairs[threadIdx.x] = static_cast<unsigned>(p) < static_cast<unsigned>(g.P) ? p : -1;
+    }
+    __syncthreads();
+    const int KB = g.K / kBlockWeights;
+    const size_t row_bytes = static_cast<size_t>(KB) * kBlockBytes;
+    constexpr int kWaveN = kSwiglu ? 32 : 64;
+    const int n0 = (blockIdx.x * 4 + wave) * kWaveN;
+
+    // x: this wave copies rows 4 RT wave .. + 4 RT of the tile, four per
+    // instruction; a row's 16-byte pieces are exchanged by its number (piece c
+    // in slot c ^ (row % 16)), so that a column of pieces reads 16 banks apart.
+    const uint8_t *xsrc[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+        const int row = wave * RT * 4 + j * 4 + quarter;
+        const size_t xr = max(pairs[row], 0) / g.x_div;
+        xsrc[j] = g.x.img + xr * KB * kImageBlock + ((c16 ^ (row & 15)) * 16);
+    }
+    const uint8_t *ssrc = g.x.sums;
+    if (lane < RT * 8) {
+        const size_t xr = max(pairs[wave * RT * 4 + (lane >> 1)], 0) / g.x_div;
+        ssrc += xr * KB * kSumsBlock + (lane & 1) * 16;
+    }
+    // W: two halves of 32 rows, 288 pieces of 16 bytes each (4.5 instructions);
+    // row 16c + r of the wave's 64 is column r of its tile c (SwiGLU: the
+    // halves are gate and up).  Rows behind N read zeros.
+    uint32_t woff[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        const int piece = k * 64 + lane, j = piece / 9, part = piece - 9 * j;
+        woff[k] = j * static_cast<uint32_t>(row_bytes) + part * 16;
+    }
+    rsrc_t wbuf[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int first = min(n0 + (kSwiglu ? 0 : 32 * h), g.N), rows = min(32, g.N - first);
+        wbuf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(t.e) * g.N + first) * row_bytes,
+                            rows * static_cast<uint32_t>(row_bytes));
+    }
+    uint8_t *const wlds = lds + L::kWAt + wave * L::kW;
+    const uint32_t lds0 = lds_address(lds), wlds0 = lds0 + L::kWAt + wave * L::kW;
+    const auto copy_x = [&](int b, int i, int buf) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+            copy_to_lds(xsrc[j] + (static_cast<size_t>(b) * kImageBlock + i * 256), lds0 + buf * L::kX + (wave * RT + j) * 1024);
+    };
+    const auto copy_sums = [&](int b) {
+        if (lane < RT * 8)
+            copy_to_lds(ssrc + static_cast<size_t>(b) * kSumsBlock, lds0 + L::kSumsAt + (b & 1) * L::kSums + wave * RT * 128);
+    };
+    const auto copy_w = [&](int b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+                if (k < 4 || lane < 32)
+                    copy_to_lds(wbuf[h], woff[k], b * kBlockBytes, wlds0 + h * (L::kW / 2) + k * 1024);
+    };
+    float4v acc[RT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
+    copy_w(0);
+    copy_x(0, 0, 0);
+    copy_sums(0);
+    for (int b = 0; b < KB; ++b) {
+        WScales ws[4];
+        float4v blk[RT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // x of this quarter has arrived; the others' too behind the barrier
+            wait_and_barrier<0>();
+            if (i < 3) copy_x(b, i + 1, (i + 1) & 1);
+            else if (b + 1 < KB) {
+                copy_x(b + 1, 0, 0);
+                copy_sums(b + 1);
+            }
+            if (i == 0) {
+                half8 am[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const uint4 s = *reinterpret_cast<const uint4 *>(lds + L::kSumsAt + (b & 1) * L::kSums +
+                                                                     (r * 16 + c16) * kSumsBlock + (quarter & 1) * 16);
+                    am[r] = __builtin_bit_cast(half8, quarter < 2 ? s : uint4{0, 0, 0, 0});
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    ws[c] = block_scales(*reinterpret_cast<const uint4 *>(wlds + (c * 16 + c16) * kBlockBytes), quarter);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const float4v cm = mfma(am[r], ws[c].mins, float4v{0.f, 0.f, 0.f, 0.f});
+                        blk[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[r][c][k] = __builtin_fmaf(ws[c].nm, cm[k], acc[r][c][k]);
+                    }
+                }
+            }
+            uint2 q[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                q[c] = *reinterpret_cast<const uint2 *>(wlds + (c * 16 + c16) * kBlockBytes + 16 + 32 * quarter + 8 * i);
+            if (i == 3 && b + 1 < KB) {
+                // every read of this wave's W slot has returned: refill it
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_waitcnt(0xC07F);
+                copy_w(b + 1);
+            }
+            const uint8_t *xb = lds + (i & 1) * L::kX;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __builtin_amdgcn_sched_barrier(0);  // one step's operands in registers at a time
+                half8 a[RT][2];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        a[r][part] = *reinterpret_cast<const half8 *>(
+                            xb + (r * 16 + c16) * 256 + (((h * 2 + part) * 4 + quarter) ^ c16) * 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    half8 op;
+                    operand(q[c].x, q[c].y, ws[c], h, op);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) blk[r][c] = mfma(a[r][0], op, blk[r][c]);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) blk[r][c] = mfma(a[r][1], op, blk[r][c]);
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[r][c][k] = __builtin_fmaf(ws[c].d, blk[r][c][k], acc[r][c][k]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = r * 16 + 4 * quarter + k;
+            const int p = pairs[i];
+            if (i >= t.count || p < 0) continue;
+            const float back = g.x.back[p / g.x_div];
+            float *yr = g.y + static_cast<size_t>(p) * g.N;
+            if (kSwiglu) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (n0 + 16 * c + c16 < g.N)
+                        yr[n0 + 16 * c + c16] = swiglu(acc[r][c][k] * back, acc[r][2 + c][k] * back);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n0 + 16 * c + c16 < g.N) yr[n0 + 16 * c + c16] = acc[r][c][k] * back;
+            }
+        }
+}
+
 // out[m, n] = sum_j weight[m, j] * y[m * top_k + j, n] over the choices with a
 // valid expert, in ascending j.
 __global__ __launch_bounds__(256) void combine_kernel(const float *y, const int *expert, const float *weight,
@@ -334,6 +568,16 @@ hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
                        back);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
+    if (g.P >= 24 * g.E) {
+        const int tiles = g.P / 48 + (g.E < g.P ? g.E : g.P);
+        const dim3 grid((g.N + (g.w2 ? 127 : 255)) / (g.w2 ? 128 : 256), tiles);
+        const void *k = g.w2 ? reinterpret_cast<const void *>(tile_kernel<3, true>) : reinterpret_cast<const void *>(tile_kernel<3, false>);
+        err = allow_dynamic_lds(k, TileLds<3>::kBytes);
+        if (err != hipSuccess) return err;
+        if (g.w2) hipLaunchKernelGGL((tile_kernel<3, true>), grid, dim3(256), TileLds<3>::kBytes, stream, g);
+        else hipLaunchKernelGGL((tile_kernel<3, false>), grid, dim3(256), TileLds<3>::kBytes, stream, g);
+        return hipGetLastError();
+    }
     const int tiles = g.P / 16 + (g.E < g.P ? g.E : g.P);
     const int cols = g.w2 ? 64 : 128;
     const dim3 grid((g.N + cols - 1) / cols, tiles);
