@@ -259,16 +259,26 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
 
 
 def _checked_tensor(name, t, dtype, shape, like):
-    """t is a contiguous tensor of this dtype and shape on like's device."""
+    """t is a contiguous tensor of this dtype and shape on like's device; its address."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == like.device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be shaped {list(shape)}, not {list(t.shape)}")
     if not t.is_cuda or t.device != like.device:
         raise ValueError(f"{name} must be a device tensor on {like.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_for(x, stream) -> int:
+    """The handle of the given stream, or of the current one; x has to be on the
+    current device, whose context the library launches in."""
+    import torch
+    current = torch._C._cuda_getDevice()
+    if x.device.index != current:
+        raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{current}")
+    return torch._C._cuda_getCurrentRawStream(current) if stream is None else _stream_handle(stream)
 
 
 class Adjustment:
@@ -300,26 +310,29 @@ class Adjustment:
     def _checked(self, like, M, N):
         """The C struct for logits [M, N] on like's device."""
         import torch
-        c = _Adjustment()
+        history = repetition = frequency = presence = bias_id = bias_value = mask = None
+        L = B = 0
         if self.history is not None:
             if self.history.dim() != 2:
                 raise ValueError("history must be int32 [M, L]")
-            c.history_len = self.history.shape[1]
-            c.history = _checked_tensor("history", self.history, torch.int32, (M, c.history_len), like)
-            for name in ("repetition", "frequency", "presence"):
-                t = getattr(self, name)
-                if t is not None:
-                    setattr(c, name, _checked_tensor(name, t, torch.float32, (M,), like))
+            L = self.history.shape[1]
+            history = _checked_tensor("history", self.history, torch.int32, (M, L), like)
+            if self.repetition is not None:
+                repetition = _checked_tensor("repetition", self.repetition, torch.float32, (M,), like)
+            if self.frequency is not None:
+                frequency = _checked_tensor("frequency", self.frequency, torch.float32, (M,), like)
+            if self.presence is not None:
+                presence = _checked_tensor("presence", self.presence, torch.float32, (M,), like)
         if self.bias_id is not None:
             if self.bias_id.dim() != 2:
                 raise ValueError("bias_id must be int32 [M, B]")
-            c.bias_len = self.bias_id.shape[1]
-            c.bias_id = _checked_tensor("bias_id", self.bias_id, torch.int32, (M, c.bias_len), like)
-            c.bias_value = _checked_tensor("bias_value", self.bias_value, torch.float32, (M, c.bias_len), like)
+            B = self.bias_id.shape[1]
+            bias_id = _checked_tensor("bias_id", self.bias_id, torch.int32, (M, B), like)
+            bias_value = _checked_tensor("bias_value", self.bias_value, torch.float32, (M, B), like)
         if self.mask is not None:
             dtype = torch.uint32 if self.mask.dtype == torch.uint32 else torch.int32
-            c.mask = _checked_tensor("mask", self.mask, dtype, (M, (N + 31) // 32), like)
-        return c
+            mask = _checked_tensor("mask", self.mask, dtype, (M, (N + 31) // 32), like)
+        return _Adjustment(history, repetition, frequency, presence, bias_id, bias_value, mask, L, B)
 
 
 def _checked_logits(logits):
@@ -341,7 +354,7 @@ def logits_adjust(logits, adjustment, out=None, stream=None):
     elif out is not logits:
         _checked_tensor("out", out, torch.float32, (M, N), logits)
     rc = library().q4k_logits_adjust(logits.data_ptr(), out.data_ptr(), adjustment._checked(logits, M, N), M, N,
-                                     _stream_handle(stream))
+                                     _stream_for(logits, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_logits_adjust")
     return out
@@ -354,13 +367,14 @@ def logits_argmax(logits, adjustment, index=None, value=None, stream=None):
     not written."""
     import torch
     M, N = _checked_logits(logits)
-    if index is None:
-        index = torch.empty(M, dtype=torch.int32, device=logits.device)
-    if value is None:
-        value = torch.empty(M, dtype=torch.float32, device=logits.device)
-    _check_outputs(logits, index, value, M)
+    if index is None and value is None:
+        index, value = logits.new_empty(M, dtype=torch.int32), logits.new_empty(M)
+    else:
+        index = logits.new_empty(M, dtype=torch.int32) if index is None else index
+        value = logits.new_empty(M) if value is None else value
+        _check_outputs(logits, index, value, M)
     rc = library().q4k_logits_argmax(logits.data_ptr(), adjustment._checked(logits, M, N), M, N, index.data_ptr(),
-                                     value.data_ptr(), _stream_handle(stream))
+                                     value.data_ptr(), _stream_for(logits, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_logits_argmax")
     return index, value
@@ -395,11 +409,9 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, normalize: b
         raise Q4KError(ERR_BAD_DIM, f"E={E} top_k={k}")
     bias_ptr = None if bias is None else _checked_tensor("bias", bias, torch.float32, (E,), logits)
     if out is None:
-        dev = logits.device
-        out = Routing(torch.empty((M, k), dtype=torch.int32, device=dev),
-                      torch.empty((M, k), dtype=torch.float32, device=dev),
-                      torch.empty(E + 1, dtype=torch.int32, device=dev),
-                      torch.empty(M * k, dtype=torch.int32, device=dev))
+        new = logits.new_empty
+        out = Routing(new((M, k), dtype=torch.int32), new((M, k)), new(E + 1, dtype=torch.int32),
+                      new(M * k, dtype=torch.int32))
     else:
         _checked_tensor("expert", out.expert, torch.int32, (M, k), logits)
         _checked_tensor("weight", out.weight, torch.float32, (M, k), logits)
@@ -408,7 +420,7 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, normalize: b
     flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_NORMALIZE if normalize else 0)
     rc = library().q4k_moe_route(logits.data_ptr(), bias_ptr, M, E, k, flags, float(scale), out.expert.data_ptr(),
                                  out.weight.data_ptr(), out.offsets.data_ptr(), out.rows.data_ptr(),
-                                 _stream_handle(stream))
+                                 _stream_for(logits, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_moe_route")
     return out
@@ -427,7 +439,7 @@ def moe_group(expert, E: int, stream=None):
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
     offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
     rows = torch.empty(P, dtype=torch.int32, device=expert.device)
-    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(), _stream_handle(stream))
+    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(), _stream_for(expert, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_moe_group")
     return offsets, rows
@@ -468,11 +480,11 @@ def matmul_grouped(w, x, offsets, rows=None, y=None, x_div: int = 1, stream=None
     import torch
     P, E, N, K, rows_ptr = _grouped_checked((w,), x, offsets, rows, x_div)
     if y is None:
-        y = torch.empty((P, N), dtype=torch.float32, device=x.device)
+        y = x.new_empty((P, N))
     else:
         _checked_tensor("y", y, torch.float32, (P, N), x)
     rc = library().q4k_matmul_grouped(w.data_ptr(), x.data_ptr(), x_div, offsets.data_ptr(), rows_ptr, y.data_ptr(),
-                                      E, P, N, K, _stream_handle(stream))
+                                      E, P, N, K, _stream_for(x, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped")
     return y
@@ -484,12 +496,12 @@ def matmul_grouped_swiglu(w_gate, w_up, x, offsets, rows=None, out=None, x_div: 
     import torch
     P, E, N, K, rows_ptr = _grouped_checked((w_gate, w_up), x, offsets, rows, x_div)
     if out is None:
-        out = torch.empty((P, N), dtype=torch.float32, device=x.device)
+        out = x.new_empty((P, N))
     else:
         _checked_tensor("out", out, torch.float32, (P, N), x)
     rc = library().q4k_matmul_grouped_swiglu(w_gate.data_ptr(), w_up.data_ptr(), x.data_ptr(), x_div,
                                              offsets.data_ptr(), rows_ptr, out.data_ptr(), E, P, N, K,
-                                             _stream_handle(stream))
+                                             _stream_for(x, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_swiglu")
     return out
@@ -507,12 +519,12 @@ def matmul_grouped_combine(w, x, routing: Routing, out=None, stream=None):
     _checked_tensor("expert", routing.expert, torch.int32, (M, top_k), x)
     _checked_tensor("weight", routing.weight, torch.float32, (M, top_k), x)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        out = x.new_empty((M, N))
     else:
         _checked_tensor("out", out, torch.float32, (M, N), x)
     rc = library().q4k_matmul_grouped_combine(w.data_ptr(), x.data_ptr(), routing.expert.data_ptr(),
                                               routing.weight.data_ptr(), routing.offsets.data_ptr(), rows_ptr,
-                                              out.data_ptr(), E, M, top_k, N, K, _stream_handle(stream))
+                                              out.data_ptr(), E, M, top_k, N, K, _stream_for(x, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_combine")
     return out

@@ -51,6 +51,16 @@ struct Staged {
     const float *back;    // [rows]: 2^(24 - e)
 };
 
+// The e of the scale 2^e that puts a largest magnitude mx in [2^14, 2^15),
+// limited so that 2^e and 2^(24 - e) are normal (zeros and subnormals: 127,
+// infinity and NaN: 0).
+__device__ __forceinline__ int scale_exponent(float mx) {
+    const int E = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
+    const int e = E == 0 ? 127 : (E == 255 ? 0 : 141 - E);
+    return max(-103, min(127, e));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // Stages one row of x per workgroup (see above): thread u takes eight
 // consecutive values at a time.
 __global__ __launch_bounds__(256) void stage_rows_kernel(const float *x, int K, uint8_t *img, uint8_t *sums,
@@ -69,12 +79,9 @@ __global__ __launch_bounds__(256) void stage_rows_kernel(const float *x, int K, 
     if ((threadIdx.x & 63) == 0) wave_mx[threadIdx.x >> 6] = mx;
     __syncthreads();
     mx = fmaxf(fmaxf(wave_mx[0], wave_mx[1]), fmaxf(wave_mx[2], wave_mx[3]));
-    // 2^e with e = 14 - floor(log2 mx), limited so that 2^e and 2^(24-e) are normal
-    const int E = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
-    int e = E == 0 ? 127 : (E == 255 ? 0 : 141 - E);
-    e = max(-103, min(127, e));
-    const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-    if (threadIdx.x == 0) back[row] = __uint_as_float(static_cast<uint32_t>(24 - e + 127) << 23);
+    const int e = scale_exponent(mx);
+    const float up = power_of_two(e);
+    if (threadIdx.x == 0) back[row] = power_of_two(24 - e);
     uint8_t *im = img + row * (K / kBlockWeights) * kImageBlock;
     uint8_t *sm = sums + row * (K / kBlockWeights) * kSumsBlock;
     for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
@@ -520,6 +527,189 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
         }
 }
 
+// ---- few rows per expert -----------------------------------------------------
+
+// Four rows of x times 32 rows of W (SwiGLU: 16 gate and the same 16 up rows)
+// per workgroup; the waves split K by super-blocks, each with its own LDS:
+// one super-block of the 32 rows of W, the staged x and its factors.
+constexpr int kFewRows = 4;
+struct FewLds {
+    static constexpr int kW = 32 * kBlockBytes, kX = kFewRows * kImageBlock, kSums = kFewRows * kSumsBlock;
+    static constexpr int kXAt = kW, kSumsAt = kXAt + kX, kBackAt = kSumsAt + kSums, kWave = kBackAt + 16;
+};
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp_move(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, false));
+}
+
+// Stages one super-block of four rows for the wave: lane 16r + p holds values
+// 16p .. 16p + 15 of row r.  The scale is per row and super-block here, so
+// that a wave needs nothing from the others.
+__device__ __forceinline__ void stage_few(const float4 v[4], int lane, uint8_t *base) {
+    const int r = lane >> 4, p = lane & 15;
+    const float x[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
+                         v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(x[i]));
+    mx = fmaxf(mx, dpp_move<0x121>(mx));  // rotations by 1, 2, 4, 8 within the row of 16 lanes
+    mx = fmaxf(mx, dpp_move<0x122>(mx));
+    mx = fmaxf(mx, dpp_move<0x124>(mx));
+    mx = fmaxf(mx, dpp_move<0x128>(mx));
+    const int e = scale_exponent(mx);
+    const float up = power_of_two(e);
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        constexpr int order[8] = {0, 2, 1, 3, 4, 6, 5, 7};
+        half8 hi, lo;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = x[8 * u + order[i]] * up;
+            hi[i] = static_cast<_Float16>(t);
+            lo[i] = static_cast<_Float16>(t - static_cast<float>(hi[i]));
+            s += t;
+        }
+        // k = 16p + 8u: quarter p / 4, half (p / 2) % 2, step pair 2 (p % 2) + u
+        const int quarter = p >> 2, h = (p >> 1) & 1, i = 2 * (p & 1) + u;
+        uint8_t *o = base + FewLds::kXAt + r * kImageBlock + (2 * i + h) * 128 + quarter * 16;
+        *reinterpret_cast<half8 *>(o) = hi;
+        *reinterpret_cast<half8 *>(o + 64) = lo;
+    }
+    s += dpp_move<0xB1>(s);  // the other half of the sub-block (lanes exchanged in pairs)
+    s *= 0.015625f;
+    if ((p & 1) == 0) {
+        const _Float16 sh = static_cast<_Float16>(s);
+        _Float16 *so = reinterpret_cast<_Float16 *>(base + FewLds::kSumsAt + r * kSumsBlock) + (p >> 1);
+        so[0] = sh;
+        so[8] = static_cast<_Float16>(s - static_cast<float>(sh));
+    }
+    if (p == 0) reinterpret_cast<float *>(base + FewLds::kBackAt)[r] = power_of_two(24 - e);
+}
+
+template <int WAVES, bool kSwiglu>
+__global__ __launch_bounds__(64 * WAVES) void few_kernel(Grouped g, const float *x) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c16 = lane & 15, quarter = lane >> 4;
+    const Tile t = find_tile<kFewRows>(g.offsets, g.E, g.P, blockIdx.y, lane);
+    if (t.count == 0) return;
+    const auto pair_at = [&](int i) {
+        const int at = t.first + min(i, t.count - 1);
+        return g.rows ? g.rows[at] : at;
+    };
+    const int KB = g.K / kBlockWeights;
+    const size_t row_bytes = static_cast<size_t>(KB) * kBlockBytes;
+    constexpr int kTileN = kSwiglu ? 16 : 32;
+    const int n0 = blockIdx.x * kTileN;
+    uint8_t *const base = lds + wave * FewLds::kWave;
+    const uint32_t wlds = lds_address(base);
+    // two halves of 16 rows (SwiGLU: gate and up), 144 pieces of 16 bytes each
+    uint32_t woff[3];
+    rsrc_t wbuf[2];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int piece = k * 64 + lane, j = piece / 9, part = piece - 9 * j;
+        woff[k] = j * static_cast<uint32_t>(row_bytes) + part * 16;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int first = min(n0 + (kSwiglu ? 0 : 16 * h), g.N), rows = min(16, g.N - first);
+        wbuf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(t.e) * g.N + first) * row_bytes,
+                            rows * static_cast<uint32_t>(row_bytes));
+    }
+    const auto copy_w = [&](int b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < 2 || lane < 16)
+                    copy_to_lds(wbuf[h], woff[k], b * kBlockBytes, wlds + h * (FewLds::kW / 2) + k * 1024);
+    };
+    if (wave < KB) copy_w(wave);
+    // lane 16r + p reads values 16p .. of row r (the last row again behind the end)
+    int pair = pair_at(quarter);
+    pair = static_cast<unsigned>(pair) < static_cast<unsigned>(g.P) ? pair : 0;
+    const float *xr = x + static_cast<size_t>(pair / g.x_div) * g.K + c16 * 16;
+    float4 xv[4];
+    const auto load_x = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4 *>(xr + static_cast<size_t>(b) * kBlockWeights + i * 4);
+    };
+    if (wave < KB) load_x(wave);
+    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const int arow = min(c16, kFewRows - 1);
+    for (int b = wave; b < KB; b += WAVES) {
+        stage_few(xv, lane, base);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);  // W has arrived, x is staged (both this wave's own)
+        asm volatile("" ::: "memory");
+        WBlock wb[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) wb[c] = load_block(base + (c * 16 + c16) * kBlockBytes, 0, quarter);
+        half8 a[16];
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+            a[s] = *reinterpret_cast<const half8 *>(base + FewLds::kXAt + arow * kImageBlock + s * 64 + quarter * 16);
+        const uint4 sm = *reinterpret_cast<const uint4 *>(base + FewLds::kSumsAt + arow * kSumsBlock + (quarter & 1) * 16);
+        const half8 am = __builtin_bit_cast(half8, quarter < 2 ? sm : uint4{0, 0, 0, 0});
+        const float4 back = *reinterpret_cast<const float4 *>(base + FewLds::kBackAt);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // everything read: the slots may be filled again
+        if (b + WAVES < KB) {
+            copy_w(b + WAVES);
+            load_x(b + WAVES);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const WScales ws = block_scales(wb[c].head, quarter);
+            const uint32_t q[8] = {wb[c].q0.x, wb[c].q0.y, wb[c].q0.z, wb[c].q0.w,
+                                   wb[c].q1.x, wb[c].q1.y, wb[c].q1.z, wb[c].q1.w};
+            float4v b0 = {0.f, 0.f, 0.f, 0.f}, b1 = b0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                half8 low, high;
+                operand(q[2 * i], q[2 * i + 1], ws, 0, low);
+                operand(q[2 * i], q[2 * i + 1], ws, 1, high);
+                b0 = mfma(a[4 * i + 0], low, b0);
+                b1 = mfma(a[4 * i + 2], high, b1);
+                b0 = mfma(a[4 * i + 1], low, b0);
+                b1 = mfma(a[4 * i + 3], high, b1);
+            }
+            const float4v cm = mfma(am, ws.mins, float4v{0.f, 0.f, 0.f, 0.f});
+            const float bk[4] = {back.x, back.y, back.z, back.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[c][r] = __builtin_fmaf(bk[r], __builtin_fmaf(ws.nm, cm[r], ws.d * (b0[r] + b1[r])), acc[c][r]);
+        }
+    }
+    // rows 0..3 of the tile are in lanes 0..15 (column c16): join the waves
+    float *red = reinterpret_cast<float *>(base);
+    asm volatile("" ::: "memory");
+    if (quarter == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[(c * 4 + r) * 16 + c16] = acc[c][r];
+    }
+    __syncthreads();
+    if (threadIdx.x >= 128) return;
+    const int c = threadIdx.x >> 6, r = (threadIdx.x >> 4) & 3;
+    if ((kSwiglu && c) || r >= t.count) return;
+    const int p = pair_at(r);
+    const int n = n0 + 16 * c + c16;
+    if (n >= g.N || static_cast<unsigned>(p) >= static_cast<unsigned>(g.P)) return;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const float *part = reinterpret_cast<const float *>(lds + w * FewLds::kWave);
+        s[0] += part[(c * 4 + r) * 16 + c16];
+        if (kSwiglu) s[1] += part[(4 + r) * 16 + c16];
+    }
+    g.y[static_cast<size_t>(p) * g.N + n] = kSwiglu ? swiglu(s[0], s[1]) : s[0];
+}
+
 // out[m, n] = sum_j weight[m, j] * y[m * top_k + j, n] over the choices with a
 // valid expert, in ascending j.
 __global__ __launch_bounds__(256) void combine_kernel(const float *y, const int *expert, const float *weight,
@@ -555,9 +745,25 @@ int check_grouped(const void *w, const void *w2, const float *x, int x_div, cons
     return Q4K_OK;
 }
 
+bool few_rows(const Grouped &g) { return g.P <= 2 * g.E; }
+
+template <int WAVES, bool kSwiglu>
+hipError_t launch_few(const Grouped &g, const float *x, hipStream_t stream) {
+    constexpr int kBytes = WAVES * FewLds::kWave, kTileN = kSwiglu ? 16 : 32;
+    const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(few_kernel<WAVES, kSwiglu>), kBytes);
+    if (err != hipSuccess) return err;
+    const dim3 grid((g.N + kTileN - 1) / kTileN, g.P / kFewRows + (g.E < g.P ? g.E : g.P));
+    hipLaunchKernelGGL((few_kernel<WAVES, kSwiglu>), grid, dim3(64 * WAVES), kBytes, stream, g, x);
+    return hipGetLastError();
+}
+
 // Stages x, then the products.  g.x is filled in here.
 hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     const size_t xrows = (static_cast<size_t>(g.P) + g.x_div - 1) / g.x_div, KB = g.K / kBlockWeights;
+    if (few_rows(g)) {
+        if (g.w2) return KB > 4 ? launch_few<8, true>(g, x, stream) : launch_few<4, true>(g, x, stream);
+        return KB > 4 ? launch_few<8, false>(g, x, stream) : launch_few<4, false>(g, x, stream);
+    }
     float *ws = nullptr;
     hipError_t err = workspace(stream, xrows * (KB * (kImageBlock + kSumsBlock) + 16), &ws);
     if (err != hipSuccess) return err;

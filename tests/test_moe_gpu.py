@@ -121,7 +121,7 @@ def _table(sizes, tag):
 
 SIZES = [
     [1], [0, 1], [1] * 8 + [0] * 8, [3, 0, 17, 16, 15, 1], [64, 63, 65, 0, 129], [300, 2, 0, 40], [5, 7, 0, 0, 33, 9],
-    [0, 0, 700], [31, 32, 33, 34],
+    [0, 0, 700], [31, 32, 33, 34], [0] * 30 + [9, 4], [2, 5, 0, 0, 1, 0, 0, 3],
 ]
 
 
