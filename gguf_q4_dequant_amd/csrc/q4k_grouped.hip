@@ -589,7 +589,7 @@ __device__ __forceinline__ void stage_few(const float4 v[4], int lane, uint8_t *
 }
 
 template <int WAVES, bool kSwiglu>
-__global__ __launch_bounds__(64 * WAVES) void few_kernel(Grouped g, const float *x) {
+__global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const float *x) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, quarter = lane >> 4;
@@ -648,41 +648,51 @@ __global__ __launch_bounds__(64 * WAVES) void few_kernel(Grouped g, const float 
         WBlock wb[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) wb[c] = load_block(base + (c * 16 + c16) * kBlockBytes, 0, quarter);
-        half8 a[16];
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-            a[s] = *reinterpret_cast<const half8 *>(base + FewLds::kXAt + arow * kImageBlock + s * 64 + quarter * 16);
-        const uint4 sm = *reinterpret_cast<const uint4 *>(base + FewLds::kSumsAt + arow * kSumsBlock + (quarter & 1) * 16);
-        const half8 am = __builtin_bit_cast(half8, quarter < 2 ? sm : uint4{0, 0, 0, 0});
-        const float4 back = *reinterpret_cast<const float4 *>(base + FewLds::kBackAt);
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // everything read: the slots may be filled again
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // W is in registers: its slot may be filled again
         if (b + WAVES < KB) {
             copy_w(b + WAVES);
             load_x(b + WAVES);
         }
+        WScales ws[2];
+        float4v blk[2][2], cm[2];
+        const uint4 sm = *reinterpret_cast<const uint4 *>(base + FewLds::kSumsAt + arow * kSumsBlock + (quarter & 1) * 16);
+        const half8 am = __builtin_bit_cast(half8, quarter < 2 ? sm : uint4{0, 0, 0, 0});
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const WScales ws = block_scales(wb[c].head, quarter);
-            const uint32_t q[8] = {wb[c].q0.x, wb[c].q0.y, wb[c].q0.z, wb[c].q0.w,
-                                   wb[c].q1.x, wb[c].q1.y, wb[c].q1.z, wb[c].q1.w};
-            float4v b0 = {0.f, 0.f, 0.f, 0.f}, b1 = b0;
+            ws[c] = block_scales(wb[c].head, quarter);
+            cm[c] = mfma(am, ws[c].mins, float4v{0.f, 0.f, 0.f, 0.f});
+            blk[c][0] = blk[c][1] = float4v{0.f, 0.f, 0.f, 0.f};
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // the operands of one pair of steps in registers at a time
+            half8 a[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                a[s] = *reinterpret_cast<const half8 *>(base + FewLds::kXAt + arow * kImageBlock + (4 * i + s) * 64 + quarter * 16);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint4 qq = i < 2 ? wb[c].q0 : wb[c].q1;
+                const uint32_t u = i & 1 ? qq.z : qq.x, v = i & 1 ? qq.w : qq.y;
                 half8 low, high;
-                operand(q[2 * i], q[2 * i + 1], ws, 0, low);
-                operand(q[2 * i], q[2 * i + 1], ws, 1, high);
-                b0 = mfma(a[4 * i + 0], low, b0);
-                b1 = mfma(a[4 * i + 2], high, b1);
-                b0 = mfma(a[4 * i + 1], low, b0);
-                b1 = mfma(a[4 * i + 3], high, b1);
+                operand(u, v, ws[c], 0, low);
+                operand(u, v, ws[c], 1, high);
+                blk[c][0] = mfma(a[0], low, blk[c][0]);
+                blk[c][1] = mfma(a[2], high, blk[c][1]);
+                blk[c][0] = mfma(a[1], low, blk[c][0]);
+                blk[c][1] = mfma(a[3], high, blk[c][1]);
             }
-            const float4v cm = mfma(am, ws.mins, float4v{0.f, 0.f, 0.f, 0.f});
-            const float bk[4] = {back.x, back.y, back.z, back.w};
+        }
+        const float4 back = *reinterpret_cast<const float4 *>(base + FewLds::kBackAt);
+        const float bk[4] = {back.x, back.y, back.z, back.w};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                acc[c][r] = __builtin_fmaf(bk[r], __builtin_fmaf(ws.nm, cm[r], ws.d * (b0[r] + b1[r])), acc[c][r]);
-        }
+                acc[c][r] = __builtin_fmaf(bk[r], __builtin_fmaf(ws[c].nm, cm[c][r], ws[c].d * (blk[c][0][r] + blk[c][1][r])),
+                                           acc[c][r]);
+        asm volatile("" ::: "memory");
     }
     // rows 0..3 of the tile are in lanes 0..15 (column c16): join the waves
     float *red = reinterpret_cast<float *>(base);
