@@ -6,14 +6,16 @@
 // that finds the lowest expert holding it: a round costs about a hundred
 // cycles, against the three thousand of comparing every pair of 128 scores.
 //
-// Grouping is a stable counting sort, without atomics whose order could
-// change a result: pairs are taken 64 at a time by a wave, each lane finds
-// the lanes with its own expert by one ballot per bit of the expert number
-// (its rank is the number of them below it), and per-wave counts per expert,
-// summed over waves (and workgroups) in order, give every wave its first
-// place in every group.  Up to kSingleTokens tokens one workgroup of sixteen
-// waves does all of it in one launch; above, the routing workgroups leave
-// their counts in the workspace and a second launch places the pairs.
+// Grouping is a stable counting sort without atomics whose order could change
+// a result.  Up to kSingleTokens tokens one workgroup of sixteen waves routes
+// and groups in one launch: pairs are taken 64 at a time by a wave, each lane
+// finds the lanes with its own expert by one ballot per bit of the expert
+// number (its rank is the number of them below it), and per-wave counts per
+// expert, summed over the waves in order, give every wave its first place in
+// every group.  Above, a second launch has one workgroup per expert, which
+// reads the whole table of choices: a ballot of "before my expert" gives the
+// group's offset, one of "my expert" the places.  Every workgroup reads all P
+// choices, but from the L2 and 64 at a time, and no counts cross workgroups.
 #include <math.h>
 
 #include "../../include/q4k_moe.h"
@@ -22,9 +24,7 @@
 namespace q4k {
 namespace {
 
-constexpr int kSingleTokens = 64;   // tokens routed and grouped by one workgroup
-constexpr int kSinglePairs = 8192;  // pairs grouped by one workgroup (q4k_moe_group)
-constexpr int kMaxBlocks = 256;     // workgroups of the two-launch forms
+constexpr int kSingleTokens = 64;  // tokens routed and grouped by one workgroup
 constexpr int kSingleThreads = 1024;
 constexpr int kThreads = 256;
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ void route_token(const float *logits, const float *bi
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = v * 64 + lane;
-            s[v] = s[v] / sum;
+            if (!sigmoid) s[v] = s[v] / sum;
             key[v] = l[v] > -INFINITY ? s[v] + static_cast<double>(bias[e]) : -INFINITY;
             if (!(key[v] > -INFINITY)) key[v] = -INFINITY;
         }
@@ -189,30 +189,21 @@ __device__ __forceinline__ void count_pairs(F expert_of, int count, int E, int *
     }
 }
 
-// Places the workgroup's pairs first + [0, count): hist [waves][E] holds
-// the counts of count_pairs, tot [E + 1] is scratch, both in LDS.  counts
-// [blocks][E] are all workgroups' counts (one workgroup: null, its own).
+// Places the pairs of one workgroup: hist [waves][E] holds the counts of
+// count_pairs, tot [E + 1] is scratch, both in LDS.
 template <class F>
-__device__ __forceinline__ void place_pairs(F expert_of, int first, int count, int E, int P, int *hist, int *tot,
-                                            const int *counts, int block, int blocks, int *offsets, int *rows) {
+__device__ __forceinline__ void place_pairs(F expert_of, int count, int E, int *hist, int *tot, int *offsets,
+                                            int *rows) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int before = 0, all = 0;
-        if (counts) {
-            for (int g = 0; g < blocks; ++g) {
-                const int c = counts[g * E + e];
-                before += g < block ? c : 0;
-                all += c;
-            }
-        }
-        int run = before;
+        int run = 0;
         for (int w = 0; w < waves; ++w) {
             const int c = hist[w * E + e];
             hist[w * E + e] = run;
             run += c;
         }
-        tot[e] = counts ? all : run;
+        tot[e] = run;
     }
     __syncthreads();
     if (wave == 0) {  // exclusive scan of the totals over the experts
@@ -231,8 +222,7 @@ __device__ __forceinline__ void place_pairs(F expert_of, int first, int count, i
         if (lane == 0) tot[E] = carry;
     }
     __syncthreads();
-    if (block == 0)
-        for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = tot[e];
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = tot[e];
     const int chunks = (count + 63) / 64, per = (chunks + waves - 1) / waves, bits = expert_bits(E);
     for (int c = wave * per; c < min(chunks, (wave + 1) * per); ++c) {
         const int i = c * 64 + lane;
@@ -241,115 +231,141 @@ __device__ __forceinline__ void place_pairs(F expert_of, int first, int count, i
         const uint64_t same = same_expert(e, valid, bits);
         const uint64_t below = same & lanes_below(lane);
         if (valid) {
-            rows[tot[e] + hist[wave * E + e] + __builtin_popcountll(below)] = first + i;
+            rows[tot[e] + hist[wave * E + e] + __builtin_popcountll(below)] = i;
             if (below == 0) atomicAdd(&hist[wave * E + e], __builtin_popcountll(same));
         }
     }
-    for (int64_t i = static_cast<int64_t>(tot[E]) + block * blockDim.x + threadIdx.x; i < P; i += blocks * blockDim.x)
-        rows[i] = -1;
+    for (int i = tot[E] + threadIdx.x; i < count; i += blockDim.x) rows[i] = -1;
 }
 
 struct RouteArgs {
     const float *logits, *bias;
     int *expert;
     float *weight;
-    int *offsets, *rows, *counts;  // counts: workspace [blocks][E] (two launches) or null
-    int M, E, top_k, flags, per;   // per: tokens of a workgroup
+    int *offsets, *rows;
+    int M, E, top_k, flags;
     float scale;
 };
 
-// LDS: hist [waves][E], tot [E + 1], and the workgroup's choices [per][top_k].
+// One workgroup: routing and grouping.  LDS: hist [waves][E], tot [E + 1] and
+// the choices [M][top_k].
 template <int VPL, class T>
-__global__ __launch_bounds__(kSingleThreads) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(kSingleThreads) void route_group_kernel(RouteArgs a) {
     extern __shared__ int lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     int *hist = lds, *tot = hist + waves * a.E, *chosen = tot + a.E + 1;
     for (int i = threadIdx.x; i < waves * a.E; i += blockDim.x) hist[i] = 0;
-    const int m0 = blockIdx.x * a.per, tokens = min(a.per, a.M - m0);
-    for (int t = wave; t < tokens; t += waves) {
-        const size_t m = m0 + t;
+    for (int m = wave; m < a.M; m += waves) {
         int e;
         float w;
-        route_token<VPL, T>(a.logits + m * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
+        route_token<VPL, T>(a.logits + static_cast<size_t>(m) * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
         if (lane < a.top_k) {
-            chosen[t * a.top_k + lane] = e;
+            chosen[m * a.top_k + lane] = e;
             a.expert[m * a.top_k + lane] = e;
             a.weight[m * a.top_k + lane] = w;
         }
     }
     __syncthreads();
-    const int count = tokens * a.top_k;
+    const int count = a.M * a.top_k;
     const auto expert_of = [&](int i) { return chosen[i]; };
     count_pairs(expert_of, count, a.E, hist);
-    if (a.counts) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-            int c = 0;
-            for (int w = 0; w < waves; ++w) c += hist[w * a.E + e];
-            a.counts[blockIdx.x * a.E + e] = c;
+    place_pairs(expert_of, count, a.E, hist, tot, a.offsets, a.rows);
+}
+
+// Routing only: one token per wave.
+template <int VPL, class T>
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 63;
+    const size_t m = static_cast<size_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+    if (m >= static_cast<size_t>(a.M)) return;
+    int e;
+    float w;
+    route_token<VPL, T>(a.logits + m * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
+    if (lane < a.top_k) {
+        a.expert[m * a.top_k + lane] = e;
+        a.weight[m * a.top_k + lane] = w;
+    }
+}
+
+// Grouping: workgroup e places the pairs of expert e; the last one also closes
+// the offsets and fills the tail of rows.
+__global__ __launch_bounds__(kSingleThreads) void group_kernel(const int *expert, int P, int E, int *offsets, int *rows) {
+    constexpr int kWaves = kSingleThreads / 64, kAhead = 8;
+    __shared__ int s_less[kWaves], s_same[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int mine = blockIdx.x;
+    // this wave's share, in steps of 64 pairs
+    const int64_t steps = (static_cast<int64_t>(P) + 63) / 64, per = (steps + kWaves - 1) / kWaves;
+    const int64_t i0 = wave * per * 64, i1 = min(static_cast<int64_t>(P), i0 + per * 64);
+    int less = 0, same = 0;
+    for (int64_t i = i0; i < i1; i += 64 * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) e[k] = i + k * 64 + lane < i1 ? expert[i + k * 64 + lane] : -1;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            // as unsigned, -1 and every other negative number is above any expert
+            less += __builtin_popcountll(__ballot(static_cast<unsigned>(e[k]) < static_cast<unsigned>(mine)));
+            same += __builtin_popcountll(__ballot(e[k] == mine));
         }
-        return;
     }
-    place_pairs(expert_of, 0, count, a.E, count, hist, tot, nullptr, 0, 1, a.offsets, a.rows);
+    if (lane == 0) {
+        s_less[wave] = less;
+        s_same[wave] = same;
+    }
+    __syncthreads();
+    int base = 0, before = 0, all = 0;
+    for (int w = 0; w < kWaves; ++w) {
+        base += s_less[w];
+        before += w < wave ? s_same[w] : 0;
+        all += s_same[w];
+    }
+    if (threadIdx.x == 0) offsets[mine] = base;
+    int at = base + before;
+    for (int64_t i = i0; i < i1; i += 64 * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) e[k] = i + k * 64 + lane < i1 ? expert[i + k * 64 + lane] : -1;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint64_t with = __ballot(e[k] == mine);
+            if (e[k] == mine) rows[at + __builtin_popcountll(with & lanes_below(lane))] = static_cast<int>(i + k * 64 + lane);
+            at += __builtin_popcountll(with);
+        }
+    }
+    if (mine == E - 1) {
+        if (threadIdx.x == 0) offsets[E] = base + all;
+        for (int64_t i = base + all + static_cast<int64_t>(threadIdx.x); i < P; i += kSingleThreads) rows[i] = -1;
+    }
 }
 
-// Counts of each workgroup's share of a table of choices.
-__global__ __launch_bounds__(kThreads) void count_kernel(const int *expert, int P, int E, int per, int *counts) {
-    extern __shared__ int lds[];
-    const int waves = blockDim.x >> 6;
-    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) lds[i] = 0;
-    __syncthreads();
-    const int first = blockIdx.x * per, count = min(per, P - first);
-    count_pairs([&](int i) { return expert[first + i]; }, count, E, lds);
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int c = 0;
-        for (int w = 0; w < waves; ++w) c += lds[w * E + e];
-        counts[blockIdx.x * E + e] = c;
-    }
-}
-
-// Places each workgroup's share; counts as left by the launch before, or null
-// for a single workgroup.
-__global__ __launch_bounds__(kSingleThreads) void place_kernel(const int *expert, int P, int E, int per,
-                                                               const int *counts, int *offsets, int *rows) {
-    extern __shared__ int lds[];
-    const int waves = blockDim.x >> 6;
-    int *hist = lds, *tot = hist + waves * E;
-    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
-    const int first = blockIdx.x * per, count = min(per, P - first);
-    const auto expert_of = [&](int i) { return expert[first + i]; };
-    count_pairs(expert_of, count, E, hist);
-    place_pairs(expert_of, first, count, E, P, hist, tot, counts, blockIdx.x, gridDim.x, offsets, rows);
+hipError_t launch_group(const int *expert, int P, int E, int *offsets, int *rows, hipStream_t stream) {
+    hipLaunchKernelGGL(group_kernel, dim3(E), dim3(kSingleThreads), 0, stream, expert, P, E, offsets, rows);
+    return hipGetLastError();
 }
 
 template <int VPL, class T>
-hipError_t launch_route(const RouteArgs &a, int blocks, int threads, hipStream_t stream) {
-    const int bytes = ((threads / 64) * a.E + a.E + 1 + a.per * a.top_k) * 4;
-    hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_kernel<VPL, T>), 128 << 10);
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((route_kernel<VPL, T>), dim3(blocks), dim3(threads), bytes, stream, a);
-    return hipGetLastError();
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
+    if (a.M <= kSingleTokens) {
+        const int waves = kSingleThreads / 64;
+        const int bytes = (waves * a.E + a.E + 1 + a.M * a.top_k) * 4;
+        const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_group_kernel<VPL, T>), 96 << 10);
+        if (err != hipSuccess) return err;
+        hipLaunchKernelGGL((route_group_kernel<VPL, T>), dim3(1), dim3(kSingleThreads), bytes, stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((route_kernel<VPL, T>), dim3((a.M - 1) / (kThreads / 64) + 1), dim3(kThreads), 0, stream, a);
+    const hipError_t err = hipGetLastError();
+    return err != hipSuccess ? err : launch_group(a.expert, a.M * a.top_k, a.E, a.offsets, a.rows, stream);
 }
 
 template <class T>
-hipError_t launch_route_for(const RouteArgs &a, int blocks, int threads, hipStream_t stream) {
-    if (a.E <= 64) return launch_route<1, T>(a, blocks, threads, stream);
-    if (a.E <= 128) return launch_route<2, T>(a, blocks, threads, stream);
-    if (a.E <= 256) return launch_route<4, T>(a, blocks, threads, stream);
-    if (a.E <= 512) return launch_route<8, T>(a, blocks, threads, stream);
-    return launch_route<16, T>(a, blocks, threads, stream);
-}
-
-hipError_t launch_place(const int *expert, int P, int E, int per, int blocks, int threads, const int *counts,
-                        int *offsets, int *rows, hipStream_t stream) {
-    const int bytes = ((threads / 64) * E + E + 1) * 4;
-    hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(place_kernel), 128 << 10);
-    if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(threads), bytes, stream, expert, P, E, per, counts, offsets,
-                       rows);
-    return hipGetLastError();
+hipError_t launch_route_for(const RouteArgs &a, hipStream_t stream) {
+    if (a.E <= 64) return launch_route<1, T>(a, stream);
+    if (a.E <= 128) return launch_route<2, T>(a, stream);
+    if (a.E <= 256) return launch_route<4, T>(a, stream);
+    if (a.E <= 512) return launch_route<8, T>(a, stream);
+    return launch_route<16, T>(a, stream);
 }
 
 bool misaligned4(const void *a, const void *b = nullptr, const void *c = nullptr, const void *d = nullptr,
@@ -376,26 +392,9 @@ extern "C" int q4k_moe_route(const float *logits, const float *bias, int M, int 
     if (misaligned4(logits, bias, expert, weight, offsets, rows)) return Q4K_ERR_ALIGN;
     const int dev_rc = check_device();
     if (dev_rc != Q4K_OK) return dev_rc;
-    if (M == 0) return status(launch_place(nullptr, 0, E, 0, 1, kThreads, nullptr, offsets, rows, stream));
-    RouteArgs a = {logits, bias, expert, weight, offsets, rows, nullptr, M, E, top_k, flags, M, scale};
-    int blocks = 1, threads = kSingleThreads;
-    if (M > kSingleTokens) {
-        // one wave per token in flight, at most kMaxBlocks workgroups of four
-        a.per = (M - 1) / kMaxBlocks + 1;
-        a.per = a.per < 4 ? 4 : a.per;
-        // the choices share the LDS with the counts
-        if (static_cast<int64_t>(a.per) * top_k * 4 > (64 << 10)) a.per = (64 << 10) / (4 * top_k);
-        blocks = (M - 1) / a.per + 1;
-        threads = kThreads;
-        float *ws = nullptr;
-        if (workspace(stream, static_cast<size_t>(blocks) * E * 4, &ws) != hipSuccess) return Q4K_ERR_ALLOC;
-        a.counts = reinterpret_cast<int *>(ws);
-    }
-    hipError_t err = bias ? launch_route_for<double>(a, blocks, threads, stream)
-                          : launch_route_for<float>(a, blocks, threads, stream);
-    if (err == hipSuccess && a.counts)
-        err = launch_place(expert, M * top_k, E, a.per * top_k, blocks, kThreads, a.counts, offsets, rows, stream);
-    return status(err);
+    if (M == 0) return status(launch_group(nullptr, 0, E, offsets, rows, stream));
+    const RouteArgs a = {logits, bias, expert, weight, offsets, rows, M, E, top_k, flags, scale};
+    return status(bias ? launch_route_for<double>(a, stream) : launch_route_for<float>(a, stream));
 }
 
 extern "C" int q4k_moe_group(const int *expert, int P, int E, int *offsets, int *rows, hipStream_t stream) {
@@ -405,16 +404,5 @@ extern "C" int q4k_moe_group(const int *expert, int P, int E, int *offsets, int 
     if (misaligned4(expert, offsets, rows)) return Q4K_ERR_ALIGN;
     const int dev_rc = check_device();
     if (dev_rc != Q4K_OK) return dev_rc;
-    if (P <= kSinglePairs)
-        return status(launch_place(expert, P, E, P, 1, kSingleThreads, nullptr, offsets, rows, stream));
-    const int per = (((P - 1) / kMaxBlocks + 1) + 255) & ~255;
-    const int blocks = (P - 1) / per + 1;
-    float *ws = nullptr;
-    if (workspace(stream, static_cast<size_t>(blocks) * E * 4, &ws) != hipSuccess) return Q4K_ERR_ALLOC;
-    int *counts = reinterpret_cast<int *>(ws);
-    hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(kThreads), (kThreads / 64) * E * 4, stream, expert, P, E, per,
-                       counts);
-    hipError_t err = hipGetLastError();
-    if (err == hipSuccess) err = launch_place(expert, P, E, per, blocks, kThreads, counts, offsets, rows, stream);
-    return status(err);
+    return status(launch_group(expert, P, E, offsets, rows, stream));
 }
