@@ -1,14 +1,14 @@
 // Penalties for repeated tokens, biases and grammar masks on logits, and the
 // greedy choice under them (include/q4k_select.h).
 //
-// One workgroup per chunk of one row.  A chunk's counts of history tokens and
-// its sums of biases are built in LDS from the row's two short lists (every
-// workgroup of a row reads them whole; they stay in L2), so the logits
-// themselves are read once and written once, and no [M, N] table of counts or
-// biases ever exists.  The kernel is bound by that one pass over the logits.
-// Counts are integers (LDS atomics in any order give the same); the biases of
-// a token named more than once are added in list order by the thread that
-// owns its first mention.
+// One workgroup per chunk of one row.  The chunk's counts of history tokens
+// are gathered in LDS, its biases in an ordered LDS list, both from the row's
+// two short lists (every workgroup of a row reads them whole; they stay in the
+// L2), so the logits are read once and written once and no [M, N] table of
+// counts or biases ever exists.  The kernel is bound by that one pass over the
+// logits.  Counts are integers (LDS atomics in any order give the same); the
+// biases of a token named more than once are added in list order by the thread
+// that holds its logit.
 #include <limits.h>
 #include <math.h>
 
@@ -19,7 +19,9 @@ namespace q4k {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBiases = 512;  // biases looked through at a time
 
+typedef int int4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));  // rows of odd N start anywhere
 
 __device__ __forceinline__ void take_better(float &v, int &i, float v2, int i2) {
@@ -54,8 +56,9 @@ template <int kPer, bool kSelect>
 __global__ __launch_bounds__(kThreads) void adjust_kernel(const float *logits, float *out, q4k_adjustment a, int N,
                                                           int chunks, float *part) {
     constexpr int kChunk = kThreads * kPer;
-    __shared__ int counts[kChunk];
-    __shared__ float biases[kChunk];
+    __shared__ __align__(16) int counts[kChunk];
+    __shared__ float2 list[kBiases];  // (place in the chunk, value)
+    __shared__ int listed;
     const int tid = threadIdx.x, c = blockIdx.x;
     const size_t m = blockIdx.y;
     const int n0 = c * kChunk, n_here = min(kChunk, N - n0);
@@ -75,49 +78,78 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(const float *logits, f
             for (int k = 0; k < 4; ++k) z[j + k] = i + k < n_here ? row[i + k] : 0.f;
         }
     }
-    const bool history = a.history_len > 0, bias = a.bias_len > 0;
-    if (history || bias) {
+    if (a.history_len > 0) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            counts[j * kThreads + tid] = 0;
-            biases[j * kThreads + tid] = 0.f;
-        }
+        for (int j = 0; j < kPer; j += 4) *reinterpret_cast<int4 *>(&counts[(j * kThreads / 4 + tid) * 4]) = int4{0, 0, 0, 0};
         __syncthreads();
         const int *ids = a.history + m * a.history_len;
-        for (int i = tid; i < a.history_len; i += kThreads) {
+        const auto count = [&](int id) {
             // negative ids wrap to far above any chunk
-            const unsigned at = static_cast<unsigned>(ids[i]) - static_cast<unsigned>(n0);
-            if (at < static_cast<unsigned>(n_here)) atomicAdd(&counts[at], 1);
-        }
-        const int *bid = a.bias_id + m * a.bias_len;
-        const float *bval = a.bias_value + m * a.bias_len;
-        for (int i = tid; i < a.bias_len; i += kThreads) {
-            const int id = bid[i];
             const unsigned at = static_cast<unsigned>(id) - static_cast<unsigned>(n0);
-            if (at >= static_cast<unsigned>(n_here)) continue;
-            float sum = 0.f;
-            bool first = true;
-            for (int k = 0; k < a.bias_len; ++k) {
-                if (bid[k] != id) continue;
-                if (k < i) {
-                    first = false;
-                    break;
-                }
-                sum += bval[k];
-            }
-            if (first) biases[at] = sum;
+            if (at < static_cast<unsigned>(n_here)) atomicAdd(&counts[at], 1);
+        };
+        const int fours = a.history_len / 4;
+        for (int i = tid; i < fours; i += kThreads) {
+            const int4u v = *reinterpret_cast<const int4u *>(ids + 4 * i);
+            count(v.x);
+            count(v.y);
+            count(v.z);
+            count(v.w);
         }
+        if (tid < a.history_len - 4 * fours) count(ids[4 * fours + tid]);
         __syncthreads();
         const float rep = a.repetition ? a.repetition[m] : 1.f;
         const float freq = a.frequency ? a.frequency[m] : 0.f;
         const float pres = a.presence ? a.presence[m] : 0.f;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int i = ((j & ~3) * kThreads / 4 + tid) * 4 + (j & 3);
-            const int n = counts[i];
-            if (n > 0) z[j] = penalised(z[j], static_cast<float>(n), rep, freq, pres);
-            if (bias) z[j] += biases[i];
+        for (int j = 0; j < kPer; j += 4) {
+            const int4 c4 = *reinterpret_cast<const int4 *>(&counts[(j * kThreads / 4 + tid) * 4]);
+            const int n[4] = {c4.x, c4.y, c4.z, c4.w};
+            if ((c4.x | c4.y | c4.z | c4.w) != 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (n[k] > 0) z[j + k] = penalised(z[j + k], static_cast<float>(n[k]), rep, freq, pres);
+            }
         }
+    }
+    if (a.bias_len > 0) {
+        const int *bid = a.bias_id + m * a.bias_len;
+        const float *bval = a.bias_value + m * a.bias_len;
+        float sum[kPer];
+        uint32_t named = 0;  // bit j: logit j of this thread has a bias
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum[j] = 0.f;
+        for (int first = 0; first < a.bias_len; first += kBiases) {
+            __syncthreads();  // the list of the round before has been read
+            if (tid < 64) {   // one wave packs the chunk's entries in list order
+                int found = 0;
+                const int end = min(a.bias_len, first + kBiases);
+                for (int i = first; i < end; i += 64) {
+                    const int id = i + tid < end ? bid[i + tid] : -1;
+                    const unsigned at = static_cast<unsigned>(id) - static_cast<unsigned>(n0);
+                    const bool here = at < static_cast<unsigned>(n_here);
+                    const uint64_t with = __ballot(here);
+                    if (here) list[found + __builtin_popcountll(with & ((1ull << tid) - 1))] = float2{__uint_as_float(at), bval[i + tid]};
+                    found += __builtin_popcountll(with);
+                }
+                if (tid == 0) listed = found;
+            }
+            __syncthreads();
+            for (int h = 0; h < listed; ++h) {
+                const unsigned at = __float_as_uint(list[h].x);
+                if (((at >> 2) & (kThreads - 1)) != static_cast<unsigned>(tid)) continue;
+                const float value = list[h].y;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (at == static_cast<unsigned>(((j & ~3) * kThreads / 4 + tid) * 4 + (j & 3))) {
+                        sum[j] += value;
+                        named |= 1u << j;
+                    }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if ((named >> j) & 1u) z[j] += sum[j];
     }
     uint32_t allowed = 0xFFFFFFFFu;  // bit j: logit j of this thread
     if (a.mask) {

@@ -61,59 +61,79 @@ __device__ __forceinline__ int scale_exponent(float mx) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Stages one row of x per workgroup (see above): thread u takes eight
-// consecutive values at a time.
-__global__ __launch_bounds__(256) void stage_rows_kernel(const float *x, int K, uint8_t *img, uint8_t *sums,
-                                                         float *back) {
-    __shared__ float wave_mx[4];
+// Stages eight consecutive values of a row at k (see above); the four threads
+// of a sub-block are neighbours and join its sum.
+__device__ __forceinline__ void stage_eight(const float4 a, const float4 b, int k, float up, uint8_t *im, uint8_t *sm) {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    constexpr int order[8] = {0, 2, 1, 3, 4, 6, 5, 7};
+    half8 hi, lo;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = v[order[i]] * up;
+        hi[i] = static_cast<_Float16>(t);
+        lo[i] = static_cast<_Float16>(t - static_cast<float>(hi[i]));
+        s += t;
+    }
+    const int blk = k / kBlockWeights, in = k % kBlockWeights;
+    const int quarter = in >> 6, h = (in >> 5) & 1, i = (in >> 3) & 3;
+    uint8_t *o = im + blk * kImageBlock + (2 * i + h) * 128 + quarter * 16;
+    *reinterpret_cast<half8 *>(o) = hi;
+    *reinterpret_cast<half8 *>(o + 64) = lo;
+    // 32 values below 2^15 each: times 2^-6 to stay in binary16's range
+    s += __shfl_xor(s, 1);
+    s += __shfl_xor(s, 2);
+    s *= 0.015625f;
+    if (i == 0) {
+        const _Float16 sh = static_cast<_Float16>(s);
+        _Float16 *so = reinterpret_cast<_Float16 *>(sm + blk * kSumsBlock) + (in >> 5);
+        so[0] = sh;
+        so[8] = static_cast<_Float16>(s - static_cast<float>(sh));
+    }
+}
+
+// Stages one row of x per workgroup: the row's first kKept * 8 values of every
+// thread stay in registers between the maximum and the conversion.
+constexpr int kStageThreads = 256, kKept = 4;
+__global__ __launch_bounds__(kStageThreads) void stage_rows_kernel(const float *x, int K, uint8_t *img, uint8_t *sums,
+                                                                   float *back) {
+    __shared__ float wave_mx[kStageThreads / 64];
     const size_t row = blockIdx.x;
     const float *xr = x + row * K;
-    float mx = 0.f;
-    for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
-        const float4 a = *reinterpret_cast<const float4 *>(xr + k), b = *reinterpret_cast<const float4 *>(xr + k + 4);
-        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))));
-        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+    const int step = blockDim.x * 8, k0 = threadIdx.x * 8;
+    float4 a[kKept], b[kKept];
+#pragma unroll
+    for (int j = 0; j < kKept; ++j) {
+        a[j] = b[j] = float4{0.f, 0.f, 0.f, 0.f};
+        if (k0 + j * step < K) {
+            a[j] = *reinterpret_cast<const float4 *>(xr + k0 + j * step);
+            b[j] = *reinterpret_cast<const float4 *>(xr + k0 + j * step + 4);
+        }
     }
+    const auto largest = [](float mx, const float4 v) {
+        return fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+    };
+    float mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < kKept; ++j) mx = largest(largest(mx, a[j]), b[j]);
+    for (int64_t k = k0 + static_cast<int64_t>(kKept) * step; k < K; k += step)
+        mx = largest(largest(mx, *reinterpret_cast<const float4 *>(xr + k)), *reinterpret_cast<const float4 *>(xr + k + 4));
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
     if ((threadIdx.x & 63) == 0) wave_mx[threadIdx.x >> 6] = mx;
     __syncthreads();
-    mx = fmaxf(fmaxf(wave_mx[0], wave_mx[1]), fmaxf(wave_mx[2], wave_mx[3]));
+    for (unsigned w = 0; w < blockDim.x >> 6; ++w) mx = fmaxf(mx, wave_mx[w]);
     const int e = scale_exponent(mx);
     const float up = power_of_two(e);
     if (threadIdx.x == 0) back[row] = power_of_two(24 - e);
     uint8_t *im = img + row * (K / kBlockWeights) * kImageBlock;
     uint8_t *sm = sums + row * (K / kBlockWeights) * kSumsBlock;
-    for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
-        const float4 a = *reinterpret_cast<const float4 *>(xr + k), b = *reinterpret_cast<const float4 *>(xr + k + 4);
-        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        constexpr int order[8] = {0, 2, 1, 3, 4, 6, 5, 7};
-        half8 hi, lo;
-        float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float t = v[order[i]] * up;
-            hi[i] = static_cast<_Float16>(t);
-            lo[i] = static_cast<_Float16>(t - static_cast<float>(hi[i]));
-            s += v[i] * up;
-        }
-        const int blk = k / kBlockWeights, in = k % kBlockWeights;
-        const int quarter = in >> 6, h = (in >> 5) & 1, i = (in >> 3) & 3;
-        uint8_t *o = im + blk * kImageBlock + (2 * i + h) * 128 + quarter * 16;
-        *reinterpret_cast<half8 *>(o) = hi;
-        *reinterpret_cast<half8 *>(o + 64) = lo;
-        // the sub-block's sum over its four threads (32 values below 2^15
-        // each), times 2^-6 to stay in binary16's range
-        s += __shfl_xor(s, 1);
-        s += __shfl_xor(s, 2);
-        s *= 0.015625f;
-        if (i == 0) {
-            const _Float16 sh = static_cast<_Float16>(s);
-            _Float16 *so = reinterpret_cast<_Float16 *>(sm + blk * kSumsBlock) + (in >> 5);
-            so[0] = sh;
-            so[8] = static_cast<_Float16>(s - static_cast<float>(sh));
-        }
-    }
+    for (int j = 0; j < kKept; ++j)
+        if (k0 + j * step < K) stage_eight(a[j], b[j], k0 + j * step, up, im, sm);
+    for (int64_t k = k0 + static_cast<int64_t>(kKept) * step; k < K; k += step)
+        stage_eight(*reinterpret_cast<const float4 *>(xr + k), *reinterpret_cast<const float4 *>(xr + k + 4),
+                    static_cast<int>(k), up, im, sm);
 }
 
 struct Grouped {
@@ -128,35 +148,77 @@ struct Tile {
     int e, first, count;  // rows[first .. first + count) of expert e
 };
 
-// Tile number t of the groups cut into tiles of TM rows (count 0: no such
-// tile).  Every wave scans the offsets by itself, 64 experts at a time.
+// The groups cut into tiles of TM rows.  Lane l of a wave owns experts 4l ..
+// 4l + 3 of each 256; every wave scans the offsets by itself (one memory round
+// trip and a scan in the vector unit for up to 256 experts).
 template <int TM>
-__device__ __forceinline__ Tile find_tile(const int *offsets, int E, int P, int t, int lane) {
-    int done = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        int b = 0, c = 0;
-        if (e0 + lane < E) {
-            b = min(max(offsets[e0 + lane], 0), P);
-            c = max(min(offsets[e0 + lane + 1], P) - b, 0);
-        }
-        const int tiles = (c + TM - 1) / TM;
-        int incl = tiles;
+struct Tiles {
+    const int *offsets;
+    int E, P, lane;
+    int first[4], count[4], before;  // of the 256 experts from e0; before: tiles of this lane's predecessors
+    int sum;                         // tiles of these 256 experts
+
+    __device__ __forceinline__ void load(int e0) {
+        int o[5];
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(incl, o);
-            incl += lane >= o ? up : 0;
+        for (int i = 0; i < 5; ++i) o[i] = min(max(offsets[min(e0 + 4 * lane + i, E)], 0), P);
+        int own = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            first[i] = o[i];
+            count[i] = max(o[i + 1] - o[i], 0);
+            own += (count[i] + TM - 1) / TM;
         }
-        const uint64_t past = __ballot(done + incl > t);
-        if (past != 0) {
-            const int owner = __builtin_ctzll(past);
-            const int begin = __builtin_amdgcn_readlane(b, owner), all = __builtin_amdgcn_readlane(c, owner);
-            const int at = t - done - (__builtin_amdgcn_readlane(incl, owner) - __builtin_amdgcn_readlane(tiles, owner));
-            return {e0 + owner, begin + at * TM, min(TM, all - at * TM)};
-        }
-        done += __builtin_amdgcn_readlane(incl, 63);
+        int v = own;  // inclusive scan: within rows of 16 lanes, then across them
+        v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+        v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+        v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+        v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+        v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+        v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+        before = v - own;
+        sum = __builtin_amdgcn_readlane(v, 63);
     }
-    return {0, 0, 0};
-}
+
+    __device__ __forceinline__ Tiles(const int *off, int experts, int pairs, int ln)
+        : offsets(off), E(experts), P(pairs), lane(ln) {
+        load(0);
+    }
+
+    // Tiles of all experts.  Leaves the first 256 experts loaded.
+    __device__ __forceinline__ int total() {
+        if (E <= 256) return sum;
+        int n = 0;
+        for (int e0 = (E - 1) / 256 * 256; e0 >= 0; e0 -= 256) {
+            load(e0);
+            n += sum;
+        }
+        return n;
+    }
+
+    // Tile number t (count 0: there is none); the first 256 experts are loaded.
+    __device__ __forceinline__ Tile find(int t) {
+        for (int e0 = 0;;) {
+            if (t < sum) {
+                // the last lane with before <= t owns it
+                const int owner = 63 - __builtin_clzll(__ballot(before <= t));
+                int at = t - __builtin_amdgcn_readlane(before, owner);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = __builtin_amdgcn_readlane(count[i], owner), n = (c + TM - 1) / TM;
+                    if (at < n)
+                        return {e0 + 4 * owner + i, __builtin_amdgcn_readlane(first[i], owner) + at * TM,
+                                min(TM, c - at * TM)};
+                    at -= n;
+                }
+            }
+            t -= sum;
+            e0 += 256;
+            if (e0 >= E) return {0, 0, 0};
+            load(e0);
+        }
+    }
+};
 
 // One lane's part of one super-block of its row of W.
 struct WBlock {
@@ -194,123 +256,32 @@ __device__ __forceinline__ WScales block_scales(const uint4 hd, int quarter) {
     return s;
 }
 
-// The operands of steps 2i (low nibbles) and 2i + 1 (high) from two dwords.
+// The operand of step 2i + h (h = 0: low nibbles, 1: high) from two dwords.
 __device__ __forceinline__ half2v scaled(uint32_t bits, half2v s) { return __builtin_bit_cast(half2v, bits) * s; }
 __device__ __forceinline__ half8 join(half2v a, half2v b, half2v c, half2v d) {
     return half8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
-__device__ __forceinline__ void operands(uint32_t u, uint32_t v, const WScales &s, half8 &low, half8 &high) {
-    const uint32_t LM = 0x000F000Fu, HM = 0x00F000F0u;
-    const uint32_t u8 = u >> 8, v8 = v >> 8;
-    low = join(scaled(u & LM, s.s0), scaled(u8 & LM, s.s0), scaled(v & LM, s.s0), scaled(v8 & LM, s.s0));
-    high = join(scaled(u & HM, s.s1), scaled(u8 & HM, s.s1), scaled(v & HM, s.s1), scaled(v8 & HM, s.s1));
-}
-
-// The operand of one of the two steps.
-__device__ __forceinline__ void operand(uint32_t u, uint32_t v, const WScales &s, int h, half8 &op) {
+__device__ __forceinline__ half8 operand(uint32_t u, uint32_t v, const WScales &s, int h) {
     const uint32_t mask = h ? 0x00F000F0u : 0x000F000Fu;
     const half2v sc = h ? s.s1 : s.s0;
-    op = join(scaled(u & mask, sc), scaled((u >> 8) & mask, sc), scaled(v & mask, sc), scaled((v >> 8) & mask, sc));
+    return join(scaled(u & mask, sc), scaled((u >> 8) & mask, sc), scaled(v & mask, sc), scaled((v >> 8) & mask, sc));
 }
 
 __device__ __forceinline__ float4v mfma(half8 a, half8 b, float4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// 16 rows of x times 32 rows of W (SwiGLU: 16 gate and the same 16 up rows)
-// per wave, four waves side by side; operands straight from memory.
-template <bool kSwiglu>
-__global__ __launch_bounds__(256) void grouped_kernel(Grouped g) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, quarter = lane >> 4;
-    const Tile t = find_tile<16>(g.offsets, g.E, g.P, blockIdx.y, lane);
-    if (t.count == 0) return;
-    constexpr int kWaveN = kSwiglu ? 16 : 32;
-    const int n0 = (blockIdx.x * 4 + wave) * kWaveN;
-    if (n0 >= g.N) return;
-    const int KB = g.K / kBlockWeights;
-    const size_t row_bytes = static_cast<size_t>(KB) * kBlockBytes;
-    const uint8_t *wrow[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int n = min(n0 + (kSwiglu ? 0 : 16 * c) + c16, g.N - 1);
-        wrow[c] = (kSwiglu && c ? g.w2 : g.w) + (static_cast<size_t>(t.e) * g.N + n) * row_bytes;
-    }
-    // this lane's row of x as the A operand: row c16 of the tile (the last one again behind the end)
-    const auto pair_at = [&](int i) {
-        const int at = t.first + min(i, t.count - 1);
-        return g.rows ? g.rows[at] : at;
-    };
-    int pair = pair_at(c16);
-    pair = static_cast<unsigned>(pair) < static_cast<unsigned>(g.P) ? pair : 0;
-    const size_t xr = pair / g.x_div;
-    const uint8_t *img = g.x.img + xr * KB * kImageBlock + quarter * 16;
-    const uint8_t *sums = g.x.sums + xr * KB * kSumsBlock + (quarter & 1) * 16;
-    float4v acc[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
-    for (int b = 0; b < KB; ++b) {
-        WBlock wb[2];
-        WScales ws[2];
-        float4v blk[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            wb[c] = load_block(wrow[c], b, quarter);
-            blk[c] = float4v{0.f, 0.f, 0.f, 0.f};
-        }
-        half8 a[16];
-#pragma unroll
-        for (int s = 0; s < 16; ++s) a[s] = *reinterpret_cast<const half8 *>(img + b * kImageBlock + s * 64);
-        const uint4 sm = *reinterpret_cast<const uint4 *>(sums + b * kSumsBlock);
-        const half8 am = __builtin_bit_cast(half8, quarter < 2 ? sm : uint4{0, 0, 0, 0});
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            ws[c] = block_scales(wb[c].head, quarter);
-            const uint32_t q[8] = {wb[c].q0.x, wb[c].q0.y, wb[c].q0.z, wb[c].q0.w,
-                                   wb[c].q1.x, wb[c].q1.y, wb[c].q1.z, wb[c].q1.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                half8 low, high;
-                operands(q[2 * i], q[2 * i + 1], ws[c], low, high);
-                blk[c] = mfma(a[4 * i + 0], low, blk[c]);
-                blk[c] = mfma(a[4 * i + 1], low, blk[c]);
-                blk[c] = mfma(a[4 * i + 2], high, blk[c]);
-                blk[c] = mfma(a[4 * i + 3], high, blk[c]);
-            }
-            const float4v cm = mfma(am, ws[c].mins, float4v{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                acc[c][r] = __builtin_fmaf(ws[c].nm, cm[r], __builtin_fmaf(ws[c].d, blk[c][r], acc[c][r]));
-        }
-    }
-    // lane l holds rows 4 * (l / 16) + r of the tile for column l % 16
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int i = 4 * quarter + r;
-        const int p = pair_at(i);
-        if (i >= t.count || static_cast<unsigned>(p) >= static_cast<unsigned>(g.P)) continue;
-        const float back = g.x.back[p / g.x_div];
-        float *yr = g.y + static_cast<size_t>(p) * g.N;
-        if (kSwiglu) {
-            if (n0 + c16 < g.N) yr[n0 + c16] = swiglu(acc[0][r] * back, acc[1][r] * back);
-        } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (n0 + 16 * c + c16 < g.N) yr[n0 + 16 * c + c16] = acc[c][r] * back;
-        }
-    }
-}
-
 // ---- many rows per expert: tiles of RT * 16 rows times 256 columns ----------
 
 // LDS of a workgroup: two buffers of x (a quarter of a super-block: two steps,
 // 256 bytes a row), two of its sub-block sums, one super-block of each wave's
-// own 64 rows of W, and the tile's pair numbers.
-template <int RT>
+// own rows of W, and the tile's pairs and factors.
+template <int RT, int NC>
 struct TileLds {
     static constexpr int kRows = RT * 16;
-    static constexpr int kX = kRows * 256, kSums = kRows * kSumsBlock, kW = 64 * kBlockBytes;
+    static constexpr int kX = kRows * 256, kSums = kRows * kSumsBlock, kW = 16 * NC * kBlockBytes;
     static constexpr int kSumsAt = 2 * kX, kWAt = kSumsAt + 2 * kSums, kPairsAt = kWAt + 4 * kW;
-    static constexpr int kBytes = kPairsAt + kRows * 4;
+    static constexpr int kBackAt = kPairsAt + kRows * 4, kBytes = kBackAt + kRows * 4;
 };
 
 typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
@@ -345,35 +316,123 @@ __device__ __forceinline__ rsrc_t buffer_at(const uint8_t *p, uint32_t bytes) {
     return r;
 }
 
-// At most VM vector-memory operations of this wave outstanding and no LDS
-// operation, then the workgroup's barrier.
-template <int VM>
-__device__ __forceinline__ void wait_and_barrier() {
+// Every copy and LDS operation of this wave has ended.
+__device__ __forceinline__ void wait_all() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (VM & 15));
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    asm volatile("" ::: "memory");
+}
+// Every LDS operation of this wave has ended (copies may be on their way).
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+}
+// The same for the whole workgroup.
+__device__ __forceinline__ void wait_and_barrier() {
+    wait_all();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-template <int RT, bool kSwiglu>
+// A wave's 16 NC rows of W, copied to its own LDS slot one super-block at a
+// time, 144 bytes a row: two halves of 8 NC rows (SwiGLU: gate and up), row
+// 16c + r of the slot being column r of the wave's column tile c.  Rows behind
+// N read zeros.
+template <int NC, bool kSwiglu>
+struct WTile {
+    static constexpr int kHalfRows = 8 * NC, kPieces = 9 * kHalfRows, kCopies = (kPieces + 63) / 64;
+    static constexpr int kLast = kPieces - 64 * (kCopies - 1);  // lanes of the last copy
+    static constexpr int kBytes = 2 * kPieces * 16;
+    static constexpr int kN = kSwiglu ? 8 * NC : 16 * NC;  // outputs of a wave
+    uint32_t off[kCopies];
+    rsrc_t buf[2];
+    uint32_t lds;
+    int lane;
+
+    __device__ __forceinline__ WTile(const Grouped &g, int e, int n0, uint8_t *slot, int ln)
+        : lds(lds_address(slot)), lane(ln) {
+        const uint32_t row_bytes = static_cast<uint32_t>(g.K / kBlockWeights) * kBlockBytes;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) {
+            const int piece = k * 64 + lane, j = piece / 9;
+            off[k] = j * row_bytes + (piece - 9 * j) * 16;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int first = min(n0 + (kSwiglu ? 0 : kHalfRows * h), g.N), rows = min(kHalfRows, g.N - first);
+            buf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(e) * g.N + first) * row_bytes,
+                               rows * row_bytes);
+        }
+    }
+    __device__ __forceinline__ void copy(int b) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < kCopies; ++k)
+                if (k < kCopies - 1 || lane < kLast)
+                    copy_to_lds(buf[h], off[k], b * kBlockBytes, lds + h * (kPieces * 16) + k * 1024);
+    }
+};
+
+// The address of workgroup `id` in the work of `tiles` row tiles times n_tiles
+// column tiles (-1: none).  Workgroups go to the eight XCDs in turn: each XCD
+// takes one contiguous eighth of the work, column tiles fastest, so that the
+// workgroups that share rows of x or an expert's matrix share an L2.
+__device__ __forceinline__ int place_in_work(unsigned id, int tiles, int n_tiles) {
+    const int64_t work = static_cast<int64_t>(tiles) * n_tiles, per = (work + 7) / 8;
+    const int64_t at = (id & 7) * per + (id >> 3);
+    return (id >> 3) >= per || at >= work ? -1 : static_cast<int>(at);
+}
+
+// The tile's pairs (-1: entries outside [0, P)) and the factors of their rows.
+__device__ __forceinline__ void load_pairs(const Grouped &g, const Tile &t, int rows, int *pairs, float *back) {
+    const int i = threadIdx.x;
+    if (i < rows) {
+        const int at = t.first + min(i, t.count - 1);
+        const int p = g.rows ? g.rows[at] : at;
+        const bool valid = static_cast<unsigned>(p) < static_cast<unsigned>(g.P);
+        pairs[i] = valid ? p : -1;
+        back[i] = g.x.back[(valid ? p : 0) / g.x_div];
+    }
+}
+
+// Writes row i of the tile's columns: acc[c] for column n0 + 16c + c16
+// (SwiGLU: tiles 0 .. NC / 2 - 1 gate, the others up).
+template <int NC, bool kSwiglu>
+__device__ __forceinline__ void store_row(const Grouped &g, int p, float back, int n0, int c16, const float acc[NC]) {
+    float *yr = g.y + static_cast<size_t>(p) * g.N;
+    constexpr int kOut = kSwiglu ? NC / 2 : NC;
+#pragma unroll
+    for (int c = 0; c < kOut; ++c) {
+        const float v = acc[c] * back;
+        const float out = kSwiglu ? swiglu(v, acc[(c + kOut) % NC] * back) : v;
+        if (n0 + 16 * c + c16 < g.N) yr[n0 + 16 * c + c16] = out;
+    }
+}
+
+template <int RT, int NC, bool kSwiglu>
 __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
-    using L = TileLds<RT>;
+    using L = TileLds<RT, NC>;
+    using W = WTile<NC, kSwiglu>;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, quarter = lane >> 4;
-    const Tile t = find_tile<L::kRows>(g.offsets, g.E, g.P, blockIdx.y, lane);
+    Tiles<L::kRows> tiles(g.offsets, g.E, g.P, lane);
+    const int n_tiles = (g.N - 1) / (4 * W::kN) + 1;
+    const int at = place_in_work(blockIdx.x, tiles.total(), n_tiles);
+    if (at < 0) return;
+    const Tile t = tiles.find(at / n_tiles);
     if (t.count == 0) return;
+    const int n0 = (at % n_tiles * 4 + wave) * W::kN;
+    uint8_t *const wslot = lds + L::kWAt + wave * L::kW;
+    const W w(g, t.e, n0, wslot, lane);
+    w.copy(0);
     int *pairs = reinterpret_cast<int *>(lds + L::kPairsAt);
-    if (threadIdx.x < L::kRows) {
-        const int at = t.first + min(static_cast<int>(threadIdx.x), t.count - 1);
-        const int p = g.rows ? g.rows[at] : at;
-        pairs[threadIdx.x] = static_cast<unsigned>(p) < static_cast<unsigned>(g.P) ? p : -1;
-    }
+    float *back = reinterpret_cast<float *>(lds + L::kBackAt);
+    load_pairs(g, t, L::kRows, pairs, back);
     __syncthreads();
     const int KB = g.K / kBlockWeights;
-    const size_t row_bytes = static_cast<size_t>(KB) * kBlockBytes;
-    constexpr int kWaveN = kSwiglu ? 32 : 64;
-    const int n0 = (blockIdx.x * 4 + wave) * kWaveN;
 
     // x: this wave copies rows 4 RT wave .. + 4 RT of the tile, four per
     // instruction; a row's 16-byte pieces are exchanged by its number (piece c
@@ -390,24 +449,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
         const size_t xr = max(pairs[wave * RT * 4 + (lane >> 1)], 0) / g.x_div;
         ssrc += xr * KB * kSumsBlock + (lane & 1) * 16;
     }
-    // W: two halves of 32 rows, 288 pieces of 16 bytes each (4.5 instructions);
-    // row 16c + r of the wave's 64 is column r of its tile c (SwiGLU: the
-    // halves are gate and up).  Rows behind N read zeros.
-    uint32_t woff[5];
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-        const int piece = k * 64 + lane, j = piece / 9, part = piece - 9 * j;
-        woff[k] = j * static_cast<uint32_t>(row_bytes) + part * 16;
-    }
-    rsrc_t wbuf[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int first = min(n0 + (kSwiglu ? 0 : 32 * h), g.N), rows = min(32, g.N - first);
-        wbuf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(t.e) * g.N + first) * row_bytes,
-                            rows * static_cast<uint32_t>(row_bytes));
-    }
-    uint8_t *const wlds = lds + L::kWAt + wave * L::kW;
-    const uint32_t lds0 = lds_address(lds), wlds0 = lds0 + L::kWAt + wave * L::kW;
+    const uint32_t lds0 = lds_address(lds);
     const auto copy_x = [&](int b, int i, int buf) {
 #pragma unroll
         for (int j = 0; j < RT; ++j)
@@ -417,29 +459,20 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
         if (lane < RT * 8)
             copy_to_lds(ssrc + static_cast<size_t>(b) * kSumsBlock, lds0 + L::kSumsAt + (b & 1) * L::kSums + wave * RT * 128);
     };
-    const auto copy_w = [&](int b) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < 5; ++k)
-                if (k < 4 || lane < 32)
-                    copy_to_lds(wbuf[h], woff[k], b * kBlockBytes, wlds0 + h * (L::kW / 2) + k * 1024);
-    };
-    float4v acc[RT][4];
+    float4v acc[RT][NC];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
-    copy_w(0);
+        for (int c = 0; c < NC; ++c) acc[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
     copy_x(0, 0, 0);
     copy_sums(0);
     for (int b = 0; b < KB; ++b) {
-        WScales ws[4];
-        float4v blk[RT][4];
+        WScales ws[NC];
+        float4v blk[RT][NC];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             // x of this quarter has arrived; the others' too behind the barrier
-            wait_and_barrier<0>();
+            wait_and_barrier();
             if (i < 3) copy_x(b, i + 1, (i + 1) & 1);
             else if (b + 1 < KB) {
                 copy_x(b + 1, 0, 0);
@@ -454,9 +487,9 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
                     am[r] = __builtin_bit_cast(half8, quarter < 2 ? s : uint4{0, 0, 0, 0});
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < NC; ++c) {
                     __builtin_amdgcn_sched_barrier(0);
-                    ws[c] = block_scales(*reinterpret_cast<const uint4 *>(wlds + (c * 16 + c16) * kBlockBytes), quarter);
+                    ws[c] = block_scales(*reinterpret_cast<const uint4 *>(wslot + (c * 16 + c16) * kBlockBytes), quarter);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         const float4v cm = mfma(am[r], ws[c].mins, float4v{0.f, 0.f, 0.f, 0.f});
@@ -466,15 +499,14 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
                     }
                 }
             }
-            uint2 q[4];
+            uint2 q[NC];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                q[c] = *reinterpret_cast<const uint2 *>(wlds + (c * 16 + c16) * kBlockBytes + 16 + 32 * quarter + 8 * i);
+            for (int c = 0; c < NC; ++c)
+                q[c] = *reinterpret_cast<const uint2 *>(wslot + (c * 16 + c16) * kBlockBytes + 16 + 32 * quarter + 8 * i);
             if (i == 3 && b + 1 < KB) {
                 // every read of this wave's W slot has returned: refill it
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_s_waitcnt(0xC07F);
-                copy_w(b + 1);
+                wait_lds();
+                w.copy(b + 1);
             }
             const uint8_t *xb = lds + (i & 1) * L::kX;
 #pragma unroll
@@ -488,9 +520,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
                         a[r][part] = *reinterpret_cast<const half8 *>(
                             xb + (r * 16 + c16) * 256 + (((h * 2 + part) * 4 + quarter) ^ c16) * 16);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    half8 op;
-                    operand(q[c].x, q[c].y, ws[c], h, op);
+                for (int c = 0; c < NC; ++c) {
+                    const half8 op = operand(q[c].x, q[c].y, ws[c], h);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) blk[r][c] = mfma(a[r][0], op, blk[r][c]);
 #pragma unroll
@@ -499,7 +530,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
             }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -509,22 +540,131 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int i = r * 16 + 4 * quarter + k;
-            const int p = pairs[i];
+            const int i = r * 16 + 4 * quarter + k, p = pairs[i];
             if (i >= t.count || p < 0) continue;
-            const float back = g.x.back[p / g.x_div];
-            float *yr = g.y + static_cast<size_t>(p) * g.N;
-            if (kSwiglu) {
+            float v[NC];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (n0 + 16 * c + c16 < g.N)
-                        yr[n0 + 16 * c + c16] = swiglu(acc[r][c][k] * back, acc[r][2 + c][k] * back);
-            } else {
+            for (int c = 0; c < NC; ++c) v[c] = acc[r][c][k];
+            store_row<NC, kSwiglu>(g, p, back[i], n0, c16, v);
+        }
+}
+
+// ---- up to about sixteen rows per expert ---------------------------------------
+
+// One row tile of 16: here the stream of W sets the pace.  x comes a whole
+// super-block at a time (double buffered), W moves to registers at the start
+// of a super-block and its slot is refilled at once, so that copies are on
+// their way during all of the arithmetic, with one barrier per super-block.
+template <int NC>
+struct ThinLds {
+    static constexpr int kX = 16 * kImageBlock, kSums = 16 * kSumsBlock, kW = 16 * NC * kBlockBytes;
+    static constexpr int kSumsAt = 2 * kX, kWAt = kSumsAt + 2 * kSums, kPairsAt = kWAt + 4 * kW;
+    static constexpr int kBackAt = kPairsAt + 64, kBytes = kBackAt + 64;
+};
+
+template <int NC, bool kSwiglu>
+__global__ __launch_bounds__(256, 2) void thin_kernel(Grouped g) {
+    using L = ThinLds<NC>;
+    using W = WTile<NC, kSwiglu>;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c16 = lane & 15, quarter = lane >> 4;
+    Tiles<16> tiles(g.offsets, g.E, g.P, lane);
+    const int n_tiles = (g.N - 1) / (4 * W::kN) + 1;
+    const int at = place_in_work(blockIdx.x, tiles.total(), n_tiles);
+    if (at < 0) return;
+    const Tile t = tiles.find(at / n_tiles);
+    if (t.count == 0) return;
+    const int n0 = (at % n_tiles * 4 + wave) * W::kN;
+    uint8_t *const wslot = lds + L::kWAt + wave * L::kW;
+    const W w(g, t.e, n0, wslot, lane);
+    w.copy(0);
+    int *pairs = reinterpret_cast<int *>(lds + L::kPairsAt);
+    float *back = reinterpret_cast<float *>(lds + L::kBackAt);
+    load_pairs(g, t, 16, pairs, back);
+    __syncthreads();
+    const int KB = g.K / kBlockWeights;
+    // x: this wave copies rows 4 wave .. + 4, a row's 1024 bytes in one
+    // instruction, its pieces exchanged by the row's number as in tile_kernel
+    const uint8_t *xsrc[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (n0 + 16 * c + c16 < g.N) yr[n0 + 16 * c + c16] = acc[r][c][k] * back;
+    for (int j = 0; j < 4; ++j) {
+        const int row = wave * 4 + j;
+        const size_t xr = max(pairs[row], 0) / g.x_div;
+        xsrc[j] = g.x.img + xr * KB * kImageBlock + ((lane ^ row) * 16);
+    }
+    const uint8_t *ssrc = g.x.sums;
+    if (lane < 8) {
+        const size_t xr = max(pairs[wave * 4 + (lane >> 1)], 0) / g.x_div;
+        ssrc += xr * KB * kSumsBlock + (lane & 1) * 16;
+    }
+    const uint32_t lds0 = lds_address(lds);
+    const auto copy_x = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            copy_to_lds(xsrc[j] + static_cast<size_t>(b) * kImageBlock, lds0 + (b & 1) * L::kX + (wave * 4 + j) * 1024);
+        if (lane < 8)
+            copy_to_lds(ssrc + static_cast<size_t>(b) * kSumsBlock, lds0 + L::kSumsAt + (b & 1) * L::kSums + wave * 128);
+    };
+    float4v acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
+    copy_x(0);
+    for (int b = 0; b < KB; ++b) {
+        wait_and_barrier();
+        WBlock wb[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) wb[c] = load_block(wslot + (c * 16 + c16) * kBlockBytes, 0, quarter);
+        if (b + 1 < KB) {
+            wait_lds();  // W is in registers
+            w.copy(b + 1);
+            copy_x(b + 1);  // the other buffer, which every wave has left
+        }
+        WScales ws[NC];
+        float4v blk[NC];
+        const uint4 s = *reinterpret_cast<const uint4 *>(lds + L::kSumsAt + (b & 1) * L::kSums + c16 * kSumsBlock + (quarter & 1) * 16);
+        const half8 am = __builtin_bit_cast(half8, quarter < 2 ? s : uint4{0, 0, 0, 0});
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            ws[c] = block_scales(wb[c].head, quarter);
+            const float4v cm = mfma(am, ws[c].mins, float4v{0.f, 0.f, 0.f, 0.f});
+            blk[c] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[c][k] = __builtin_fmaf(ws[c].nm, cm[k], acc[c][k]);
+        }
+        const uint8_t *xb = lds + (b & 1) * L::kX + c16 * 1024;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // the operands of one pair of steps in registers at a time
+            half8 a[4];
+#pragma unroll
+            for (int s4 = 0; s4 < 4; ++s4)
+                a[s4] = *reinterpret_cast<const half8 *>(xb + (((4 * i + s4) * 4 + quarter) ^ c16) * 16);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const uint4 qq = i < 2 ? wb[c].q0 : wb[c].q1;
+                const uint32_t u = i & 1 ? qq.z : qq.x, v = i & 1 ? qq.w : qq.y;
+                const half8 low = operand(u, v, ws[c], 0), high = operand(u, v, ws[c], 1);
+                blk[c] = mfma(a[0], low, blk[c]);
+                blk[c] = mfma(a[1], low, blk[c]);
+                blk[c] = mfma(a[2], high, blk[c]);
+                blk[c] = mfma(a[3], high, blk[c]);
             }
         }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[c][k] = __builtin_fmaf(ws[c].d, blk[c][k], acc[c][k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = 4 * quarter + k, p = pairs[i];
+        if (i >= t.count || p < 0) continue;
+        float v[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) v[c] = acc[c][k];
+        store_row<NC, kSwiglu>(g, p, back[i], n0, c16, v);
+    }
 }
 
 // ---- few rows per expert -----------------------------------------------------
@@ -593,41 +733,18 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, quarter = lane >> 4;
-    const Tile t = find_tile<kFewRows>(g.offsets, g.E, g.P, blockIdx.y, lane);
+    const Tile t = Tiles<kFewRows>(g.offsets, g.E, g.P, lane).find(blockIdx.y);
     if (t.count == 0) return;
     const auto pair_at = [&](int i) {
         const int at = t.first + min(i, t.count - 1);
         return g.rows ? g.rows[at] : at;
     };
     const int KB = g.K / kBlockWeights;
-    const size_t row_bytes = static_cast<size_t>(KB) * kBlockBytes;
-    constexpr int kTileN = kSwiglu ? 16 : 32;
-    const int n0 = blockIdx.x * kTileN;
+    using W = WTile<2, kSwiglu>;
+    const int n0 = blockIdx.x * W::kN;
     uint8_t *const base = lds + wave * FewLds::kWave;
-    const uint32_t wlds = lds_address(base);
-    // two halves of 16 rows (SwiGLU: gate and up), 144 pieces of 16 bytes each
-    uint32_t woff[3];
-    rsrc_t wbuf[2];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const int piece = k * 64 + lane, j = piece / 9, part = piece - 9 * j;
-        woff[k] = j * static_cast<uint32_t>(row_bytes) + part * 16;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int first = min(n0 + (kSwiglu ? 0 : 16 * h), g.N), rows = min(16, g.N - first);
-        wbuf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(t.e) * g.N + first) * row_bytes,
-                            rows * static_cast<uint32_t>(row_bytes));
-    }
-    const auto copy_w = [&](int b) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (k < 2 || lane < 16)
-                    copy_to_lds(wbuf[h], woff[k], b * kBlockBytes, wlds + h * (FewLds::kW / 2) + k * 1024);
-    };
-    if (wave < KB) copy_w(wave);
+    const W w(g, t.e, n0, base, lane);
+    if (wave < KB) w.copy(wave);
     // lane 16r + p reads values 16p .. of row r (the last row again behind the end)
     int pair = pair_at(quarter);
     pair = static_cast<unsigned>(pair) < static_cast<unsigned>(g.P) ? pair : 0;
@@ -642,16 +759,13 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
     const int arow = min(c16, kFewRows - 1);
     for (int b = wave; b < KB; b += WAVES) {
         stage_few(xv, lane, base);
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);  // W has arrived, x is staged (both this wave's own)
-        asm volatile("" ::: "memory");
+        wait_all();  // W has arrived, x is staged (both this wave's own)
         WBlock wb[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) wb[c] = load_block(base + (c * 16 + c16) * kBlockBytes, 0, quarter);
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // W is in registers: its slot may be filled again
+        wait_lds();  // W is in registers: its slot may be filled again
         if (b + WAVES < KB) {
-            copy_w(b + WAVES);
+            w.copy(b + WAVES);
             load_x(b + WAVES);
         }
         WScales ws[2];
@@ -675,9 +789,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
             for (int c = 0; c < 2; ++c) {
                 const uint4 qq = i < 2 ? wb[c].q0 : wb[c].q1;
                 const uint32_t u = i & 1 ? qq.z : qq.x, v = i & 1 ? qq.w : qq.y;
-                half8 low, high;
-                operand(u, v, ws[c], 0, low);
-                operand(u, v, ws[c], 1, high);
+                const half8 low = operand(u, v, ws[c], 0), high = operand(u, v, ws[c], 1);
                 blk[c][0] = mfma(a[0], low, blk[c][0]);
                 blk[c][1] = mfma(a[2], high, blk[c][1]);
                 blk[c][0] = mfma(a[1], low, blk[c][0]);
@@ -705,7 +817,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
     }
     __syncthreads();
     if (threadIdx.x >= 128) return;
-    const int c = threadIdx.x >> 6, r = (threadIdx.x >> 4) & 3;
+    const int c = threadIdx.x >> 6, r = (threadIdx.x >> 4) & 3;  // column tile and row of this thread's output
     if ((kSwiglu && c) || r >= t.count) return;
     const int p = pair_at(r);
     const int n = n0 + 16 * c + c16;
@@ -721,19 +833,44 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
 }
 
 // out[m, n] = sum_j weight[m, j] * y[m * top_k + j, n] over the choices with a
-// valid expert, in ascending j.
+// valid expert, in ascending j; a thread holds four columns and requests eight
+// choices' values before it adds the first.
+typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));  // rows of odd N start anywhere
 __global__ __launch_bounds__(256) void combine_kernel(const float *y, const int *expert, const float *weight,
-                                                      float *out, int E, int top_k, int N) {
-    const int m = blockIdx.y;
-    const int n = blockIdx.x * 256 + threadIdx.x;
+                                                      float *out, int E, int M, int top_k, int N) {
+    const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
     if (n >= N) return;
-    float acc = 0.f;
-    for (int j = 0; j < top_k; ++j) {
-        const size_t p = static_cast<size_t>(m) * top_k + j;
-        if (static_cast<unsigned>(expert[p]) >= static_cast<unsigned>(E)) continue;
-        acc = __builtin_fmaf(weight[p], y[p * N + n], acc);
+    for (int m = blockIdx.y; m < M; m += gridDim.y) {
+        float4u acc = {0.f, 0.f, 0.f, 0.f};
+        const size_t p0 = static_cast<size_t>(m) * top_k;
+        for (int j0 = 0; j0 < top_k; j0 += 8) {
+            float4u v[8];
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const size_t p = p0 + min(j0 + i, top_k - 1);
+                const bool use = j0 + i < top_k && static_cast<unsigned>(expert[p]) < static_cast<unsigned>(E);
+                w[i] = use ? weight[p] : 0.f;
+                v[i] = float4u{0.f, 0.f, 0.f, 0.f};
+                if (use) {
+                    const float *src = y + p * N + n;
+                    if (n + 4 <= N) v[i] = *reinterpret_cast<const float4u *>(src);
+                    else
+                        for (int k = 0; k < 3; ++k)
+                            if (n + k < N) v[i][k] = src[k];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(w[i], v[i][k], acc[k]);
+        }
+        float *o = out + static_cast<size_t>(m) * N + n;
+        if (n + 4 <= N) *reinterpret_cast<float4u *>(o) = acc;
+        else
+            for (int k = 0; k < 3; ++k)
+                if (n + k < N) o[k] = acc[k];
     }
-    out[static_cast<size_t>(m) * N + n] = acc;
 }
 
 bool misaligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
@@ -755,7 +892,34 @@ int check_grouped(const void *w, const void *w2, const float *x, int x_div, cons
     return Q4K_OK;
 }
 
-bool few_rows(const Grouped &g) { return g.P <= 2 * g.E; }
+enum class Variant { kFew, kThin, kTile, kLargeTile };
+
+// The kernel for a call, from what the host knows (the groups' sizes are on
+// the device): P pairs over E experts, and the bytes of an expert's matrices.
+//   * Few rows: each tile of four rows streams its expert's matrix at about
+//     3.3 TB/s after 4.5 us; sixteen-row tiles stream it at about 4.2 TB/s, but
+//     after 11 us (two launches and deeper pipelines).  With at most
+//     min(E, P) experts in use and one more tile of four for every four pairs
+//     above one per expert, four-row tiles win while
+//     (1.27 tiles - experts) * bytes < 27 MB.  Both sides measured, 64 experts
+//     of 1024 x 2048 (SwiGLU): 1 token 7.5 / 14.8 us, 4 tokens 24.1 / 23.8 us,
+//     8 tokens 33.6 / 29.3 us; 8 experts of 1999 x 1280: 8 tokens 6.9 / 12.3 us,
+//     32 tokens 14.4 / 12.5 us.
+//   * Sixteen rows by 128 columns up to 16 pairs per expert, 32 by 128 above:
+//     at 8 per expert 29.6 / 29.4 us (16 experts of 4096 x 2048), at 24 38.9 /
+//     36.1 us, at 64 72.0 / 56.8 us.
+//   * 48 rows by 256 columns from 64 pairs per expert, where that still gives
+//     two workgroups to every CU: 64 experts of 1024 x 2048 (SwiGLU), 256 rows
+//     each, 310 against 330 us; 16 of 4096 x 2048, 48 rows each, 56.3 against 47.5 us.
+Variant choose(const Grouped &g) {
+    const double experts = g.E < g.P ? g.E : g.P, matrices = g.w2 ? 2 : 1;
+    const double bytes = matrices * g.N * (g.K / kBlockWeights) * kBlockBytes;
+    const double fours = experts + (g.P > g.E ? (g.P - g.E) / 4 : 0);
+    if (fours < 16384 && (1.27 * fours - experts) * bytes < 27e6) return Variant::kFew;
+    if (g.P < 16 * static_cast<int64_t>(g.E)) return Variant::kThin;
+    const double workgroups = (g.P / 48 + 0.5 * g.E) * (matrices * g.N / 256);
+    return g.P >= 64 * static_cast<int64_t>(g.E) && workgroups >= 512 ? Variant::kLargeTile : Variant::kTile;
+}
 
 template <int WAVES, bool kSwiglu>
 hipError_t launch_few(const Grouped &g, const float *x, hipStream_t stream) {
@@ -767,10 +931,34 @@ hipError_t launch_few(const Grouped &g, const float *x, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <class K>
+hipError_t launch_tiles(K kernel, const Grouped &g, int rows, int cols, int bytes, hipStream_t stream) {
+    const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes);
+    if (err != hipSuccess) return err;
+    const int64_t tiles = g.P / rows + (g.E < g.P ? g.E : g.P);
+    const int64_t blocks = (tiles * ((g.N - 1) / cols + 1) + 7) / 8 * 8;
+    if (blocks > INT_MAX) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), bytes, stream, g);
+    return hipGetLastError();
+}
+template <int RT, int NC>
+hipError_t launch_tile(const Grouped &g, hipStream_t stream) {
+    if (g.w2)
+        return launch_tiles(tile_kernel<RT, NC, true>, g, RT * 16, 4 * WTile<NC, true>::kN, TileLds<RT, NC>::kBytes, stream);
+    return launch_tiles(tile_kernel<RT, NC, false>, g, RT * 16, 4 * WTile<NC, false>::kN, TileLds<RT, NC>::kBytes, stream);
+}
+template <int NC>
+hipError_t launch_thin(const Grouped &g, hipStream_t stream) {
+    if (g.w2)
+        return launch_tiles(thin_kernel<NC, true>, g, 16, 4 * WTile<NC, true>::kN, ThinLds<NC>::kBytes, stream);
+    return launch_tiles(thin_kernel<NC, false>, g, 16, 4 * WTile<NC, false>::kN, ThinLds<NC>::kBytes, stream);
+}
+
 // Stages x, then the products.  g.x is filled in here.
 hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     const size_t xrows = (static_cast<size_t>(g.P) + g.x_div - 1) / g.x_div, KB = g.K / kBlockWeights;
-    if (few_rows(g)) {
+    const Variant variant = choose(g);
+    if (variant == Variant::kFew) {
         if (g.w2) return KB > 4 ? launch_few<8, true>(g, x, stream) : launch_few<4, true>(g, x, stream);
         return KB > 4 ? launch_few<8, false>(g, x, stream) : launch_few<4, false>(g, x, stream);
     }
@@ -780,26 +968,16 @@ hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     uint8_t *img = reinterpret_cast<uint8_t *>(ws), *sums = img + xrows * KB * kImageBlock;
     float *back = reinterpret_cast<float *>(sums + xrows * KB * kSumsBlock);
     g.x = {img, sums, back};
-    hipLaunchKernelGGL(stage_rows_kernel, dim3(static_cast<unsigned>(xrows)), dim3(256), 0, stream, x, g.K, img, sums,
-                       back);
+    const int threads = g.K >= 8 * kStageThreads ? kStageThreads : (g.K / 8 + 63) / 64 * 64;
+    hipLaunchKernelGGL(stage_rows_kernel, dim3(static_cast<unsigned>(xrows)), dim3(threads), 0, stream, x, g.K, img,
+                       sums, back);
     err = hipGetLastError();
     if (err != hipSuccess) return err;
-    if (g.P >= 24 * g.E) {
-        const int tiles = g.P / 48 + (g.E < g.P ? g.E : g.P);
-        const dim3 grid((g.N + (g.w2 ? 127 : 255)) / (g.w2 ? 128 : 256), tiles);
-        const void *k = g.w2 ? reinterpret_cast<const void *>(tile_kernel<3, true>) : reinterpret_cast<const void *>(tile_kernel<3, false>);
-        err = allow_dynamic_lds(k, TileLds<3>::kBytes);
-        if (err != hipSuccess) return err;
-        if (g.w2) hipLaunchKernelGGL((tile_kernel<3, true>), grid, dim3(256), TileLds<3>::kBytes, stream, g);
-        else hipLaunchKernelGGL((tile_kernel<3, false>), grid, dim3(256), TileLds<3>::kBytes, stream, g);
-        return hipGetLastError();
+    switch (variant) {
+    case Variant::kThin: return launch_thin<2>(g, stream);
+    case Variant::kTile: return launch_tile<2, 2>(g, stream);
+    default: return launch_tile<3, 4>(g, stream);
     }
-    const int tiles = g.P / 16 + (g.E < g.P ? g.E : g.P);
-    const int cols = g.w2 ? 64 : 128;
-    const dim3 grid((g.N + cols - 1) / cols, tiles);
-    if (g.w2) hipLaunchKernelGGL(grouped_kernel<true>, grid, dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL(grouped_kernel<false>, grid, dim3(256), 0, stream, g);
-    return hipGetLastError();
 }
 
 }  // namespace
@@ -846,7 +1024,7 @@ extern "C" int q4k_matmul_grouped_combine(const void *w_packed, const float *x, 
     hipError_t err = run_grouped({static_cast<const uint8_t *>(w_packed), nullptr, {}, offsets, rows, y, E, P, N, K, 1},
                                  x, stream);
     if (err != hipSuccess) return status(err);
-    hipLaunchKernelGGL(combine_kernel, dim3((N + 255) / 256, M), dim3(256), 0, stream, y, expert, weight, out, E,
-                       top_k, N);
+    hipLaunchKernelGGL(combine_kernel, dim3((N - 1) / 1024 + 1, M < 65535 ? M : 65535), dim3(256), 0, stream, y, expert,
+                       weight, out, E, M, top_k, N);
     return status(hipGetLastError());
 }
