@@ -328,9 +328,17 @@ __device__ __forceinline__ void wait_lds() {
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("" ::: "memory");
 }
-// The same for the whole workgroup.
-__device__ __forceinline__ void wait_and_barrier() {
-    wait_all();
+// All but the last VM copies of this wave, and every LDS operation, have ended.
+template <int VM>
+__device__ __forceinline__ void wait_copies() {
+    static_assert(VM < 16, "one field of the counter");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | VM);
+    asm volatile("" ::: "memory");
+}
+// The workgroup's barrier (what its waves have waited for is then there for all).
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -385,15 +393,21 @@ __device__ __forceinline__ int place_in_work(unsigned id, int tiles, int n_tiles
     return (id >> 3) >= per || at >= work ? -1 : static_cast<int>(at);
 }
 
-// The tile's pairs (-1: entries outside [0, P)) and the factors of their rows.
+// Pair i of the tile, the last one again behind its end; -1 for an entry
+// outside [0, P).
+__device__ __forceinline__ int pair_of(const Grouped &g, const Tile &t, int i) {
+    const int at = t.first + min(i, t.count - 1);
+    const int p = g.rows ? g.rows[at] : at;
+    return static_cast<unsigned>(p) < static_cast<unsigned>(g.P) ? p : -1;
+}
+
+// The tile's pairs and the factors of their rows.
 __device__ __forceinline__ void load_pairs(const Grouped &g, const Tile &t, int rows, int *pairs, float *back) {
     const int i = threadIdx.x;
     if (i < rows) {
-        const int at = t.first + min(i, t.count - 1);
-        const int p = g.rows ? g.rows[at] : at;
-        const bool valid = static_cast<unsigned>(p) < static_cast<unsigned>(g.P);
-        pairs[i] = valid ? p : -1;
-        back[i] = g.x.back[(valid ? p : 0) / g.x_div];
+        const int p = pair_of(g, t, i);
+        pairs[i] = p;
+        back[i] = g.x.back[max(p, 0) / g.x_div];
     }
 }
 
@@ -472,7 +486,8 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             // x of this quarter has arrived; the others' too behind the barrier
-            wait_and_barrier();
+            wait_all();
+            barrier();
             if (i < 3) copy_x(b, i + 1, (i + 1) & 1);
             else if (b + 1 < KB) {
                 copy_x(b + 1, 0, 0);
@@ -551,19 +566,22 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
 
 // ---- up to about sixteen rows per expert ---------------------------------------
 
-// One row tile of 16: here the stream of W sets the pace.  x comes a whole
-// super-block at a time (double buffered), W moves to registers at the start
-// of a super-block and its slot is refilled at once, so that copies are on
-// their way during all of the arithmetic, with one barrier per super-block.
+// One row tile of 16: here the stream of W sets the pace.  W moves to
+// registers at the start of a super-block and its slot is refilled at once, so
+// that copies are on their way during all of the arithmetic; x comes half a
+// super-block (512 bytes a row) at a time in two buffers.  That keeps a
+// workgroup within a quarter of the LDS, and four to a CU.  (Staging x inside
+// this kernel instead of by a launch of its own was slower: 32 against 29 us
+// for 48 x 8 rows over 64 experts of 2048 x 1024, 66 against 48 us at 128 x 8.)
 template <int NC>
 struct ThinLds {
-    static constexpr int kX = 16 * kImageBlock, kSums = 16 * kSumsBlock, kW = 16 * NC * kBlockBytes;
+    static constexpr int kX = 16 * kImageBlock / 2, kSums = 16 * kSumsBlock, kW = 16 * NC * kBlockBytes;
     static constexpr int kSumsAt = 2 * kX, kWAt = kSumsAt + 2 * kSums, kPairsAt = kWAt + 4 * kW;
     static constexpr int kBackAt = kPairsAt + 64, kBytes = kBackAt + 64;
 };
 
 template <int NC, bool kSwiglu>
-__global__ __launch_bounds__(256, 2) void thin_kernel(Grouped g) {
+__global__ __launch_bounds__(256, 4) void thin_kernel(Grouped g) {
     using L = ThinLds<NC>;
     using W = WTile<NC, kSwiglu>;
     extern __shared__ __align__(16) uint8_t lds[];
@@ -584,42 +602,45 @@ __global__ __launch_bounds__(256, 2) void thin_kernel(Grouped g) {
     load_pairs(g, t, 16, pairs, back);
     __syncthreads();
     const int KB = g.K / kBlockWeights;
-    // x: this wave copies rows 4 wave .. + 4, a row's 1024 bytes in one
-    // instruction, its pieces exchanged by the row's number as in tile_kernel
-    const uint8_t *xsrc[4];
+    // x: this wave copies rows 4 wave .. + 4, two per instruction, their pieces
+    // exchanged by the row's number as in tile_kernel
+    const uint8_t *xsrc[2], *ssrc = g.x.sums;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = wave * 4 + j;
+    for (int j = 0; j < 2; ++j) {
+        const int row = wave * 4 + j * 2 + (lane >> 5);
         const size_t xr = max(pairs[row], 0) / g.x_div;
-        xsrc[j] = g.x.img + xr * KB * kImageBlock + ((lane ^ row) * 16);
+        xsrc[j] = g.x.img + xr * KB * kImageBlock + (((lane & 31) ^ row) * 16);
     }
-    const uint8_t *ssrc = g.x.sums;
     if (lane < 8) {
         const size_t xr = max(pairs[wave * 4 + (lane >> 1)], 0) / g.x_div;
         ssrc += xr * KB * kSumsBlock + (lane & 1) * 16;
     }
     const uint32_t lds0 = lds_address(lds);
-    const auto copy_x = [&](int b) {
+    const auto copy_x = [&](int b, int half) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            copy_to_lds(xsrc[j] + static_cast<size_t>(b) * kImageBlock, lds0 + (b & 1) * L::kX + (wave * 4 + j) * 1024);
+        for (int j = 0; j < 2; ++j)
+            copy_to_lds(xsrc[j] + (static_cast<size_t>(b) * kImageBlock + half * (kImageBlock / 2)),
+                        lds0 + half * L::kX + (wave * 2 + j) * 1024);
+    };
+    const auto copy_sums = [&](int b) {
         if (lane < 8)
             copy_to_lds(ssrc + static_cast<size_t>(b) * kSumsBlock, lds0 + L::kSumsAt + (b & 1) * L::kSums + wave * 128);
     };
     float4v acc[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
-    copy_x(0);
+    copy_x(0, 0);
+    copy_sums(0);
     for (int b = 0; b < KB; ++b) {
-        wait_and_barrier();
+        wait_all();
+        barrier();
         WBlock wb[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) wb[c] = load_block(wslot + (c * 16 + c16) * kBlockBytes, 0, quarter);
-        if (b + 1 < KB) {
-            wait_lds();  // W is in registers
-            w.copy(b + 1);
-            copy_x(b + 1);  // the other buffer, which every wave has left
-        }
+        wait_lds();  // W is in registers
+        copy_x(b, 1);
+        const bool more = b + 1 < KB;
+        if (more) w.copy(b + 1);
         WScales ws[NC];
         float4v blk[NC];
         const uint4 s = *reinterpret_cast<const uint4 *>(lds + L::kSumsAt + (b & 1) * L::kSums + c16 * kSumsBlock + (quarter & 1) * 16);
@@ -632,14 +653,24 @@ __global__ __launch_bounds__(256, 2) void thin_kernel(Grouped g) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[c][k] = __builtin_fmaf(ws[c].nm, cm[k], acc[c][k]);
         }
-        const uint8_t *xb = lds + (b & 1) * L::kX + c16 * 1024;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            if (i == 2) {
+                // the second half of x, requested before W of the next block,
+                // which may stay on its way
+                if (more) wait_copies<2 * W::kCopies>();
+                else wait_all();
+                barrier();
+                if (more) {
+                    copy_x(b + 1, 0);
+                    copy_sums(b + 1);
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);  // the operands of one pair of steps in registers at a time
+            const uint8_t *xb = lds + (i >> 1) * L::kX + c16 * (kImageBlock / 2) + (i & 1) * 256;
             half8 a[4];
 #pragma unroll
-            for (int s4 = 0; s4 < 4; ++s4)
-                a[s4] = *reinterpret_cast<const half8 *>(xb + (((4 * i + s4) * 4 + quarter) ^ c16) * 16);
+            for (int s4 = 0; s4 < 4; ++s4) a[s4] = *reinterpret_cast<const half8 *>(xb + ((4 * s4 + quarter) ^ c16) * 16);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const uint4 qq = i < 2 ? wb[c].q0 : wb[c].q1;
@@ -735,10 +766,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
     const int c16 = lane & 15, quarter = lane >> 4;
     const Tile t = Tiles<kFewRows>(g.offsets, g.E, g.P, lane).find(blockIdx.y);
     if (t.count == 0) return;
-    const auto pair_at = [&](int i) {
-        const int at = t.first + min(i, t.count - 1);
-        return g.rows ? g.rows[at] : at;
-    };
     const int KB = g.K / kBlockWeights;
     using W = WTile<2, kSwiglu>;
     const int n0 = blockIdx.x * W::kN;
@@ -746,9 +773,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
     const W w(g, t.e, n0, base, lane);
     if (wave < KB) w.copy(wave);
     // lane 16r + p reads values 16p .. of row r (the last row again behind the end)
-    int pair = pair_at(quarter);
-    pair = static_cast<unsigned>(pair) < static_cast<unsigned>(g.P) ? pair : 0;
-    const float *xr = x + static_cast<size_t>(pair / g.x_div) * g.K + c16 * 16;
+    const float *xr = x + static_cast<size_t>(max(pair_of(g, t, quarter), 0) / g.x_div) * g.K + c16 * 16;
     float4 xv[4];
     const auto load_x = [&](int b) {
 #pragma unroll
@@ -819,9 +844,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
     if (threadIdx.x >= 128) return;
     const int c = threadIdx.x >> 6, r = (threadIdx.x >> 4) & 3;  // column tile and row of this thread's output
     if ((kSwiglu && c) || r >= t.count) return;
-    const int p = pair_at(r);
+    const int p = pair_of(g, t, r);
     const int n = n0 + 16 * c + c16;
-    if (n >= g.N || static_cast<unsigned>(p) >= static_cast<unsigned>(g.P)) return;
+    if (n >= g.N || p < 0) return;
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
