@@ -231,9 +231,9 @@ __device__ __forceinline__ WBlock load_block(const uint8_t *row, int b, int quar
 }
 
 struct WScales {
-    float d, nm;    // d, -64 * dmin
-    half2v s0, s1;  // the lane's two scales, the second / 16 (its nibbles are 16q)
-    half8 mins;     // m_0..m_7 as subnormals m * 2^-24
+    float d, nm;  // d, -64 * dmin
+    half2v s;     // the lane's two scales, the second / 16 (its nibbles are 16q)
+    half8 mins;   // m_0..m_7 as subnormals m * 2^-24
 };
 __device__ __forceinline__ WScales block_scales(const uint4 hd, int quarter) {
     WScales s;
@@ -242,16 +242,16 @@ __device__ __forceinline__ WScales block_scales(const uint4 hd, int quarter) {
     const uint32_t scA = hd.y & 0x3F3F3F3Fu, mnA = hd.z & 0x3F3F3F3Fu;
     const uint32_t scB = (hd.w & 0x0F0F0F0Fu) | ((hd.y >> 2) & 0x30303030u);
     const uint32_t mnB = ((hd.w >> 4) & 0x0F0F0F0Fu) | ((hd.z >> 2) & 0x30303030u);
-    const uint32_t two = (quarter & 2 ? scB : scA) >> (16 * (quarter & 1));
-    const _Float16 a = static_cast<_Float16>(static_cast<float>(two & 0xFFu));
-    const _Float16 b = static_cast<_Float16>(0.0625f * static_cast<float>((two >> 8) & 0xFFu));
-    s.s0 = half2v{a, a};
-    s.s1 = half2v{b, b};
-    uint4 m;
-    m.x = (mnA & 0xFFu) | ((mnA & 0xFF00u) << 8);
-    m.y = ((mnA >> 16) & 0xFFu) | ((mnA >> 8) & 0xFF0000u);
-    m.z = (mnB & 0xFFu) | ((mnB & 0xFF00u) << 8);
-    m.w = ((mnB >> 16) & 0xFFu) | ((mnB >> 8) & 0xFF0000u);
+    // bytes 2 quarter and 2 quarter + 1 of scA, scB as 16-bit lanes; 0x6400 |
+    // sc is the binary16 1024 + sc
+    const uint32_t two = __builtin_amdgcn_perm(scB, scA, 0x0C010C00u + 0x00020002u * quarter);
+    const half2v sc = __builtin_bit_cast(half2v, two | 0x64006400u) - half2v{1024, 1024};
+    s.s = sc * half2v{1, static_cast<_Float16>(0.0625f)};
+    uint4 m;  // bytes to 16-bit lanes
+    m.x = __builtin_amdgcn_perm(0u, mnA, 0x0C010C00u);
+    m.y = __builtin_amdgcn_perm(0u, mnA, 0x0C030C02u);
+    m.z = __builtin_amdgcn_perm(0u, mnB, 0x0C010C00u);
+    m.w = __builtin_amdgcn_perm(0u, mnB, 0x0C030C02u);
     s.mins = __builtin_bit_cast(half8, m);
     return s;
 }
@@ -263,7 +263,7 @@ __device__ __forceinline__ half8 join(half2v a, half2v b, half2v c, half2v d) {
 }
 __device__ __forceinline__ half8 operand(uint32_t u, uint32_t v, const WScales &s, int h) {
     const uint32_t mask = h ? 0x00F000F0u : 0x000F000Fu;
-    const half2v sc = h ? s.s1 : s.s0;
+    const half2v sc = h ? half2v{s.s.y, s.s.y} : half2v{s.s.x, s.s.x};
     return join(scaled(u & mask, sc), scaled((u >> 8) & mask, sc), scaled(v & mask, sc), scaled((v >> 8) & mask, sc));
 }
 
@@ -523,24 +523,23 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
                 wait_lds();
                 w.copy(b + 1);
             }
-            const uint8_t *xb = lds + (i & 1) * L::kX;
+            const uint8_t *xb = lds + (i & 1) * L::kX + c16 * 256;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 __builtin_amdgcn_sched_barrier(0);  // one step's operands in registers at a time
-                half8 a[RT][2];
+                half8 op[NC];
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+                for (int c = 0; c < NC; ++c) op[c] = operand(q[c].x, q[c].y, ws[c], h);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        a[r][part] = *reinterpret_cast<const half8 *>(
-                            xb + (r * 16 + c16) * 256 + (((h * 2 + part) * 4 + quarter) ^ c16) * 16);
+                for (int part = 0; part < 2; ++part) {
+                    half8 a[RT];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const half8 op = operand(q[c].x, q[c].y, ws[c], h);
+                    for (int r = 0; r < RT; ++r)
+                        a[r] = *reinterpret_cast<const half8 *>(xb + ((((h * 2 + part) * 4 + quarter) ^ c16) * 16) + r * 4096);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) blk[r][c] = mfma(a[r][0], op, blk[r][c]);
+                    for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) blk[r][c] = mfma(a[r][1], op, blk[r][c]);
+                        for (int r = 0; r < RT; ++r) blk[r][c] = mfma(a[r], op[c], blk[r][c]);
                 }
             }
         }
