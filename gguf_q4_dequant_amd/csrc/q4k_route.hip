@@ -73,89 +73,167 @@ __device__ __forceinline__ T wave_sum(T v) {
     return wave_reduce(v, static_cast<T>(0), [](T a, T b) { return a + b; });
 }
 
+// Floats as unsigned integers of the same order, all above 0 (-0 as +0), and back.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f + 0.f);
+    return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+    return __uint_as_float(o ^ (static_cast<uint32_t>(static_cast<int>(~o) >> 31) | 0x80000000u));
+}
+
+// The largest over the 64 lanes, uniform; one instruction a step, since 0 is
+// the identity of the unsigned maximum and what a move from outside reads.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t max_step(uint32_t v) {
+    const uint32_t o = __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xF, kRows == 0xF);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max_step<0x111, 0xF>(v);
+    v = max_step<0x112, 0xF>(v);
+    v = max_step<0x114, 0xF>(v);
+    v = max_step<0x118, 0xF>(v);
+    v = max_step<0x142, 0xA>(v);
+    v = max_step<0x143, 0xC>(v);
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
 // The softmax's numerator: 1 at the largest logit also where that is +inf.
 __device__ __forceinline__ float softmax_term(float l, float mx) { return l == mx ? 1.f : expf(l - mx); }
 __device__ __forceinline__ double softmax_term(double l, double mx) { return l == mx ? 1.0 : exp(l - mx); }
 
-// Routes one token; lane j < top_k ends with choice j.  T is float where the
-// logits themselves decide (no bias), else double.
-template <int VPL, class T>
+// Routes one token; lane j < top_k ends with choice j.
+//   Without a bias the logits decide, which needs no arithmetic.  With one the
+// scores do, and close scores have to be told apart: they are computed in
+// float32, whose error here is below 2^-19 + 2^-24 |score + bias| (of a score
+// of at most 1: an exponential and a quotient of a few 2^-24, for the softmax
+// also its argument's, at most 0.4, and its sum of 16 terms a lane over 64
+// lanes, 22; and the rounding of the last sum), and where another candidate
+// comes within twice that of a round's best, the scores are computed once more
+// in double, for the whole token, and decide.  (In double throughout, 4096
+// tokens over 256 experts took 10.6 us, 1000 vector instructions a token.)
+template <int VPL, bool kBias>
 __device__ __forceinline__ void route_token(const float *logits, const float *bias, int E, int top_k, int flags,
                                             float scale, int lane, int &expert, float &weight) {
-    constexpr bool kBias = sizeof(T) == 8;
     const bool sigmoid = (flags & Q4K_ROUTE_SIGMOID) != 0;
-    float l[VPL];
+    float l[VPL], bs[kBias ? VPL : 1];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
         const int e = v * 64 + lane;
         l[v] = e < E ? logits[e] : -INFINITY;
-        if (!(l[v] > -INFINITY)) l[v] = -INFINITY;  // NaN too
+        if constexpr (kBias) bs[v] = e < E ? bias[e] : 0.f;
     }
-    float mx = l[0];
+    // keys: the order of the logits (of the scores under a bias), 0: not to be chosen
+    uint32_t key[VPL], top = 0;
 #pragma unroll
-    for (int v = 1; v < VPL; ++v) mx = fmaxf(mx, l[v]);
-    mx = wave_max(mx);
-    T sum = 0;
-    T s[kBias ? VPL : 1], key[VPL];
+    for (int v = 0; v < VPL; ++v) {
+        key[v] = l[v] > -INFINITY ? ordered(l[v]) : 0;  // NaN: 0 too
+        top = key[v] > top ? key[v] : top;
+    }
+    const float mx = from_ordered(wave_max(top));
+    float sum = 1.f;  // of the softmax's numerators
+    float term[VPL];
+    if (!sigmoid && (kBias || !(flags & Q4K_ROUTE_NORMALIZE))) {
+        sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            term[v] = key[v] != 0 ? softmax_term(l[v], mx) : 0.f;
+            sum += term[v];
+        }
+        sum = wave_sum(sum);
+    }
     if constexpr (kBias) {
+        if (sigmoid) {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) term[v] = 1.f / (1.f + expf(-l[v]));
+        }
+        const float share = 1.f / sum;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const double z = l[v];
-            s[v] = !(l[v] > -INFINITY) ? 0.0 : sigmoid ? 1.0 / (1.0 + exp(-z)) : softmax_term(z, static_cast<double>(mx));
-            sum += s[v];
+            const float s = term[v] * share + bs[v];
+            key[v] = key[v] != 0 && s > -INFINITY ? ordered(s) : 0;
         }
-        sum = sigmoid ? 1.0 : wave_sum(sum);
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            const int e = v * 64 + lane;
-            if (!sigmoid) s[v] = s[v] / sum;
-            key[v] = l[v] > -INFINITY ? s[v] + static_cast<double>(bias[e]) : -INFINITY;
-            if (!(key[v] > -INFINITY)) key[v] = -INFINITY;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            key[v] = l[v];
-            if (!sigmoid && !(flags & Q4K_ROUTE_NORMALIZE)) sum += l[v] > -INFINITY ? softmax_term(l[v], mx) : 0.f;
-        }
-        sum = sigmoid ? 1.f : wave_sum(sum);
     }
+    double exact[kBias ? VPL : 1];
+    bool have_exact = false;
     expert = -1;
-    T mine = 0;  // the choice's score (bias) or logit (no bias)
+    float mine = 0.f;  // the choice's logit
     for (int j = 0; j < top_k; ++j) {
-        T best = key[0];
+        uint32_t best = key[0];
 #pragma unroll
         for (int v = 1; v < VPL; ++v) best = key[v] > best ? key[v] : best;
         best = wave_max(best);
-        if (!(best > static_cast<T>(-INFINITY))) break;  // uniform: nothing left to choose
-        bool found = false;
+        if (best == 0) break;  // uniform: nothing left to choose
+        uint64_t at[VPL];      // the lanes of the best (without close ones: exactly one)
+        uint32_t least = best;
+        if constexpr (kBias) {
+            const float f = from_ordered(best), near = f - (0x1p-18f + 0x1p-22f * fabsf(f));
+            least = near > -INFINITY ? ordered(near) : best;  // NaN where the best is infinite
+        }
+        int found = 0;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-            const uint64_t at = __ballot(key[v] == best);
-            if (!found && at != 0) {
-                found = true;
-                const int owner = __builtin_ctzll(at);
-                const T val = kBias ? lane_value(s[kBias ? v : 0], owner) : best;
-                if (lane == j) {
-                    expert = v * 64 + owner;
-                    mine = val;
+            at[v] = __ballot(key[v] >= least);
+            found += __builtin_popcountll(at[v]);
+        }
+        if constexpr (kBias) {
+            if (found > 1) {
+                if (!have_exact) {
+                    have_exact = true;
+                    double total = 0.0;
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v) {
+                        float z = l[v];
+                        asm volatile("" : "+v"(z));  // keeps the doubles out of the common path (and one at a time)
+                        exact[v] = !(z > -INFINITY) ? 0.0
+                                   : sigmoid       ? 1.0 / (1.0 + exp(-static_cast<double>(z)))
+                                                   : softmax_term(static_cast<double>(z), static_cast<double>(mx));
+                        total += exact[v];
+                    }
+                    total = sigmoid ? 1.0 : wave_sum(total);
+#pragma unroll
+                    for (int v = 0; v < VPL; ++v)
+                        exact[v] = exact[v] / total + static_cast<double>(bias[min(v * 64 + lane, E - 1)]);
                 }
-                if (lane == owner) key[v] = -INFINITY;
+                double largest = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < VPL; ++v)
+                    if (key[v] >= least && exact[v] > largest) largest = exact[v];
+                largest = wave_max(largest);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) at[v] = __ballot(key[v] >= least && exact[v] == largest);
             }
+        }
+        int owner = 0, slot = -1;
+#pragma unroll
+        for (int v = VPL - 1; v >= 0; --v) {
+            slot = at[v] != 0 ? v : slot;
+            owner = at[v] != 0 ? __builtin_ctzll(at[v]) : owner;
+        }
+        float val = l[0];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            val = slot == v ? l[v] : val;
+            key[v] = slot == v && lane == owner ? 0 : key[v];
+        }
+        val = lane_value(val, owner);
+        if (lane == j) {
+            expert = slot * 64 + owner;
+            mine = val;
         }
     }
     // One value per lane from here: in double, where a sigmoid does not
     // underflow before -745 and the shares of very low scores stay exact.
     double w = 0.0;
-    if (expert >= 0) {
-        if constexpr (kBias) w = mine;
-        else w = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(mine))) : static_cast<double>(softmax_term(mine, mx));
-    }
+    if (expert >= 0)
+        w = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(mine)))
+                    : softmax_term(static_cast<double>(mine), static_cast<double>(mx));
     if (flags & Q4K_ROUTE_NORMALIZE) {
         const double total = wave_sum(w);
         w = total > 0.0 ? w / total : 0.0;
-    } else if constexpr (!kBias) {
-        w = expert >= 0 ? w / static_cast<double>(sum) : 0.0;
+    } else {
+        w = w / static_cast<double>(sum);
     }
     weight = expert >= 0 ? scale * static_cast<float>(w) : 0.f;
 }
@@ -249,8 +327,13 @@ struct RouteArgs {
 
 // One workgroup: routing and grouping.  LDS: hist [waves][E], tot [E + 1] and
 // the choices [M][top_k].
-template <int VPL, class T>
-__global__ __launch_bounds__(kSingleThreads) void route_group_kernel(RouteArgs a) {
+// (Half the waves where sixteen scores a lane and their doubles need more than
+// a sixteenth of the registers.)
+template <int VPL, bool kBias>
+constexpr int kGroupThreads = VPL > 8 && kBias ? kSingleThreads / 2 : kSingleThreads;
+
+template <int VPL, bool kBias>
+__global__ __launch_bounds__((kGroupThreads<VPL, kBias>)) void route_group_kernel(RouteArgs a) {
     extern __shared__ int lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     int *hist = lds, *tot = hist + waves * a.E, *chosen = tot + a.E + 1;
@@ -258,7 +341,7 @@ __global__ __launch_bounds__(kSingleThreads) void route_group_kernel(RouteArgs a
     for (int m = wave; m < a.M; m += waves) {
         int e;
         float w;
-        route_token<VPL, T>(a.logits + static_cast<size_t>(m) * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
+        route_token<VPL, kBias>(a.logits + static_cast<size_t>(m) * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
         if (lane < a.top_k) {
             chosen[m * a.top_k + lane] = e;
             a.expert[m * a.top_k + lane] = e;
@@ -273,14 +356,14 @@ __global__ __launch_bounds__(kSingleThreads) void route_group_kernel(RouteArgs a
 }
 
 // Routing only: one token per wave.
-template <int VPL, class T>
+template <int VPL, bool kBias>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 63;
     const size_t m = static_cast<size_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
     if (m >= static_cast<size_t>(a.M)) return;
     int e;
     float w;
-    route_token<VPL, T>(a.logits + m * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
+    route_token<VPL, kBias>(a.logits + m * a.E, a.bias, a.E, a.top_k, a.flags, a.scale, lane, e, w);
     if (lane < a.top_k) {
         a.expert[m * a.top_k + lane] = e;
         a.weight[m * a.top_k + lane] = w;
@@ -288,20 +371,26 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
 }
 
 // Grouping: workgroup e places the pairs of expert e; the last one also closes
-// the offsets and fills the tail of rows.
+// the offsets and fills the tail of rows.  A wave reads its share of the
+// choices in rounds of kAhead steps of 64, all of a round's loads requested
+// together; up to kAhead * 1024 pairs there is one round, whose choices stay
+// in registers from the counts to the places.
 __global__ __launch_bounds__(kSingleThreads) void group_kernel(const int *expert, int P, int E, int *offsets, int *rows) {
-    constexpr int kWaves = kSingleThreads / 64, kAhead = 8;
+    constexpr int kWaves = kSingleThreads / 64, kAhead = 32;
     __shared__ int s_less[kWaves], s_same[kWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int mine = blockIdx.x;
-    // this wave's share, in steps of 64 pairs
-    const int64_t steps = (static_cast<int64_t>(P) + 63) / 64, per = (steps + kWaves - 1) / kWaves;
-    const int64_t i0 = wave * per * 64, i1 = min(static_cast<int64_t>(P), i0 + per * 64);
-    int less = 0, same = 0;
-    for (int64_t i = i0; i < i1; i += 64 * kAhead) {
-        int e[kAhead];
+    // this wave's share, in steps of 64 pairs (unsigned: a step may pass P)
+    const unsigned steps = (static_cast<unsigned>(P) + 63) / 64, per = (steps + kWaves - 1) / kWaves;
+    const unsigned i0 = wave * per * 64, i1 = min(static_cast<unsigned>(P), i0 + per * 64);
+    int e[kAhead];
+    const auto load = [&](unsigned i) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) e[k] = i + k * 64 + lane < i1 ? expert[i + k * 64 + lane] : -1;
+    };
+    int less = 0, same = 0;
+    for (unsigned i = i0; i < i1; i += 64 * kAhead) {
+        load(i);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             // as unsigned, -1 and every other negative number is above any expert
@@ -315,6 +404,7 @@ __global__ __launch_bounds__(kSingleThreads) void group_kernel(const int *expert
     }
     __syncthreads();
     int base = 0, before = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         base += s_less[w];
         before += w < wave ? s_same[w] : 0;
@@ -322,20 +412,19 @@ __global__ __launch_bounds__(kSingleThreads) void group_kernel(const int *expert
     }
     if (threadIdx.x == 0) offsets[mine] = base;
     int at = base + before;
-    for (int64_t i = i0; i < i1; i += 64 * kAhead) {
-        int e[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) e[k] = i + k * 64 + lane < i1 ? expert[i + k * 64 + lane] : -1;
+    for (unsigned i = i0; i < i1; i += 64 * kAhead) {
+        if (per > kAhead) load(i);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const uint64_t with = __ballot(e[k] == mine);
+            if (with == 0) continue;  // uniform
             if (e[k] == mine) rows[at + __builtin_popcountll(with & lanes_below(lane))] = static_cast<int>(i + k * 64 + lane);
             at += __builtin_popcountll(with);
         }
     }
     if (mine == E - 1) {
         if (threadIdx.x == 0) offsets[E] = base + all;
-        for (int64_t i = base + all + static_cast<int64_t>(threadIdx.x); i < P; i += kSingleThreads) rows[i] = -1;
+        for (unsigned i = base + all + threadIdx.x; i < static_cast<unsigned>(P); i += kSingleThreads) rows[i] = -1;
     }
 }
 
@@ -344,28 +433,28 @@ hipError_t launch_group(const int *expert, int P, int E, int *offsets, int *rows
     return hipGetLastError();
 }
 
-template <int VPL, class T>
+template <int VPL, bool kBias>
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
     if (a.M <= kSingleTokens) {
-        const int waves = kSingleThreads / 64;
+        constexpr int kThreads1 = kGroupThreads<VPL, kBias>, waves = kThreads1 / 64;
         const int bytes = (waves * a.E + a.E + 1 + a.M * a.top_k) * 4;
-        const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_group_kernel<VPL, T>), 96 << 10);
+        const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_group_kernel<VPL, kBias>), 96 << 10);
         if (err != hipSuccess) return err;
-        hipLaunchKernelGGL((route_group_kernel<VPL, T>), dim3(1), dim3(kSingleThreads), bytes, stream, a);
+        hipLaunchKernelGGL((route_group_kernel<VPL, kBias>), dim3(1), dim3(kThreads1), bytes, stream, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((route_kernel<VPL, T>), dim3((a.M - 1) / (kThreads / 64) + 1), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((route_kernel<VPL, kBias>), dim3((a.M - 1) / (kThreads / 64) + 1), dim3(kThreads), 0, stream, a);
     const hipError_t err = hipGetLastError();
     return err != hipSuccess ? err : launch_group(a.expert, a.M * a.top_k, a.E, a.offsets, a.rows, stream);
 }
 
-template <class T>
+template <bool kBias>
 hipError_t launch_route_for(const RouteArgs &a, hipStream_t stream) {
-    if (a.E <= 64) return launch_route<1, T>(a, stream);
-    if (a.E <= 128) return launch_route<2, T>(a, stream);
-    if (a.E <= 256) return launch_route<4, T>(a, stream);
-    if (a.E <= 512) return launch_route<8, T>(a, stream);
-    return launch_route<16, T>(a, stream);
+    if (a.E <= 64) return launch_route<1, kBias>(a, stream);
+    if (a.E <= 128) return launch_route<2, kBias>(a, stream);
+    if (a.E <= 256) return launch_route<4, kBias>(a, stream);
+    if (a.E <= 512) return launch_route<8, kBias>(a, stream);
+    return launch_route<16, kBias>(a, stream);
 }
 
 bool misaligned4(const void *a, const void *b = nullptr, const void *c = nullptr, const void *d = nullptr,
@@ -394,7 +483,7 @@ extern "C" int q4k_moe_route(const float *logits, const float *bias, int M, int 
     if (dev_rc != Q4K_OK) return dev_rc;
     if (M == 0) return status(launch_group(nullptr, 0, E, offsets, rows, stream));
     const RouteArgs a = {logits, bias, expert, weight, offsets, rows, M, E, top_k, flags, scale};
-    return status(bias ? launch_route_for<double>(a, stream) : launch_route_for<float>(a, stream));
+    return status(bias ? launch_route_for<true>(a, stream) : launch_route_for<false>(a, stream));
 }
 
 extern "C" int q4k_moe_group(const int *expert, int P, int E, int *offsets, int *rows, hipStream_t stream) {
