@@ -94,7 +94,7 @@ __device__ __forceinline__ void stage_eight(const float4 a, const float4 b, int 
 
 // Stages one row of x per workgroup: the row's first kKept * 8 values of every
 // thread stay in registers between the maximum and the conversion.
-constexpr int kStageThreads = 256, kKept = 4;
+constexpr int kStageThreads = 1024, kKept = 2;
 __global__ __launch_bounds__(kStageThreads) void stage_rows_kernel(const float *x, int K, uint8_t *img, uint8_t *sums,
                                                                    float *back) {
     __shared__ float wave_mx[kStageThreads / 64];
@@ -271,7 +271,7 @@ __device__ __forceinline__ float4v mfma(half8 a, half8 b, float4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// ---- many rows per expert: tiles of RT * 16 rows times 256 columns ----------
+// ---- many rows per expert: tiles of RT * 16 rows times 64 NC columns ----------
 
 // LDS of a workgroup: two buffers of x (a quarter of a super-block: two steps,
 // 256 bytes a row), two of its sub-block sums, one super-block of each wave's
@@ -297,12 +297,14 @@ __device__ __forceinline__ uint32_t lds_address(uint8_t *p) {
 // read, whichever buffer that reads; no register is written, and the kernel
 // waits for vmcnt and the barrier before it reads a buffer.
 __device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory");
 }
 // The same from a buffer (offsets behind its end read zeros).
 __device__ __forceinline__ void copy_to_lds(rsrc_t buffer, uint32_t offset, uint32_t base, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(offset), "s"(buffer),
-                 "s"(base), "s"(dst)
+                 "s"(__builtin_amdgcn_readfirstlane(base)), "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory");
 }
 // A raw buffer of bytes at p (both uniform).
@@ -569,22 +571,48 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
 // registers at the start of a super-block and its slot is refilled at once, so
 // that copies are on their way during all of the arithmetic; x comes half a
 // super-block (512 bytes a row) at a time in two buffers.  That keeps a
-// workgroup within a quarter of the LDS, and four to a CU.  (Staging x inside
+// workgroup within a quarter of the LDS, and four to a CU.  Where the tiles
+// leave CUs idle, KS such groups of four waves split K by super-blocks (group s
+// takes blocks s, s + KS, ...), and the first adds the others' sums in order:
+// 64 pairs over 8 experts of 1024 x 2048 16.1 -> 14.0 us.  (Staging x inside
 // this kernel instead of by a launch of its own was slower: 32 against 29 us
 // for 48 x 8 rows over 64 experts of 2048 x 1024, 66 against 48 us at 128 x 8.)
 template <int NC>
 struct ThinLds {
     static constexpr int kX = 16 * kImageBlock / 2, kSums = 16 * kSumsBlock, kW = 16 * NC * kBlockBytes;
-    static constexpr int kSumsAt = 2 * kX, kWAt = kSumsAt + 2 * kSums, kPairsAt = kWAt + 4 * kW;
-    static constexpr int kBackAt = kPairsAt + 64, kBytes = kBackAt + 64;
+    static constexpr int kSumsAt = 2 * kX, kWAt = kSumsAt + 2 * kSums, kGroup = kWAt + 4 * kW;
+    static constexpr int bytes(int groups) { return groups * kGroup + 16 * 8; }
 };
 
-template <int NC, bool kSwiglu>
-__global__ __launch_bounds__(256, 4) void thin_kernel(Grouped g) {
+// Adds the wave groups' sums (R values of a thread each): groups 1 .. KS - 1
+// leave them in LDS, group 0 returns true with all of them.
+template <int KS, int R>
+__device__ __forceinline__ bool join_groups(float *acc, uint8_t *lds, int group) {
+    if constexpr (KS == 1) return true;
+    float *red = reinterpret_cast<float *>(lds) + (threadIdx.x & 255);
+    wait_all();
+    barrier();  // every group has left its buffers
+    if (group != 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) red[((group - 1) * R + i) * 256] = acc[i];
+    }
+    __syncthreads();
+    if (group != 0) return false;
+#pragma unroll
+    for (int s = 1; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < R; ++i) acc[i] += red[((s - 1) * R + i) * 256];
+    return true;
+}
+
+template <int NC, int KS, bool kSwiglu>
+__global__ __launch_bounds__(256 * KS, 4) void thin_kernel(Grouped g) {
     using L = ThinLds<NC>;
     using W = WTile<NC, kSwiglu>;
-    extern __shared__ __align__(16) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    extern __shared__ __align__(16) uint8_t all_lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+    const int group = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    uint8_t *const lds = all_lds + group * L::kGroup;
     const int c16 = lane & 15, quarter = lane >> 4;
     Tiles<16> tiles(g.offsets, g.E, g.P, lane);
     const int n_tiles = (g.N - 1) / (4 * W::kN) + 1;
@@ -595,12 +623,12 @@ __global__ __launch_bounds__(256, 4) void thin_kernel(Grouped g) {
     const int n0 = (at % n_tiles * 4 + wave) * W::kN;
     uint8_t *const wslot = lds + L::kWAt + wave * L::kW;
     const W w(g, t.e, n0, wslot, lane);
-    w.copy(0);
-    int *pairs = reinterpret_cast<int *>(lds + L::kPairsAt);
-    float *back = reinterpret_cast<float *>(lds + L::kBackAt);
+    const int KB = g.K / kBlockWeights;
+    if (group < KB) w.copy(group);
+    int *pairs = reinterpret_cast<int *>(all_lds + KS * L::kGroup);
+    float *back = reinterpret_cast<float *>(pairs + 16);
     load_pairs(g, t, 16, pairs, back);
     __syncthreads();
-    const int KB = g.K / kBlockWeights;
     // x: this wave copies rows 4 wave .. + 4, two per instruction, their pieces
     // exchanged by the row's number as in tile_kernel
     const uint8_t *xsrc[2], *ssrc = g.x.sums;
@@ -621,28 +649,36 @@ __global__ __launch_bounds__(256, 4) void thin_kernel(Grouped g) {
             copy_to_lds(xsrc[j] + (static_cast<size_t>(b) * kImageBlock + half * (kImageBlock / 2)),
                         lds0 + half * L::kX + (wave * 2 + j) * 1024);
     };
-    const auto copy_sums = [&](int b) {
+    const auto copy_sums = [&](int b, int buf) {
         if (lane < 8)
-            copy_to_lds(ssrc + static_cast<size_t>(b) * kSumsBlock, lds0 + L::kSumsAt + (b & 1) * L::kSums + wave * 128);
+            copy_to_lds(ssrc + static_cast<size_t>(b) * kSumsBlock, lds0 + L::kSumsAt + buf * L::kSums + wave * 128);
     };
     float4v acc[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
-    copy_x(0, 0);
-    copy_sums(0);
-    for (int b = 0; b < KB; ++b) {
+    if (group < KB) {
+        copy_x(group, 0);
+        copy_sums(group, 0);
+    }
+    int parity = 0;  // of the sums' buffers
+    for (int b0 = 0; b0 < KB; b0 += KS, parity ^= 1) {
+        const int b = b0 + group;
         wait_all();
         barrier();
+        if (KS > 1 && b >= KB) {  // uniform over a wave; the barriers are the workgroup's
+            barrier();
+            continue;
+        }
         WBlock wb[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) wb[c] = load_block(wslot + (c * 16 + c16) * kBlockBytes, 0, quarter);
         wait_lds();  // W is in registers
         copy_x(b, 1);
-        const bool more = b + 1 < KB;
-        if (more) w.copy(b + 1);
+        const bool more = b + KS < KB;
+        if (more) w.copy(b + KS);
         WScales ws[NC];
         float4v blk[NC];
-        const uint4 s = *reinterpret_cast<const uint4 *>(lds + L::kSumsAt + (b & 1) * L::kSums + c16 * kSumsBlock + (quarter & 1) * 16);
+        const uint4 s = *reinterpret_cast<const uint4 *>(lds + L::kSumsAt + parity * L::kSums + c16 * kSumsBlock + (quarter & 1) * 16);
         const half8 am = __builtin_bit_cast(half8, quarter < 2 ? s : uint4{0, 0, 0, 0});
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -661,8 +697,8 @@ __global__ __launch_bounds__(256, 4) void thin_kernel(Grouped g) {
                 else wait_all();
                 barrier();
                 if (more) {
-                    copy_x(b + 1, 0);
-                    copy_sums(b + 1);
+                    copy_x(b + KS, 0);
+                    copy_sums(b + KS, parity ^ 1);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);  // the operands of one pair of steps in registers at a time
@@ -686,6 +722,7 @@ __global__ __launch_bounds__(256, 4) void thin_kernel(Grouped g) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[c][k] = __builtin_fmaf(ws[c].d, blk[c][k], acc[c][k]);
     }
+    if (!join_groups<KS, NC * 4>(reinterpret_cast<float *>(acc), all_lds, group)) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int i = 4 * quarter + k, p = pairs[i];
@@ -919,30 +956,35 @@ int check_grouped(const void *w, const void *w2, const float *x, int x_div, cons
 enum class Variant { kFew, kThin, kTile, kLargeTile };
 
 // The kernel for a call, from what the host knows (the groups' sizes are on
-// the device): P pairs over E experts, and the bytes of an expert's matrices.
-//   * Few rows: each tile of four rows streams its expert's matrix at about
-//     3.3 TB/s after 4.5 us; sixteen-row tiles stream it at about 4.2 TB/s, but
-//     after 11 us (two launches and deeper pipelines).  With at most
-//     min(E, P) experts in use and one more tile of four for every four pairs
-//     above one per expert, four-row tiles win while
-//     (1.27 tiles - experts) * bytes < 27 MB.  Both sides measured, 64 experts
-//     of 1024 x 2048 (SwiGLU): 1 token 7.5 / 14.8 us, 4 tokens 24.1 / 23.8 us,
-//     8 tokens 33.6 / 29.3 us; 8 experts of 1999 x 1280: 8 tokens 6.9 / 12.3 us,
-//     32 tokens 14.4 / 12.5 us.
-//   * Sixteen rows by 128 columns up to 16 pairs per expert, 32 by 128 above:
-//     at 8 per expert 29.6 / 29.4 us (16 experts of 4096 x 2048), at 24 38.9 /
-//     36.1 us, at 64 72.0 / 56.8 us.
-//   * 48 rows by 256 columns from 64 pairs per expert, where that still gives
-//     two workgroups to every CU: 64 experts of 1024 x 2048 (SwiGLU), 256 rows
-//     each, 310 against 330 us; 16 of 4096 x 2048, 48 rows each, 56.3 against 47.5 us.
-Variant choose(const Grouped &g) {
-    const double experts = g.E < g.P ? g.E : g.P, matrices = g.w2 ? 2 : 1;
-    const double bytes = matrices * g.N * (g.K / kBlockWeights) * kBlockBytes;
-    const double fours = experts + (g.P > g.E ? (g.P - g.E) / 4 : 0);
-    if (fours < 16384 && (1.27 * fours - experts) * bytes < 27e6) return Variant::kFew;
-    if (g.P < 16 * static_cast<int64_t>(g.E)) return Variant::kThin;
-    const double workgroups = (g.P / 48 + 0.5 * g.E) * (matrices * g.N / 256);
-    return g.P >= 64 * static_cast<int64_t>(g.E) && workgroups >= 512 ? Variant::kLargeTile : Variant::kTile;
+// the device): P pairs over E experts.  Expected times in us, of a pair of
+// expected tile counts: with the pairs spread evenly E (1 - exp(-P / E))
+// experts are in use, and tiles of r rows are that many and one more for every
+// r pairs above half a tile each.  The unit of work is a super-block of one
+// column tile; the rates are those measured with the card full (tiles of 16
+// rows are then bound by W's 4.6 TB/s), the other side of each maximum is one
+// tile's own time over its K blocks, and 5 us is the staging launch that tiles
+// of four rows do without.  Measured, rows of four / of sixteen / of 32 rows by
+// 128 columns, in us:
+//     64 experts of 1024 x 2048 (SwiGLU), 8 pairs a token: 1 token 8 / 15 / 21,
+//         4 tokens 25 / 23 / 28, 64 tokens 100 / 42 / 44, 256 tokens 332 / 73 / 65
+//     16 experts of 4096 x 2048, 2 pairs: 8 tokens 18 / 22 / 27, 128 tokens
+//         96 / 31 / 37, 256 tokens 172 / 43 / 43
+//     40 experts of 50 x 2560, 5 pairs, 242 tokens: 18 / 26 / 36
+// From 64 pairs per expert, where it still gives two workgroups to every CU,
+// 48 rows by 256 columns: 64 experts of 1024 x 2048 (SwiGLU), 256 rows each, 302
+// against 330 us; 16 of 4096 x 2048, 48 rows each, 56 against 48 us.
+Variant choose(const Grouped &g, int *groups) {
+    const double P = g.P, E = g.E, KB = g.K / kBlockWeights, columns = g.w2 ? 2.0 * g.N : g.N;
+    const double used = P <= E / 8 ? P : E * (1.0 - exp(-P / E));
+    const auto tiles = [&](double rows) { return used + fmax(0.0, P / rows - 0.5 * used); };
+    const double thin_workgroups = tiles(16) * ceil(columns / 128);
+    *groups = thin_workgroups <= 256 && KB >= 4 ? 4 : thin_workgroups <= 512 && KB >= 2 ? 2 : 1;
+    const double few = tiles(4) * ceil(columns / 32) * KB / 750;
+    const double thin = fmax(thin_workgroups * KB / 250, 3.0 * KB / *groups);
+    const double tile = fmax(tiles(32) * ceil(columns / 128) * KB / 158, 1.9 * KB);
+    if (few < 5 + fmin(thin, tile) && tiles(4) < 16384) return Variant::kFew;
+    if (P >= 64 * E && (P / 48 + 0.5 * E) * columns / 256 >= 512) return Variant::kLargeTile;
+    return thin <= tile ? Variant::kThin : Variant::kTile;
 }
 
 template <int WAVES, bool kSwiglu>
@@ -955,33 +997,34 @@ hipError_t launch_few(const Grouped &g, const float *x, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <class K>
-hipError_t launch_tiles(K kernel, const Grouped &g, int rows, int cols, int bytes, hipStream_t stream) {
+hipError_t launch_tiles(void (*kernel)(Grouped), const Grouped &g, int rows, int cols, int threads, int bytes,
+                        hipStream_t stream) {
     const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes);
     if (err != hipSuccess) return err;
     const int64_t tiles = g.P / rows + (g.E < g.P ? g.E : g.P);
     const int64_t blocks = (tiles * ((g.N - 1) / cols + 1) + 7) / 8 * 8;
     if (blocks > INT_MAX) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), bytes, stream, g);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), bytes, stream, g);
     return hipGetLastError();
 }
 template <int RT, int NC>
 hipError_t launch_tile(const Grouped &g, hipStream_t stream) {
-    if (g.w2)
-        return launch_tiles(tile_kernel<RT, NC, true>, g, RT * 16, 4 * WTile<NC, true>::kN, TileLds<RT, NC>::kBytes, stream);
-    return launch_tiles(tile_kernel<RT, NC, false>, g, RT * 16, 4 * WTile<NC, false>::kN, TileLds<RT, NC>::kBytes, stream);
+    constexpr int kBytes = TileLds<RT, NC>::kBytes;
+    if (g.w2) return launch_tiles(tile_kernel<RT, NC, true>, g, RT * 16, 4 * WTile<NC, true>::kN, 256, kBytes, stream);
+    return launch_tiles(tile_kernel<RT, NC, false>, g, RT * 16, 4 * WTile<NC, false>::kN, 256, kBytes, stream);
 }
-template <int NC>
+template <int NC, int KS>
 hipError_t launch_thin(const Grouped &g, hipStream_t stream) {
-    if (g.w2)
-        return launch_tiles(thin_kernel<NC, true>, g, 16, 4 * WTile<NC, true>::kN, ThinLds<NC>::kBytes, stream);
-    return launch_tiles(thin_kernel<NC, false>, g, 16, 4 * WTile<NC, false>::kN, ThinLds<NC>::kBytes, stream);
+    constexpr int kBytes = ThinLds<NC>::bytes(KS);
+    if (g.w2) return launch_tiles(thin_kernel<NC, KS, true>, g, 16, 4 * WTile<NC, true>::kN, 256 * KS, kBytes, stream);
+    return launch_tiles(thin_kernel<NC, KS, false>, g, 16, 4 * WTile<NC, false>::kN, 256 * KS, kBytes, stream);
 }
 
 // Stages x, then the products.  g.x is filled in here.
 hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     const size_t xrows = (static_cast<size_t>(g.P) + g.x_div - 1) / g.x_div, KB = g.K / kBlockWeights;
-    const Variant variant = choose(g);
+    int groups = 1;
+    const Variant variant = choose(g, &groups);
     if (variant == Variant::kFew) {
         if (g.w2) return KB > 4 ? launch_few<8, true>(g, x, stream) : launch_few<4, true>(g, x, stream);
         return KB > 4 ? launch_few<8, false>(g, x, stream) : launch_few<4, false>(g, x, stream);
@@ -998,7 +1041,10 @@ hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     err = hipGetLastError();
     if (err != hipSuccess) return err;
     switch (variant) {
-    case Variant::kThin: return launch_thin<2>(g, stream);
+    case Variant::kThin:
+        return groups == 4   ? launch_thin<2, 4>(g, stream)
+               : groups == 2 ? launch_thin<2, 2>(g, stream)
+                             : launch_thin<2, 1>(g, stream);
     case Variant::kTile: return launch_tile<2, 2>(g, stream);
     default: return launch_tile<3, 4>(g, stream);
     }

@@ -24,7 +24,7 @@
 namespace q4k {
 namespace {
 
-constexpr int kSingleTokens = 64;  // tokens routed and grouped by one workgroup
+constexpr int kSingleTokens = 48;  // tokens routed and grouped by one workgroup (16 under a bias)
 constexpr int kSingleThreads = 1024;
 constexpr int kThreads = 256;
 
@@ -435,7 +435,7 @@ hipError_t launch_group(const int *expert, int P, int E, int *offsets, int *rows
 
 template <int VPL, bool kBias>
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-    if (a.M <= kSingleTokens) {
+    if (a.M <= (kBias ? kSingleTokens / 3 : kSingleTokens)) {
         constexpr int kThreads1 = kGroupThreads<VPL, kBias>, waves = kThreads1 / 64;
         const int bytes = (waves * a.E + a.E + 1 + a.M * a.top_k) * 4;
         const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_group_kernel<VPL, kBias>), 96 << 10);
