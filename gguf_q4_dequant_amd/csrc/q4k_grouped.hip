@@ -392,7 +392,8 @@ struct WTile {
 __device__ __forceinline__ int place_in_work(unsigned id, int tiles, int n_tiles) {
     const int64_t work = static_cast<int64_t>(tiles) * n_tiles, per = (work + 7) / 8;
     const int64_t at = (id & 7) * per + (id >> 3);
-    return (id >> 3) >= per || at >= work ? -1 : static_cast<int>(at);
+    // (a table whose offsets do not ascend may claim more than a call can hold)
+    return (id >> 3) >= per || at >= work || at > INT_MAX ? -1 : static_cast<int>(at);
 }
 
 // Pair i of the tile, the last one again behind its end; -1 for an entry
@@ -945,7 +946,8 @@ int check_grouped(const void *w, const void *w2, const float *x, int x_div, cons
                   const float *y, int E, int P, int N, int K) {
     if (E < 1 || E > Q4K_MAX_EXPERTS || P < 0 || N < 0 || K < 0 || x_div < 1) return Q4K_ERR_BAD_DIM;
     if (P == 0 || N == 0) return Q4K_OK;
-    if (K == 0 || K % kBlockWeights != 0) return Q4K_ERR_BAD_DIM;
+    // 32 rows of W are addressed as one buffer of 32-bit offsets
+    if (K == 0 || K % kBlockWeights != 0 || K > (1 << 26)) return Q4K_ERR_BAD_DIM;
     if (!w || !w2 || !x || !offsets || !y) return Q4K_ERR_NULL;
     if (misaligned(w, 16) || misaligned(w2, 16) || misaligned(x, 16) || misaligned(y, 16) || misaligned(offsets, 4) ||
         misaligned(rows, 4))

@@ -22,8 +22,9 @@
  *
  * Conventions are those of q4k.h: device pointers on the current device, the
  * caller's stream, no host synchronization, the library's per-stream
- * workspace (make one eager call of each shape before a graph capture), the
- * same status codes, nothing enqueued on an error.  Empty sizes (M, P or N
+ * workspace (make one eager call of each shape before a graph capture; host
+ * threads that share a stream take turns), the same status codes, nothing
+ * enqueued on an error.  Empty sizes (M, P or N
  * zero) are successful no-ops.
  */
 #ifndef Q4K_MOE_H
@@ -84,13 +85,13 @@ int q4k_moe_group(const int *expert, int P, int E, int *offsets, int *rows, hipS
  *   Entries of rows outside [0, P) are skipped, and offsets are read as if
  *   clamped to [0, P]; a pair of offsets that descends is an empty group.
  *   Numerics: x is split into two binary16 values scaled by a power of two per
- *   row (about 22 significant bits of each value, and never less than 2^-38 of
- *   the row's largest magnitude), the quants times their 6-bit scales are
+ *   row or per 256 values of a row (about 22 significant bits of each value;
+ *   2^-40 of the largest magnitude where that is more), the quants times their 6-bit scales are
  *   exact integers, sums and scales are fp32: rounding of the order of
  *   1e-6 * sum_k |x_k| (|d sc q| + |dmin m|).  A NaN or infinity in a row of x
  *   gives NaN or infinities in that row of y only.
  *   Errors: negative sizes, E outside [1, Q4K_MAX_EXPERTS], x_div < 1, K not a
- *   positive multiple of 256: Q4K_ERR_BAD_DIM; NULL (rows excepted):
+ *   positive multiple of 256 or above 2^26: Q4K_ERR_BAD_DIM; NULL (rows excepted):
  *   Q4K_ERR_NULL; alignment: Q4K_ERR_ALIGN; Q4K_ERR_ALLOC; Q4K_ERR_LAUNCH. */
 int q4k_matmul_grouped(const void *w_packed, const float *x, int x_div, const int *offsets, const int *rows,
                        float *y, int E, int P, int N, int K, hipStream_t stream);

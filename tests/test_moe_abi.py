@@ -50,7 +50,7 @@ def test_grouped_refusals(lib):
         return lib.q4k_matmul_grouped_swiglu(w, w2, x, x_div, offsets, rows, y, E, P, N, K, None)
 
     for call in (product, swiglu):
-        for bad in (dict(E=0), dict(E=1025), dict(P=-1), dict(N=-1), dict(K=-256), dict(K=0), dict(K=300), dict(x_div=0)):
+        for bad in (dict(E=0), dict(E=1025), dict(P=-1), dict(N=-1), dict(K=-256), dict(K=0), dict(K=300), dict(K=2 ** 26 + 256), dict(x_div=0)):
             assert call(**bad) == q4k.ERR_BAD_DIM, bad
         for name in ("w", "x", "offsets", "y"):
             assert call(**{name: None}) == q4k.ERR_NULL, name

@@ -157,6 +157,34 @@ def test_grouped_swiglu(sizes, N, K, x_div):
     assert np.all(err <= bound + 1e-30), (err / (bound + 1e-30)).max()
 
 
+# One call of each kernel that the sizes choose: four-row tiles on four and
+# eight waves, sixteen-row tiles with K over four, two and one groups of waves,
+# 32 x 128 and 48 x 256 tiles.  The groups' sizes are uneven and some are empty.
+@pytest.mark.parametrize("P,E,N,K", [(40, 2, 300, 512), (40, 2, 300, 1280), (200, 2, 1000, 1024), (400, 2, 1000, 512),
+                                     (200, 24, 2600, 512), (3000, 2, 300, 512), (3000, 2, 2300, 256),
+                                     (900, 600, 40, 256), (5000, 300, 150, 256), (70, 1024, 33, 512)])
+def test_every_kernel(P, E, N, K):
+    import torch
+    g = _rng(7, P, E)
+    share = g.random(E) ** 2
+    share[::7] = 0.0 if E > 2 else share[::7]
+    offsets, rows, P = _table(g.multinomial(P, share / share.sum()), P)
+    w, u = _weights(E, N, K, 20), _weights(E, N, K, 21)
+    x = (0.02 * qi.random_x((P + 1) // 2, K, seed=P)).astype(np.float32)
+    args = to_dev(x), to_dev(offsets), to_dev(rows)
+    y = q4k.matmul_grouped(to_dev(w), *args, x_div=2)
+    h = q4k.matmul_grouped_swiglu(to_dev(w), to_dev(u), *args, x_div=2)
+    torch.cuda.synchronize()
+    want, s = ref.grouped(w, x, offsets, rows, 2, P)
+    check_close(y.cpu().numpy(), want, s, ref.product_tol(K))
+    wu, su = ref.grouped(u, x, offsets, rows, 2, P)
+    t = ref.product_tol(K)  # as in test_grouped_swiglu
+    bound = 1.1 * t * s * (np.abs(wu) + t * su) + np.abs(ref.silu(want)) * t * su + \
+        np.abs(ref.silu(want) * wu) * (np.abs(want) + 8) * 2.0 ** -23
+    err = np.abs(h.cpu().numpy().astype(np.float64) - ref.silu(want) * wu)
+    assert np.all(err <= bound + 1e-30), (err / (bound + 1e-30)).max()
+
+
 @pytest.mark.parametrize("M,E,k,N,K", [(1, 8, 2, 96, 512), (3, 4, 4, 33, 256), (40, 16, 3, 260, 768), (257, 5, 2, 64, 512),
                                        (1, 64, 8, 300, 1280)])
 @pytest.mark.parametrize("holes", [False, True])
@@ -261,9 +289,8 @@ def test_one_hot_rows_give_the_weights():
         assert np.all(np.abs(y[r] - val[:, at[r]].T) <= 2 * 2.0 ** -24 * mag[:, at[r]].T)
 
 
-def test_results_do_not_depend_on_the_run_or_the_batch():
-    """The same call twice gives the same bits, and a pair's row does not depend
-    on which other pairs share its expert's tile."""
+def test_results_do_not_depend_on_the_run():
+    """The same call twice gives the same bits."""
     sizes = [70, 3, 0, 18]
     offsets, rows, P = _table(sizes, 12)
     w, x = to_dev(_weights(4, 90, 1024, 9)), to_dev(qi.random_x(P, 1024, seed=12))
@@ -289,6 +316,27 @@ def test_weights_behind_four_gigabytes():
     want, s = ref.grouped(last[None], x, [0, 3], np.arange(3), 1, 3)
     check_close(y[:, -64:], want, s, ref.product_tol(K))
     assert np.all(y[:, :-64] == 0.0)
+
+
+def test_outputs_behind_two_to_the_31():
+    """The last rows of y start past 2^31 elements; rows in between are left alone."""
+    import torch
+    E, N, K, P = 2, 32768, 256, 66000
+    w = _weights(E, N, K, 15)
+    x = qi.random_x(P, K, seed=15)
+    y = torch.full((P, N), 7.0, device=device())
+    offsets = np.array([0, 3, 40], np.int32)
+    rows = np.concatenate([[0, 5, P - 1], np.arange(P - 38, P - 1)]).astype(np.int32)
+    rows = np.concatenate([rows, np.full(P - 40, -1, np.int32)])
+    assert (P - 1) * N > 1 << 31
+    q4k.matmul_grouped(to_dev(w), to_dev(x), to_dev(offsets), to_dev(rows), y=y)
+    for e in range(E):
+        r = rows[offsets[e]:offsets[e + 1]]
+        val, mag = ref.unpack(w[e])
+        xs = x[r].astype(np.float64)
+        check_close(y[torch.from_numpy(r.astype(np.int64)).to(y.device)].cpu().numpy(), xs @ val.T, np.abs(xs) @ mag.T,
+                    ref.product_tol(K))
+    assert bool((y[1:5] == 7.0).all()) and bool((y[6:P - 38] == 7.0).all())
 
 
 # ---- a layer of them ---------------------------------------------------------------
