@@ -246,7 +246,7 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
         value = torch.empty(M, dtype=torch.float32, device=x.device)
     _check_outputs(x, index, value, M)
     if adjustment is not None:
-        rc = library().q4k_matmul_argmax_adjusted(w.data_ptr(), x.data_ptr(), adjustment._checked(x, M, N), M, N, K,
+        rc = library().q4k_matmul_argmax_adjusted(w.data_ptr(), x.data_ptr(), adjustment._checked(x.get_device(), M, N), M, N, K,
                                                   index.data_ptr(), value.data_ptr(), _stream_handle(stream))
         if rc != OK:
             raise Q4KError(rc, "q4k_matmul_argmax_adjusted")
@@ -258,27 +258,27 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
     return index, value
 
 
-def _checked_tensor(name, t, dtype, shape, like):
-    """t is a contiguous tensor of this dtype and shape on like's device; its address."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == like.device and t.is_contiguous():
+def _checked_tensor(name, t, dtype, shape, dev):
+    """t is a contiguous tensor of this dtype and shape on GPU number dev; its address."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be shaped {list(shape)}, not {list(t.shape)}")
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a device tensor on {like.device}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on cuda:{dev}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _stream_for(x, stream) -> int:
-    """The handle of the given stream, or of the current one; x has to be on the
-    current device, whose context the library launches in."""
+def _stream_for(dev, stream) -> int:
+    """The handle of the given stream, or of the current one; the tensors (on GPU
+    number dev) have to be on the current device, whose context the library
+    launches in."""
     import torch
-    current = torch._C._cuda_getDevice()
-    if x.device.index != current:
-        raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{current}")
-    return torch._C._cuda_getCurrentRawStream(current) if stream is None else _stream_handle(stream)
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
 
 
 class Adjustment:
@@ -307,8 +307,8 @@ class Adjustment:
         self.history, self.repetition, self.frequency, self.presence = history, repetition, frequency, presence
         self.bias_id, self.bias_value, self.mask = bias_id, bias_value, mask
 
-    def _checked(self, like, M, N):
-        """The C struct for logits [M, N] on like's device."""
+    def _checked(self, dev, M, N):
+        """The C struct for logits [M, N] on GPU number dev."""
         import torch
         history = repetition = frequency = presence = bias_id = bias_value = mask = None
         L = B = 0
@@ -316,22 +316,22 @@ class Adjustment:
             if self.history.dim() != 2:
                 raise ValueError("history must be int32 [M, L]")
             L = self.history.shape[1]
-            history = _checked_tensor("history", self.history, torch.int32, (M, L), like)
+            history = _checked_tensor("history", self.history, torch.int32, (M, L), dev)
             if self.repetition is not None:
-                repetition = _checked_tensor("repetition", self.repetition, torch.float32, (M,), like)
+                repetition = _checked_tensor("repetition", self.repetition, torch.float32, (M,), dev)
             if self.frequency is not None:
-                frequency = _checked_tensor("frequency", self.frequency, torch.float32, (M,), like)
+                frequency = _checked_tensor("frequency", self.frequency, torch.float32, (M,), dev)
             if self.presence is not None:
-                presence = _checked_tensor("presence", self.presence, torch.float32, (M,), like)
+                presence = _checked_tensor("presence", self.presence, torch.float32, (M,), dev)
         if self.bias_id is not None:
             if self.bias_id.dim() != 2:
                 raise ValueError("bias_id must be int32 [M, B]")
             B = self.bias_id.shape[1]
-            bias_id = _checked_tensor("bias_id", self.bias_id, torch.int32, (M, B), like)
-            bias_value = _checked_tensor("bias_value", self.bias_value, torch.float32, (M, B), like)
+            bias_id = _checked_tensor("bias_id", self.bias_id, torch.int32, (M, B), dev)
+            bias_value = _checked_tensor("bias_value", self.bias_value, torch.float32, (M, B), dev)
         if self.mask is not None:
             dtype = torch.uint32 if self.mask.dtype == torch.uint32 else torch.int32
-            mask = _checked_tensor("mask", self.mask, dtype, (M, (N + 31) // 32), like)
+            mask = _checked_tensor("mask", self.mask, dtype, (M, (N + 31) // 32), dev)
         return _Adjustment(history, repetition, frequency, presence, bias_id, bias_value, mask, L, B)
 
 
@@ -341,20 +341,21 @@ def _checked_logits(logits):
         raise TypeError("logits must be float32 [M, N]")
     if not logits.is_cuda or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous device tensor")
-    return logits.shape
+    M, N = logits.shape
+    return M, N, logits.get_device()
 
 
 def logits_adjust(logits, adjustment, out=None, stream=None):
     """The logits float32 [M, N] under an ``Adjustment`` (penalties, biases, -inf
     where the mask forbids), in a new tensor or in ``out`` (which may be logits)."""
     import torch
-    M, N = _checked_logits(logits)
+    M, N, dev = _checked_logits(logits)
     if out is None:
         out = torch.empty_like(logits)
     elif out is not logits:
-        _checked_tensor("out", out, torch.float32, (M, N), logits)
-    rc = library().q4k_logits_adjust(logits.data_ptr(), out.data_ptr(), adjustment._checked(logits, M, N), M, N,
-                                     _stream_for(logits, stream))
+        _checked_tensor("out", out, torch.float32, (M, N), dev)
+    rc = library().q4k_logits_adjust(logits.data_ptr(), out.data_ptr(), adjustment._checked(dev, M, N), M, N,
+                                     _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_logits_adjust")
     return out
@@ -366,15 +367,15 @@ def logits_argmax(logits, adjustment, index=None, value=None, stream=None):
     value -inf where the mask (or NaN) leaves nothing.  The adjusted logits are
     not written."""
     import torch
-    M, N = _checked_logits(logits)
+    M, N, dev = _checked_logits(logits)
     if index is None and value is None:
         index, value = logits.new_empty(M, dtype=torch.int32), logits.new_empty(M)
     else:
         index = logits.new_empty(M, dtype=torch.int32) if index is None else index
         value = logits.new_empty(M) if value is None else value
         _check_outputs(logits, index, value, M)
-    rc = library().q4k_logits_argmax(logits.data_ptr(), adjustment._checked(logits, M, N), M, N, index.data_ptr(),
-                                     value.data_ptr(), _stream_for(logits, stream))
+    rc = library().q4k_logits_argmax(logits.data_ptr(), adjustment._checked(dev, M, N), M, N, index.data_ptr(),
+                                     value.data_ptr(), _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_logits_argmax")
     return index, value
@@ -403,24 +404,24 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, normalize: b
     ``sigmoid`` their sigmoid; ``bias`` float32 [E] takes part in the choice
     only; ``normalize`` divides a token's weights by their sum."""
     import torch
-    M, E = _checked_logits(logits)
+    M, E, dev = _checked_logits(logits)
     k = int(top_k)
     if not (1 <= E <= MAX_EXPERTS and 1 <= k <= min(E, MAX_TOP_K)):
         raise Q4KError(ERR_BAD_DIM, f"E={E} top_k={k}")
-    bias_ptr = None if bias is None else _checked_tensor("bias", bias, torch.float32, (E,), logits)
+    bias_ptr = None if bias is None else _checked_tensor("bias", bias, torch.float32, (E,), dev)
     if out is None:
         new = logits.new_empty
         out = Routing(new((M, k), dtype=torch.int32), new((M, k)), new(E + 1, dtype=torch.int32),
                       new(M * k, dtype=torch.int32))
     else:
-        _checked_tensor("expert", out.expert, torch.int32, (M, k), logits)
-        _checked_tensor("weight", out.weight, torch.float32, (M, k), logits)
-        _checked_tensor("offsets", out.offsets, torch.int32, (E + 1,), logits)
-        _checked_tensor("rows", out.rows, torch.int32, (M * k,), logits)
+        _checked_tensor("expert", out.expert, torch.int32, (M, k), dev)
+        _checked_tensor("weight", out.weight, torch.float32, (M, k), dev)
+        _checked_tensor("offsets", out.offsets, torch.int32, (E + 1,), dev)
+        _checked_tensor("rows", out.rows, torch.int32, (M * k,), dev)
     flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_NORMALIZE if normalize else 0)
     rc = library().q4k_moe_route(logits.data_ptr(), bias_ptr, M, E, k, flags, float(scale), out.expert.data_ptr(),
                                  out.weight.data_ptr(), out.offsets.data_ptr(), out.rows.data_ptr(),
-                                 _stream_for(logits, stream))
+                                 _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_moe_route")
     return out
@@ -439,7 +440,7 @@ def moe_group(expert, E: int, stream=None):
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
     offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
     rows = torch.empty(P, dtype=torch.int32, device=expert.device)
-    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(), _stream_for(expert, stream))
+    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(), _stream_for(expert.get_device(), stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_moe_group")
     return offsets, rows
@@ -458,15 +459,16 @@ def _grouped_checked(ws, x, offsets, rows, x_div):
         raise Q4KError(ERR_BAD_DIM, f"K={K}")
     if not 1 <= E <= MAX_EXPERTS:
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
+    dev = x.get_device()
     for w in ws:
-        _checked_tensor("w", w, torch.uint8, (E, N, K // BLOCK_WEIGHTS * BLOCK_BYTES), x)
-    _checked_tensor("offsets", offsets, torch.int32, (E + 1,), x)
+        _checked_tensor("w", w, torch.uint8, (E, N, K // BLOCK_WEIGHTS * BLOCK_BYTES), dev)
+    _checked_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     if x_div < 1:
         raise Q4KError(ERR_BAD_DIM, f"x_div={x_div}")
     if rows is None:
         return x.shape[0] * x_div, E, N, K, None
     P = rows.numel()
-    ptr = _checked_tensor("rows", rows, torch.int32, (P,), x)
+    ptr = _checked_tensor("rows", rows, torch.int32, (P,), dev)
     if (P + x_div - 1) // x_div != x.shape[0]:
         raise ValueError(f"x has {x.shape[0]} rows, expected {P} pairs / x_div {x_div}")
     return P, E, N, K, ptr
@@ -482,9 +484,9 @@ def matmul_grouped(w, x, offsets, rows=None, y=None, x_div: int = 1, stream=None
     if y is None:
         y = x.new_empty((P, N))
     else:
-        _checked_tensor("y", y, torch.float32, (P, N), x)
+        _checked_tensor("y", y, torch.float32, (P, N), x.get_device())
     rc = library().q4k_matmul_grouped(w.data_ptr(), x.data_ptr(), x_div, offsets.data_ptr(), rows_ptr, y.data_ptr(),
-                                      E, P, N, K, _stream_for(x, stream))
+                                      E, P, N, K, _stream_for(x.get_device(), stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped")
     return y
@@ -498,10 +500,10 @@ def matmul_grouped_swiglu(w_gate, w_up, x, offsets, rows=None, out=None, x_div: 
     if out is None:
         out = x.new_empty((P, N))
     else:
-        _checked_tensor("out", out, torch.float32, (P, N), x)
+        _checked_tensor("out", out, torch.float32, (P, N), x.get_device())
     rc = library().q4k_matmul_grouped_swiglu(w_gate.data_ptr(), w_up.data_ptr(), x.data_ptr(), x_div,
                                              offsets.data_ptr(), rows_ptr, out.data_ptr(), E, P, N, K,
-                                             _stream_for(x, stream))
+                                             _stream_for(x.get_device(), stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_swiglu")
     return out
@@ -516,15 +518,15 @@ def matmul_grouped_combine(w, x, routing: Routing, out=None, stream=None):
     if routing.expert.dim() != 2 or routing.expert.numel() != P:
         raise ValueError(f"expert must be [M, top_k] with {P} entries")
     M, top_k = routing.expert.shape
-    _checked_tensor("expert", routing.expert, torch.int32, (M, top_k), x)
-    _checked_tensor("weight", routing.weight, torch.float32, (M, top_k), x)
+    _checked_tensor("expert", routing.expert, torch.int32, (M, top_k), x.get_device())
+    _checked_tensor("weight", routing.weight, torch.float32, (M, top_k), x.get_device())
     if out is None:
         out = x.new_empty((M, N))
     else:
-        _checked_tensor("out", out, torch.float32, (M, N), x)
+        _checked_tensor("out", out, torch.float32, (M, N), x.get_device())
     rc = library().q4k_matmul_grouped_combine(w.data_ptr(), x.data_ptr(), routing.expert.data_ptr(),
                                               routing.weight.data_ptr(), routing.offsets.data_ptr(), rows_ptr,
-                                              out.data_ptr(), E, M, top_k, N, K, _stream_for(x, stream))
+                                              out.data_ptr(), E, M, top_k, N, K, _stream_for(x.get_device(), stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_combine")
     return out

@@ -137,11 +137,11 @@ def test_binding_refuses_before_any_call():
         q4k.Adjustment(bias_id=offsets)
     with pytest.raises(ValueError, match="history"):
         q4k.Adjustment(presence=torch.zeros(1))
-    like = torch.zeros(1)
+    dev = 0
     for bad in (dict(history=torch.zeros((2, 5), dtype=torch.int64)), dict(mask=torch.zeros((2, 2), dtype=torch.int16))):
         with pytest.raises(TypeError):
-            q4k.Adjustment(**bad)._checked(like, 2, 64)
+            q4k.Adjustment(**bad)._checked(dev, 2, 64)
     for bad in (dict(history=torch.zeros((3, 5), dtype=torch.int32)), dict(mask=torch.zeros((2, 1), dtype=torch.int32)),
                 dict(history=torch.zeros((2, 5), dtype=torch.int32))):
         with pytest.raises(ValueError):
-            q4k.Adjustment(**bad)._checked(like, 2, 64)
+            q4k.Adjustment(**bad)._checked(dev, 2, 64)
