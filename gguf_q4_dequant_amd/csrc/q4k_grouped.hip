@@ -428,27 +428,14 @@ __device__ __forceinline__ void store_row(const Grouped &g, int p, float back, i
     }
 }
 
-template <int RT, int NC, bool kSwiglu>
-__global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
-    using L = TileLds<RT, NC>;
-    using W = WTile<NC, kSwiglu>;
-    extern __shared__ __align__(16) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// The arithmetic of one tile over its first RT row tiles of 16.
+template <int RT, class L, int NC, bool kSwiglu>
+__device__ __forceinline__ void run_tile(const Grouped &g, const Tile &t, const WTile<NC, kSwiglu> &w, uint8_t *lds, int wave,
+                                         int lane, int n0) {
     const int c16 = lane & 15, quarter = lane >> 4;
-    Tiles<L::kRows> tiles(g.offsets, g.E, g.P, lane);
-    const int n_tiles = (g.N - 1) / (4 * W::kN) + 1;
-    const int at = place_in_work(blockIdx.x, tiles.total(), n_tiles);
-    if (at < 0) return;
-    const Tile t = tiles.find(at / n_tiles);
-    if (t.count == 0) return;
-    const int n0 = (at % n_tiles * 4 + wave) * W::kN;
-    uint8_t *const wslot = lds + L::kWAt + wave * L::kW;
-    const W w(g, t.e, n0, wslot, lane);
-    w.copy(0);
-    int *pairs = reinterpret_cast<int *>(lds + L::kPairsAt);
-    float *back = reinterpret_cast<float *>(lds + L::kBackAt);
-    load_pairs(g, t, L::kRows, pairs, back);
-    __syncthreads();
+    const int *pairs = reinterpret_cast<const int *>(lds + L::kPairsAt);
+    const float *back = reinterpret_cast<const float *>(lds + L::kBackAt);
+    const uint8_t *const wslot = lds + L::kWAt + wave * L::kW;
     const int KB = g.K / kBlockWeights;
 
     // x: this wave copies rows 4 RT wave .. + 4 RT of the tile, four per
@@ -564,6 +551,29 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
             for (int c = 0; c < NC; ++c) v[c] = acc[r][c][k];
             store_row<NC, kSwiglu>(g, p, back[i], n0, c16, v);
         }
+}
+
+template <int RT, int NC, bool kSwiglu>
+__global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
+    using L = TileLds<RT, NC>;
+    using W = WTile<NC, kSwiglu>;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Tiles<L::kRows> tiles(g.offsets, g.E, g.P, lane);
+    const int n_tiles = (g.N - 1) / (4 * W::kN) + 1;
+    const int at = place_in_work(blockIdx.x, tiles.total(), n_tiles);
+    if (at < 0) return;
+    const Tile t = tiles.find(at / n_tiles);
+    if (t.count == 0) return;
+    const int n0 = (at % n_tiles * 4 + wave) * W::kN;
+    const W w(g, t.e, n0, lds + L::kWAt + wave * L::kW, lane);
+    w.copy(0);
+    load_pairs(g, t, L::kRows, reinterpret_cast<int *>(lds + L::kPairsAt), reinterpret_cast<float *>(lds + L::kBackAt));
+    __syncthreads();
+    const int active = (t.count + 15) / 16;  // uniform: a group's last tile takes the row tiles that it fills
+    if (active >= RT) run_tile<RT, L>(g, t, w, lds, wave, lane, n0);
+    else if (RT > 2 && active == 2) run_tile<2, L>(g, t, w, lds, wave, lane, n0);
+    else run_tile<1, L>(g, t, w, lds, wave, lane, n0);
 }
 
 // ---- up to about sixteen rows per expert ---------------------------------------
