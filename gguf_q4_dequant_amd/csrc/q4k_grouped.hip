@@ -762,7 +762,8 @@ __device__ __forceinline__ float dpp_move(float v) {
 }
 
 // Stages one super-block of four rows for the wave: lane 16r + p holds values
-// 16p .. 16p + 15 of row r.  The scale is per row and super-block here, so
+// 16p .. 16p + 15 of row r.  The four quarters' pieces of a step are exchanged
+// by the row's number, so that the rows read different banks.  The scale is per row and super-block here, so
 // that a wave needs nothing from the others.
 __device__ __forceinline__ void stage_few(const float4 v[4], int lane, uint8_t *base) {
     const int r = lane >> 4, p = lane & 15;
@@ -791,7 +792,7 @@ __device__ __forceinline__ void stage_few(const float4 v[4], int lane, uint8_t *
         }
         // k = 16p + 8u: quarter p / 4, half (p / 2) % 2, step pair 2 (p % 2) + u
         const int quarter = p >> 2, h = (p >> 1) & 1, i = 2 * (p & 1) + u;
-        uint8_t *o = base + FewLds::kXAt + r * kImageBlock + (2 * i + h) * 128 + quarter * 16;
+        uint8_t *o = base + FewLds::kXAt + r * kImageBlock + (2 * i + h) * 128 + (quarter ^ r) * 16;
         *reinterpret_cast<half8 *>(o) = hi;
         *reinterpret_cast<half8 *>(o + 64) = lo;
     }
@@ -856,7 +857,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
             half8 a[4];
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                a[s] = *reinterpret_cast<const half8 *>(base + FewLds::kXAt + arow * kImageBlock + (4 * i + s) * 64 + quarter * 16);
+                a[s] = *reinterpret_cast<const half8 *>(base + FewLds::kXAt + arow * kImageBlock + (4 * i + s) * 64 + (quarter ^ arow) * 16);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const uint4 qq = i < 2 ? wb[c].q0 : wb[c].q1;
