@@ -917,26 +917,25 @@ __global__ __launch_bounds__(256) void combine_kernel(const float *y, const int 
         float4u acc = {0.f, 0.f, 0.f, 0.f};
         const size_t p0 = static_cast<size_t>(m) * top_k;
         for (int j0 = 0; j0 < top_k; j0 += 8) {
+            // every choice's values are requested, and dropped where it has no expert
             float4u v[8];
             float w[8];
+            bool use[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const size_t p = p0 + min(j0 + i, top_k - 1);
-                const bool use = j0 + i < top_k && static_cast<unsigned>(expert[p]) < static_cast<unsigned>(E);
-                w[i] = use ? weight[p] : 0.f;
-                v[i] = float4u{0.f, 0.f, 0.f, 0.f};
-                if (use) {
-                    const float *src = y + p * N + n;
-                    if (n + 4 <= N) v[i] = *reinterpret_cast<const float4u *>(src);
-                    else
-                        for (int k = 0; k < 3; ++k)
-                            if (n + k < N) v[i][k] = src[k];
-                }
+                const float *src = y + p * N + n;
+                if (n + 4 <= N) v[i] = *reinterpret_cast<const float4u *>(src);
+                else
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[i][k] = src[min(k, N - 1 - n)];
+                use[i] = j0 + i < top_k && static_cast<unsigned>(expert[p]) < static_cast<unsigned>(E);
+                w[i] = weight[p];
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(w[i], v[i][k], acc[k]);
+                for (int k = 0; k < 4; ++k) acc[k] = use[i] ? __builtin_fmaf(w[i], v[i][k], acc[k]) : acc[k];
         }
         float *o = out + static_cast<size_t>(m) * N + n;
         if (n + 4 <= N) *reinterpret_cast<float4u *>(o) = acc;
@@ -1000,12 +999,19 @@ Variant choose(const Grouped &g, int *groups) {
     return thin <= tile ? Variant::kThin : Variant::kTile;
 }
 
+// No call has more tiles of `rows` rows: every group has at most one that is not
+// full, and every tile has a pair.
+int most_tiles(const Grouped &g, int rows) {
+    const int64_t tiles = static_cast<int64_t>(g.P) / rows + (g.E < g.P ? g.E : g.P);
+    return static_cast<int>(tiles < g.P ? tiles : g.P);
+}
+
 template <int WAVES, bool kSwiglu>
 hipError_t launch_few(const Grouped &g, const float *x, hipStream_t stream) {
     constexpr int kBytes = WAVES * FewLds::kWave, kTileN = kSwiglu ? 16 : 32;
     const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(few_kernel<WAVES, kSwiglu>), kBytes);
     if (err != hipSuccess) return err;
-    const dim3 grid((g.N + kTileN - 1) / kTileN, g.P / kFewRows + (g.E < g.P ? g.E : g.P));
+    const dim3 grid((g.N - 1) / kTileN + 1, most_tiles(g, kFewRows));
     hipLaunchKernelGGL((few_kernel<WAVES, kSwiglu>), grid, dim3(64 * WAVES), kBytes, stream, g, x);
     return hipGetLastError();
 }
@@ -1014,7 +1020,7 @@ hipError_t launch_tiles(void (*kernel)(Grouped), const Grouped &g, int rows, int
                         hipStream_t stream) {
     const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes);
     if (err != hipSuccess) return err;
-    const int64_t tiles = g.P / rows + (g.E < g.P ? g.E : g.P);
+    const int64_t tiles = most_tiles(g, rows);
     const int64_t blocks = (tiles * ((g.N - 1) / cols + 1) + 7) / 8 * 8;
     if (blocks > INT_MAX) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), bytes, stream, g);
