@@ -404,14 +404,14 @@ __device__ __forceinline__ int pair_of(const Grouped &g, const Tile &t, int i) {
     return static_cast<unsigned>(p) < static_cast<unsigned>(g.P) ? p : -1;
 }
 
-// The tile's pairs and the factors of their rows.
-__device__ __forceinline__ void load_pairs(const Grouped &g, const Tile &t, int rows, int *pairs, float *back) {
-    const int i = threadIdx.x;
-    if (i < rows) {
-        const int p = pair_of(g, t, i);
-        pairs[i] = p;
-        back[i] = g.x.back[max(p, 0) / g.x_div];
-    }
+// The tile's pairs.
+__device__ __forceinline__ void load_pairs(const Grouped &g, const Tile &t, int rows, int *pairs) {
+    if (threadIdx.x < rows) pairs[threadIdx.x] = pair_of(g, t, threadIdx.x);
+}
+// The factors of their rows, which only the end needs: asked for behind the
+// first copies of x, and there with the barrier that waits for those.
+__device__ __forceinline__ void load_factors(const Grouped &g, int rows, const int *pairs, float *back) {
+    if (threadIdx.x < rows) back[threadIdx.x] = g.x.back[max(pairs[threadIdx.x], 0) / g.x_div];
 }
 
 // Writes row i of the tile's columns: acc[c] for column n0 + 16c + c16
@@ -434,7 +434,7 @@ __device__ __forceinline__ void run_tile(const Grouped &g, const Tile &t, const 
                                          int lane, int n0) {
     const int c16 = lane & 15, quarter = lane >> 4;
     const int *pairs = reinterpret_cast<const int *>(lds + L::kPairsAt);
-    const float *back = reinterpret_cast<const float *>(lds + L::kBackAt);
+    float *back = reinterpret_cast<float *>(lds + L::kBackAt);
     const uint8_t *const wslot = lds + L::kWAt + wave * L::kW;
     const int KB = g.K / kBlockWeights;
 
@@ -470,6 +470,7 @@ __device__ __forceinline__ void run_tile(const Grouped &g, const Tile &t, const 
         for (int c = 0; c < NC; ++c) acc[r][c] = float4v{0.f, 0.f, 0.f, 0.f};
     copy_x(0, 0, 0);
     copy_sums(0);
+    load_factors(g, RT * 16, pairs, back);
     for (int b = 0; b < KB; ++b) {
         WScales ws[NC];
         float4v blk[RT][NC];
@@ -568,7 +569,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
     const int n0 = (at % n_tiles * 4 + wave) * W::kN;
     const W w(g, t.e, n0, lds + L::kWAt + wave * L::kW, lane);
     w.copy(0);
-    load_pairs(g, t, L::kRows, reinterpret_cast<int *>(lds + L::kPairsAt), reinterpret_cast<float *>(lds + L::kBackAt));
+    load_pairs(g, t, L::kRows, reinterpret_cast<int *>(lds + L::kPairsAt));
     __syncthreads();
     const int active = (t.count + 15) / 16;  // uniform: a group's last tile takes the row tiles that it fills
     if (active >= RT) run_tile<RT, L>(g, t, w, lds, wave, lane, n0);
@@ -638,7 +639,7 @@ __global__ __launch_bounds__(256 * KS, 4) void thin_kernel(Grouped g) {
     if (group < KB) w.copy(group);
     int *pairs = reinterpret_cast<int *>(all_lds + KS * L::kGroup);
     float *back = reinterpret_cast<float *>(pairs + 16);
-    load_pairs(g, t, 16, pairs, back);
+    load_pairs(g, t, 16, pairs);
     __syncthreads();
     // x: this wave copies rows 4 wave .. + 4, two per instruction, their pieces
     // exchanged by the row's number as in tile_kernel
@@ -671,6 +672,7 @@ __global__ __launch_bounds__(256 * KS, 4) void thin_kernel(Grouped g) {
         copy_x(group, 0);
         copy_sums(group, 0);
     }
+    load_factors(g, 16, pairs, back);
     int parity = 0;  // of the sums' buffers
     for (int b0 = 0; b0 < KB; b0 += KS, parity ^= 1) {
         const int b = b0 + group;
