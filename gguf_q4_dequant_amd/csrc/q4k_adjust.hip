@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBiases = 512;  // biases looked through at a time
+constexpr int kMaxList = 1 << 30;  // places in a list and one step behind its end stay in an int
 
 typedef int int4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef float float4u __attribute__((ext_vector_type(4), aligned(4)));  // rows of odd N start anywhere
@@ -223,7 +224,8 @@ bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) !
 int check_adjustment(const q4k_adjustment *a, int M, int N) {
     if (M < 0 || N < 0) return Q4K_ERR_BAD_DIM;
     if (!a) return Q4K_ERR_NULL;
-    if (a->history_len < 0 || a->bias_len < 0) return Q4K_ERR_BAD_DIM;
+    if (a->history_len < 0 || a->bias_len < 0 || a->history_len > kMaxList || a->bias_len > kMaxList)
+        return Q4K_ERR_BAD_DIM;
     if ((a->history_len > 0 && !a->history) || (a->bias_len > 0 && (!a->bias_id || !a->bias_value))) return Q4K_ERR_NULL;
     if (misaligned4(a->history) || misaligned4(a->repetition) || misaligned4(a->frequency) ||
         misaligned4(a->presence) || misaligned4(a->bias_id) || misaligned4(a->bias_value) || misaligned4(a->mask))

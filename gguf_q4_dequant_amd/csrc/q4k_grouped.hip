@@ -203,6 +203,7 @@ struct Tiles {
                 // the last lane with before <= t owns it
                 const int owner = 63 - __builtin_clzll(__ballot(before <= t));
                 int at = t - __builtin_amdgcn_readlane(before, owner);
+                if (at < 0) return {0, 0, 0};  // a table whose groups overlap may claim more tiles than an int counts
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = __builtin_amdgcn_readlane(count[i], owner), n = (c + TM - 1) / TM;

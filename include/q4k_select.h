@@ -47,7 +47,8 @@ typedef struct q4k_adjustment {
 
 /* out[m, n] = the adjusted logit.  logits and out: DEVICE float32 [M, N],
  * 4-byte aligned; out may be logits itself (any other overlap is not allowed).
- *   Errors: M, N, history_len or bias_len negative: Q4K_ERR_BAD_DIM; logits,
+ *   Errors: M, N, history_len or bias_len negative, or one of the last two
+ *   above 2^30: Q4K_ERR_BAD_DIM; logits,
  *   out or the struct NULL, history NULL with history_len > 0, bias_id or
  *   bias_value NULL with bias_len > 0: Q4K_ERR_NULL; Q4K_ERR_ALIGN; M above
  *   65535: Q4K_ERR_LAUNCH.  M == 0 or N == 0 is a no-op. */

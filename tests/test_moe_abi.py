@@ -98,6 +98,8 @@ def test_selection_refusals(lib):
         assert call(a=None) == q4k.ERR_NULL
         assert call(a=struct(history_len=-1)) == q4k.ERR_BAD_DIM
         assert call(a=struct(bias_len=-1)) == q4k.ERR_BAD_DIM
+        assert call(a=struct(history_len=2 ** 30 + 1, history=A)) == q4k.ERR_BAD_DIM
+        assert call(a=struct(bias_len=2 ** 31 - 1, bias_id=A, bias_value=A)) == q4k.ERR_BAD_DIM
         assert call(a=struct(history_len=3)) == q4k.ERR_NULL
         assert call(a=struct(bias_len=3, bias_id=A)) == q4k.ERR_NULL
         for name in ("history", "repetition", "frequency", "presence", "bias_id", "bias_value", "mask"):

@@ -48,6 +48,16 @@ def test_route(M, E, k, sigmoid, normalize, bias):
     _check_route(logits, k, b, sigmoid, normalize, scale=1.0 if normalize else 2.5)
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M,E,k", [(16, 300, 64), (17, 300, 2), (48, 513, 7), (49, 513, 7), (2, 1024, 64), (16, 1024, 1)])
+def test_route_around_the_change_of_kernels(M, E, k, bias):
+    g = _rng(8, M, E, k)
+    logits = (2.0 * g.standard_normal((M, E))).astype(np.float32)
+    _check_route(logits, k, (0.2 * g.standard_normal(E)).astype(np.float32) if bias else None, sigmoid=bias)
+    # few different scores: every choice is among equals
+    _check_route(np.round(logits), k, np.zeros(E, np.float32) if bias else None, sigmoid=not bias)
+
+
 @pytest.mark.parametrize("M", [5, 200])
 @pytest.mark.parametrize("bias", [False, True])
 def test_route_equal_scores_go_to_the_lower_expert(M, bias):
