@@ -587,7 +587,7 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
 // workgroup within a quarter of the LDS, and four to a CU.  Where the tiles
 // leave CUs idle, KS such groups of four waves split K by super-blocks (group s
 // takes blocks s, s + KS, ...), and the first adds the others' sums in order:
-// 64 pairs over 8 experts of 1024 x 2048 16.1 -> 14.0 us.  (Staging x inside
+// 64 pairs over 8 experts of 1024 x 2048 15.5 -> 13.6 us.  (Staging x inside
 // this kernel instead of by a launch of its own was slower: 32 against 29 us
 // for 48 x 8 rows over 64 experts of 2048 x 1024, 66 against 48 us at 128 x 8.)
 template <int NC>
@@ -980,14 +980,18 @@ enum class Variant { kFew, kThin, kTile, kLargeTile };
 // tile's own time over its K blocks, and 5 us is the staging launch that tiles
 // of four rows do without.  Measured, rows of four / of sixteen / of 32 rows by
 // 128 columns, in us:
-//     64 experts of 1024 x 2048 (SwiGLU), 8 pairs a token: 1 token 8 / 15 / 21,
-//         4 tokens 25 / 23 / 28, 64 tokens 100 / 42 / 44, 256 tokens 332 / 73 / 65
-//     16 experts of 4096 x 2048, 2 pairs: 8 tokens 18 / 22 / 27, 128 tokens
-//         96 / 31 / 37, 256 tokens 172 / 43 / 43
-//     40 experts of 50 x 2560, 5 pairs, 242 tokens: 18 / 26 / 36
-// From 64 pairs per expert, where it still gives two workgroups to every CU,
-// 48 rows by 256 columns: 64 experts of 1024 x 2048 (SwiGLU), 256 rows each, 302
-// against 330 us; 16 of 4096 x 2048, 48 rows each, 56 against 48 us.
+//     64 experts of 1024 x 2048 (SwiGLU), 8 pairs a token: 1 token 8 / 13 / 18,
+//         4 tokens 24 / 21 / 23, 64 tokens 105 / 41 / 38, 256 tokens 343 / 72 / 64
+//     16 experts of 4096 x 2048, 2 pairs: 8 tokens 18 / 21 / 22, 128 tokens
+//         96 / 31 / 34, 256 tokens 176 / 41 / 42
+//     40 experts of 50 x 2560, 5 pairs, 242 tokens: 16 / 25 / 35
+// From 64 pairs per expert, and where that gives four workgroups to every CU
+// (two rounds of them), 48 rows by 256 columns; in us, against 32 by 128:
+//     64 experts of 1024 x 2048 (SwiGLU): 64 rows each 105 against 101, 128
+//         rows 165 / 173, 256 rows 302 / 321
+//     16 experts of 4096 x 2048: 128 rows each (811 workgroups) 105 / 96, 192
+//         (1152) 134 / 138, 256 rows 165 / 187, 500 rows 302 / 339
+//     2 experts of 2000 x 4096: 1000 rows each 101 / 93
 Variant choose(const Grouped &g, int *groups) {
     const double P = g.P, E = g.E, KB = g.K / kBlockWeights, columns = g.w2 ? 2.0 * g.N : g.N;
     const double used = P <= E / 8 ? P : E * (1.0 - exp(-P / E));
@@ -998,7 +1002,7 @@ Variant choose(const Grouped &g, int *groups) {
     const double thin = fmax(thin_workgroups * KB / 250, 3.0 * KB / *groups);
     const double tile = fmax(tiles(32) * ceil(columns / 128) * KB / 158, 1.9 * KB);
     if (few < 5 + fmin(thin, tile) && tiles(4) < 16384) return Variant::kFew;
-    if (P >= 64 * E && (P / 48 + 0.5 * E) * columns / 256 >= 512) return Variant::kLargeTile;
+    if (P >= 64 * E && (P / 48 + 0.5 * E) * columns / 256 >= 1024) return Variant::kLargeTile;
     return thin <= tile ? Variant::kThin : Variant::kTile;
 }
 

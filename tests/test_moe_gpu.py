@@ -172,7 +172,8 @@ def test_grouped_swiglu(sizes, N, K, x_div):
 # 32 x 128 and 48 x 256 tiles.  The groups' sizes are uneven and some are empty.
 @pytest.mark.parametrize("P,E,N,K", [(40, 2, 300, 512), (40, 2, 300, 1280), (200, 2, 1000, 1024), (400, 2, 1000, 512),
                                      (200, 24, 2600, 512), (3000, 2, 300, 512), (3000, 2, 2300, 256),
-                                     (900, 600, 40, 256), (5000, 300, 150, 256), (70, 1024, 33, 512)])
+                                     (900, 600, 40, 256), (5000, 300, 150, 256), (70, 1024, 33, 512),
+                                     (3000, 2, 5000, 256), (5000, 3, 2600, 512)])
 def test_every_kernel(P, E, N, K):
     import torch
     g = _rng(7, P, E)
