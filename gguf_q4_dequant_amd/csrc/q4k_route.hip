@@ -16,6 +16,14 @@
 // reads the whole table of choices: a ballot of "before my expert" gives the
 // group's offset, one of "my expert" the places.  Every workgroup reads all P
 // choices, but from the L2 and 64 at a time, and no counts cross workgroups.
+//
+// Both are bound by latency: one token over 128 experts, top 8, takes 5.7 us in
+// one launch; 4096 tokens over 256 experts (sigmoid and bias, top 8) 9.3 us for
+// the choices and 6.7 us for the groups, 4.6 MB in all.  Two launches take over
+// where a wave of the one workgroup would have a second token: 128 experts
+// without a bias, in graph replays: 16 tokens 6.8 us in one launch, 32 tokens
+// 9.7 in one against 7.7 in two; 256 experts under a bias 10.3 at 16 in one
+// against 9.2 at 17 in two.
 #include <math.h>
 
 #include "../../include/q4k_moe.h"
@@ -24,7 +32,7 @@
 namespace q4k {
 namespace {
 
-constexpr int kSingleTokens = 48;  // tokens routed and grouped by one workgroup (16 under a bias)
+constexpr int kSingleTokens = 16;  // tokens routed and grouped by one workgroup: one a wave
 constexpr int kSingleThreads = 1024;
 constexpr int kThreads = 256;
 
@@ -435,7 +443,7 @@ hipError_t launch_group(const int *expert, int P, int E, int *offsets, int *rows
 
 template <int VPL, bool kBias>
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-    if (a.M <= (kBias ? kSingleTokens / 3 : kSingleTokens)) {
+    if (a.M <= kSingleTokens) {
         constexpr int kThreads1 = kGroupThreads<VPL, kBias>, waves = kThreads1 / 64;
         const int bytes = (waves * a.E + a.E + 1 + a.M * a.top_k) * 4;
         const hipError_t err = allow_dynamic_lds(reinterpret_cast<const void *>(route_group_kernel<VPL, kBias>), 96 << 10);
