@@ -261,6 +261,13 @@ __device__ __forceinline__ uint64_t same_expert(int e, bool valid, int bits) {
 
 __device__ __forceinline__ uint64_t lanes_below(int lane) { return (1ull << lane) - 1; }
 
+// The waves of a workgroup that share [0, count) in chunks of 64: a few pairs
+// leave most of them, and their rows of hist, out.
+__device__ __forceinline__ int sharing_waves(int count, int waves) {
+    const int chunks = (count + 63) / 64, per = (chunks + waves - 1) / waves;
+    return (chunks + per - 1) / per;
+}
+
 // hist[wave][e] += pairs of expert e among this wave's share of [0, count).
 template <class F>
 __device__ __forceinline__ void count_pairs(F expert_of, int count, int E, int *hist) {
@@ -275,16 +282,17 @@ __device__ __forceinline__ void count_pairs(F expert_of, int count, int E, int *
     }
 }
 
-// Places the pairs of one workgroup: hist [waves][E] holds the counts of
-// count_pairs, tot [E + 1] is scratch, both in LDS.
+// Places the pairs of one workgroup: hist [sharing waves][E] holds the counts
+// of count_pairs, tot [E + 1] is scratch, both in LDS.
 template <class F>
 __device__ __forceinline__ void place_pairs(F expert_of, int count, int E, int *hist, int *tot, int *offsets,
                                             int *rows) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int sharing = sharing_waves(count, waves);
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int run = 0;
-        for (int w = 0; w < waves; ++w) {
+        for (int w = 0; w < sharing; ++w) {
             const int c = hist[w * E + e];
             hist[w * E + e] = run;
             run += c;
@@ -333,8 +341,8 @@ struct RouteArgs {
     float scale;
 };
 
-// One workgroup: routing and grouping.  LDS: hist [waves][E], tot [E + 1] and
-// the choices [M][top_k].
+// One workgroup: routing and grouping.  LDS: hist [sharing waves][E], tot
+// [E + 1] and the choices [M][top_k].
 // (Half the waves where sixteen scores a lane and their doubles need more than
 // a sixteenth of the registers.)
 template <int VPL, bool kBias>
@@ -344,8 +352,9 @@ template <int VPL, bool kBias>
 __global__ __launch_bounds__((kGroupThreads<VPL, kBias>)) void route_group_kernel(RouteArgs a) {
     extern __shared__ int lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    int *hist = lds, *tot = hist + waves * a.E, *chosen = tot + a.E + 1;
-    for (int i = threadIdx.x; i < waves * a.E; i += blockDim.x) hist[i] = 0;
+    const int count = a.M * a.top_k, counts = sharing_waves(count, waves) * a.E;
+    int *hist = lds, *tot = hist + counts, *chosen = tot + a.E + 1;
+    for (int i = threadIdx.x; i < counts; i += blockDim.x) hist[i] = 0;
     for (int m = wave; m < a.M; m += waves) {
         int e;
         float w;
@@ -357,7 +366,6 @@ __global__ __launch_bounds__((kGroupThreads<VPL, kBias>)) void route_group_kerne
         }
     }
     __syncthreads();
-    const int count = a.M * a.top_k;
     const auto expert_of = [&](int i) { return chosen[i]; };
     count_pairs(expert_of, count, a.E, hist);
     place_pairs(expert_of, count, a.E, hist, tot, a.offsets, a.rows);
