@@ -246,8 +246,11 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
         value = torch.empty(M, dtype=torch.float32, device=x.device)
     _check_outputs(x, index, value, M)
     if adjustment is not None:
-        rc = library().q4k_matmul_argmax_adjusted(w.data_ptr(), x.data_ptr(), adjustment._checked(x.get_device(), M, N), M, N, K,
-                                                  index.data_ptr(), value.data_ptr(), _stream_handle(stream))
+        dev = x.get_device()
+        if w.get_device() != dev:
+            raise ValueError(f"w must be on cuda:{dev}, as x is")
+        rc = library().q4k_matmul_argmax_adjusted(w.data_ptr(), x.data_ptr(), adjustment._checked(dev, M, N), M, N, K,
+                                                  index.data_ptr(), value.data_ptr(), _stream_for(dev, stream))
         if rc != OK:
             raise Q4KError(rc, "q4k_matmul_argmax_adjusted")
         return index, value
@@ -440,7 +443,8 @@ def moe_group(expert, E: int, stream=None):
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
     offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
     rows = torch.empty(P, dtype=torch.int32, device=expert.device)
-    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(), _stream_for(expert.get_device(), stream))
+    rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(),
+                                 _stream_for(expert.get_device(), stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_moe_group")
     return offsets, rows

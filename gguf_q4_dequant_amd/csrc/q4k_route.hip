@@ -17,12 +17,12 @@
 // group's offset, one of "my expert" the places.  Every workgroup reads all P
 // choices, but from the L2 and 64 at a time, and no counts cross workgroups.
 //
-// Both are bound by latency: one token over 128 experts, top 8, takes 5.7 us in
+// Both are bound by latency: one token over 128 experts, top 8, takes 5.5 us in
 // one launch; 4096 tokens over 256 experts (sigmoid and bias, top 8) 9.3 us for
 // the choices and 6.7 us for the groups, 4.6 MB in all.  Two launches take over
 // where a wave of the one workgroup would have a second token: 128 experts
-// without a bias, in graph replays: 16 tokens 6.8 us in one launch, 32 tokens
-// 9.7 in one against 7.7 in two; 256 experts under a bias 10.3 at 16 in one
+// without a bias, in graph replays: 16 tokens 6.7 us in one launch, 32 tokens
+// 9.7 in one against 7.7 in two; 256 experts under a bias 10.0 at 16 in one
 // against 9.2 at 17 in two.
 #include <math.h>
 
