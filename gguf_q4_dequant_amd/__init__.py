@@ -340,12 +340,12 @@ class Adjustment:
 
 def _checked_logits(logits):
     import torch
-    if logits.dim() != 2 or logits.dtype != torch.float32:
+    shape, dev = logits.shape, logits.get_device()
+    if len(shape) != 2 or logits.dtype is not torch.float32:
         raise TypeError("logits must be float32 [M, N]")
-    if not logits.is_cuda or not logits.is_contiguous():
+    if dev < 0 or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous device tensor")
-    M, N = logits.shape
-    return M, N, logits.get_device()
+    return shape[0], shape[1], dev
 
 
 def logits_adjust(logits, adjustment, out=None, stream=None):
@@ -413,9 +413,8 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, normalize: b
         raise Q4KError(ERR_BAD_DIM, f"E={E} top_k={k}")
     bias_ptr = None if bias is None else _checked_tensor("bias", bias, torch.float32, (E,), dev)
     if out is None:
-        new = logits.new_empty
-        out = Routing(new((M, k), dtype=torch.int32), new((M, k)), new(E + 1, dtype=torch.int32),
-                      new(M * k, dtype=torch.int32))
+        expert, weight = logits.new_empty((M, k), dtype=torch.int32), logits.new_empty((M, k))
+        out = Routing(expert, weight, expert.new_empty(E + 1), expert.new_empty(M * k))
     else:
         _checked_tensor("expert", out.expert, torch.int32, (M, k), dev)
         _checked_tensor("weight", out.weight, torch.float32, (M, k), dev)
@@ -451,31 +450,33 @@ def moe_group(expert, E: int, stream=None):
 
 
 def _grouped_checked(ws, x, offsets, rows, x_div):
-    """Validate the operands of a grouped product; returns (P, E, N, K, rows pointer)."""
+    """Validate the operands of a grouped product; returns (P, E, N, K, their GPU,
+    addresses of the matrices, of offsets and of rows)."""
     import torch
-    if x.dtype != torch.float32 or x.dim() != 2 or any(w.dtype != torch.uint8 or w.dim() != 3 for w in ws):
+    w_shape, x_shape = ws[0].shape, x.shape
+    if x.dtype is not torch.float32 or len(x_shape) != 2 or len(w_shape) != 3 or ws[0].dtype is not torch.uint8:
         raise TypeError("expected w uint8 [E, N, K/256*144] and x float32 [rows, K]")
-    if not (x.is_cuda and x.is_contiguous()):
+    dev = x.get_device()
+    if dev < 0 or not x.is_contiguous():
         raise ValueError("x must be a contiguous device tensor")
-    E, N, row_bytes = ws[0].shape
-    K = x.shape[1]
+    E, N, _ = w_shape
+    x_rows, K = x_shape
     if K % BLOCK_WEIGHTS != 0 or K == 0:
         raise Q4KError(ERR_BAD_DIM, f"K={K}")
     if not 1 <= E <= MAX_EXPERTS:
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
-    dev = x.get_device()
-    for w in ws:
-        _checked_tensor("w", w, torch.uint8, (E, N, K // BLOCK_WEIGHTS * BLOCK_BYTES), dev)
-    _checked_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     if x_div < 1:
         raise Q4KError(ERR_BAD_DIM, f"x_div={x_div}")
+    shape = (E, N, K // BLOCK_WEIGHTS * BLOCK_BYTES)
+    w_ptrs = [_checked_tensor("w", w, torch.uint8, shape, dev) for w in ws]
+    offsets_ptr = _checked_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     if rows is None:
-        return x.shape[0] * x_div, E, N, K, None
+        return x_rows * x_div, E, N, K, dev, w_ptrs, offsets_ptr, None
     P = rows.numel()
-    ptr = _checked_tensor("rows", rows, torch.int32, (P,), dev)
-    if (P + x_div - 1) // x_div != x.shape[0]:
-        raise ValueError(f"x has {x.shape[0]} rows, expected {P} pairs / x_div {x_div}")
-    return P, E, N, K, ptr
+    rows_ptr = _checked_tensor("rows", rows, torch.int32, (P,), dev)
+    if (P + x_div - 1) // x_div != x_rows:
+        raise ValueError(f"x has {x_rows} rows, expected {P} pairs / x_div {x_div}")
+    return P, E, N, K, dev, w_ptrs, offsets_ptr, rows_ptr
 
 
 def matmul_grouped(w, x, offsets, rows=None, y=None, x_div: int = 1, stream=None):
@@ -484,13 +485,13 @@ def matmul_grouped(w, x, offsets, rows=None, y=None, x_div: int = 1, stream=None
     [P, N].  Rows of pairs in no group are left as they were (in a ``y`` made
     here they hold nothing meaningful).  rows None: pairs already in expert order."""
     import torch
-    P, E, N, K, rows_ptr = _grouped_checked((w,), x, offsets, rows, x_div)
+    P, E, N, K, dev, (w_ptr,), offsets_ptr, rows_ptr = _grouped_checked((w,), x, offsets, rows, x_div)
     if y is None:
         y = x.new_empty((P, N))
     else:
-        _checked_tensor("y", y, torch.float32, (P, N), x.get_device())
-    rc = library().q4k_matmul_grouped(w.data_ptr(), x.data_ptr(), x_div, offsets.data_ptr(), rows_ptr, y.data_ptr(),
-                                      E, P, N, K, _stream_for(x.get_device(), stream))
+        _checked_tensor("y", y, torch.float32, (P, N), dev)
+    rc = library().q4k_matmul_grouped(w_ptr, x.data_ptr(), x_div, offsets_ptr, rows_ptr, y.data_ptr(), E, P, N, K,
+                                      _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped")
     return y
@@ -500,14 +501,13 @@ def matmul_grouped_swiglu(w_gate, w_up, x, offsets, rows=None, out=None, x_div: 
     """out[p] = silu(x[p // x_div] . dequant(w_gate[e])^T) * (x[p // x_div] . dequant(w_up[e])^T)
     for every pair p of group e; arguments as for matmul_grouped."""
     import torch
-    P, E, N, K, rows_ptr = _grouped_checked((w_gate, w_up), x, offsets, rows, x_div)
+    P, E, N, K, dev, w_ptrs, offsets_ptr, rows_ptr = _grouped_checked((w_gate, w_up), x, offsets, rows, x_div)
     if out is None:
         out = x.new_empty((P, N))
     else:
-        _checked_tensor("out", out, torch.float32, (P, N), x.get_device())
-    rc = library().q4k_matmul_grouped_swiglu(w_gate.data_ptr(), w_up.data_ptr(), x.data_ptr(), x_div,
-                                             offsets.data_ptr(), rows_ptr, out.data_ptr(), E, P, N, K,
-                                             _stream_for(x.get_device(), stream))
+        _checked_tensor("out", out, torch.float32, (P, N), dev)
+    rc = library().q4k_matmul_grouped_swiglu(*w_ptrs, x.data_ptr(), x_div, offsets_ptr, rows_ptr, out.data_ptr(),
+                                             E, P, N, K, _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_swiglu")
     return out
@@ -518,19 +518,20 @@ def matmul_grouped_combine(w, x, routing: Routing, out=None, stream=None):
     the experts' down projections and each token's weighted sum; x float32
     [M * top_k, K], out float32 [M, N]."""
     import torch
-    P, E, N, K, rows_ptr = _grouped_checked((w,), x, routing.offsets, routing.rows, 1)
-    if routing.expert.dim() != 2 or routing.expert.numel() != P:
+    expert, weight, offsets, rows = routing
+    P, E, N, K, dev, (w_ptr,), offsets_ptr, rows_ptr = _grouped_checked((w,), x, offsets, rows, 1)
+    choices = expert.shape
+    if len(choices) != 2 or choices[0] * choices[1] != P:
         raise ValueError(f"expert must be [M, top_k] with {P} entries")
-    M, top_k = routing.expert.shape
-    _checked_tensor("expert", routing.expert, torch.int32, (M, top_k), x.get_device())
-    _checked_tensor("weight", routing.weight, torch.float32, (M, top_k), x.get_device())
+    M, top_k = choices
+    expert_ptr = _checked_tensor("expert", expert, torch.int32, choices, dev)
+    weight_ptr = _checked_tensor("weight", weight, torch.float32, choices, dev)
     if out is None:
         out = x.new_empty((M, N))
     else:
-        _checked_tensor("out", out, torch.float32, (M, N), x.get_device())
-    rc = library().q4k_matmul_grouped_combine(w.data_ptr(), x.data_ptr(), routing.expert.data_ptr(),
-                                              routing.weight.data_ptr(), routing.offsets.data_ptr(), rows_ptr,
-                                              out.data_ptr(), E, M, top_k, N, K, _stream_for(x.get_device(), stream))
+        _checked_tensor("out", out, torch.float32, (M, N), dev)
+    rc = library().q4k_matmul_grouped_combine(w_ptr, x.data_ptr(), expert_ptr, weight_ptr, offsets_ptr, rows_ptr,
+                                              out.data_ptr(), E, M, top_k, N, K, _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_combine")
     return out
