@@ -258,6 +258,23 @@ def test_rows_may_be_left_out_when_pairs_come_in_expert_order():
     check_close(y.cpu().numpy(), want, s, ref.product_tol(768))
 
 
+def test_empty_calls_do_nothing():
+    import torch
+    dev = device()
+    w, x = to_dev(_weights(3, 20, 256, 16)), torch.empty((0, 256), device=dev)
+    r = q4k.moe_route(torch.empty((0, 3), device=dev), 2)
+    assert q4k.matmul_grouped(w, x, r.offsets, r.rows).shape == (0, 20)
+    assert q4k.matmul_grouped_swiglu(w, w, x, r.offsets, r.rows, x_div=2).shape == (0, 20)
+    assert q4k.matmul_grouped_combine(w, x, r).shape == (0, 20)
+    full = q4k.moe_route(torch.zeros((4, 3), device=dev), 2)
+    assert q4k.matmul_grouped(w[:, :0].contiguous(), torch.zeros((4, 256), device=dev), full.offsets, full.rows,
+                              x_div=2).shape == (8, 0)
+    # groups that are all empty: no row is written
+    y = torch.full((8, 20), 7.0, device=dev)
+    q4k.matmul_grouped(w, torch.zeros((4, 256), device=dev), r.offsets, full.rows, y=y, x_div=2)
+    assert bool((y == 7.0).all())
+
+
 @pytest.mark.parametrize("sizes", [[2, 1], [40, 3], [200, 9]], ids=str)
 def test_unusual_activations(sizes):
     """Zero rows, tiny and huge magnitudes, and a row with NaN or infinity, which

@@ -193,3 +193,12 @@ def test_greedy_steps_captured_and_replayed():
     c["history"] = a.history.cpu().numpy()
     wi, wv = choice(plain(logits, **c), c["mask"])
     assert np.array_equal(q4k.matmul_argmax(w, x, adjustment=a)[0].cpu().numpy(), wi)
+
+
+def test_no_rows():
+    import torch
+    z = torch.empty((0, 40), device=device())
+    mask = torch.empty((0, 2), dtype=torch.int32, device=device())
+    assert q4k.logits_adjust(z, q4k.Adjustment(mask=mask)).shape == (0, 40)
+    index, value = q4k.logits_argmax(z, q4k.Adjustment(mask=mask))
+    assert index.shape == (0,) and value.shape == (0,)
