@@ -599,7 +599,10 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Grouped g) {
 // 64 pairs over 8 experts of 1024 x 2048 15.5 -> 13.6 us.  (Staging x inside
 // this kernel instead of by a launch of its own was slower: 32 against 29 us
 // for 48 x 8 rows over 64 experts of 2048 x 1024, 66 against 48 us at 128 x 8.)
-// Bound by the stream of W: those 48 x 8 rows read 75 MB in 20 us, 3.7 TB/s.
+// Bound by the stream of W: those 48 x 8 rows read 75 MB in 20 us (3.7 TB/s, one
+// round of workgroups, its start and end with it), 32 x 8 rows over 64 experts of
+// 2 x 1024 x 2048 read 151 MB in 29 us (5.2 TB/s); copying only the rows of x that
+// a tile has changed neither.
 template <int NC>
 struct ThinLds {
     static constexpr int kX = 16 * kImageBlock / 2, kSums = 16 * kSumsBlock, kW = 16 * NC * kBlockBytes;
