@@ -34,6 +34,7 @@
 
 #include "../../include/q4k_moe.h"
 #include "q4k_internal.h"
+#include "q4k_rows.h"
 
 namespace q4k {
 namespace {
@@ -350,7 +351,8 @@ __device__ __forceinline__ void barrier() {
 // A wave's 16 NC rows of W, copied to its own LDS slot one super-block at a
 // time, 144 bytes a row: two halves of 8 NC rows (SwiGLU: gate and up), row
 // 16c + r of the slot being column r of the wave's column tile c.  Rows behind
-// N read zeros.
+// N read zeros, or row N - 1 where a half has no other; their columns are never
+// stored.  (No copy is left out: the waits count them.)
 template <int NC, bool kSwiglu>
 struct WTile {
     static constexpr int kHalfRows = 8 * NC, kPieces = 9 * kHalfRows, kCopies = (kPieces + 63) / 64;
@@ -372,9 +374,9 @@ struct WTile {
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int first = min(n0 + (kSwiglu ? 0 : kHalfRows * h), g.N), rows = min(kHalfRows, g.N - first);
-            buf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(e) * g.N + first) * row_bytes,
-                               rows * row_bytes);
+            const RowWindow r = row_window(n0 + (kSwiglu ? 0 : kHalfRows * h), kHalfRows, g.N);
+            buf[h] = buffer_at((kSwiglu && h ? g.w2 : g.w) + (static_cast<size_t>(e) * g.N + r.first) * row_bytes,
+                               r.rows * row_bytes);
         }
     }
     __device__ __forceinline__ void copy(int b) const {
