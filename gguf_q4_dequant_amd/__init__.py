@@ -53,12 +53,13 @@ PATH_DECODE = 1
 PATH_PREFILL = 2
 PATH_GEMV = 3
 
-# Exported symbols of libq4k.so, as declared in include/q4k.h.
+# Exported symbols of libq4k.so, as declared in the headers under include/.
 EXPORTED = ("q4k_matmul", "q4k_matmul_batched", "q4k_matmul_path", "q4k_matmul_batched_path",
             "q4k_matmul_batched_noalloc", "q4a_matmul", "q4a_matmul_batched",
             "q4k_matmul_argmax", "q4k_matmul_swiglu", "q4k_gguf_list", "q4k_select_path", "q4k_strerror",
             "q4k_version", "q4k_moe_route", "q4k_moe_group", "q4k_matmul_grouped", "q4k_matmul_grouped_swiglu",
-            "q4k_matmul_grouped_combine", "q4k_logits_adjust", "q4k_logits_argmax", "q4k_matmul_argmax_adjusted")
+            "q4k_matmul_grouped_combine", "q4k_grouped_tile", "q4k_logits_adjust", "q4k_logits_argmax",
+            "q4k_matmul_argmax_adjusted")
 
 
 class Q4KError(RuntimeError):
@@ -125,6 +126,8 @@ def library() -> ctypes.CDLL:
     lib.q4k_matmul_grouped_swiglu.restype = ci
     lib.q4k_matmul_grouped_combine.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
     lib.q4k_matmul_grouped_combine.restype = ci
+    lib.q4k_grouped_tile.argtypes = [ci, ci, ci, ci, ci, ctypes.POINTER(ci)]
+    lib.q4k_grouped_tile.restype = ci
     lib.q4k_logits_adjust.argtypes = [vp, vp, adj, ci, ci, vp]
     lib.q4k_logits_adjust.restype = ci
     lib.q4k_logits_argmax.argtypes = [vp, adj, ci, ci, vp, vp, vp]
@@ -535,6 +538,17 @@ def matmul_grouped_combine(w, x, routing: Routing, out=None, stream=None):
     if rc != OK:
         raise Q4KError(rc, "q4k_matmul_grouped_combine")
     return out
+
+
+def grouped_tile(E: int, P: int, N: int, K: int, swiglu: bool = False) -> Tuple[int, int]:
+    """(rows, parts) of the kernel that a grouped product of these sizes runs: tiles
+    of 4, 16, 32 or 48 rows (0: nothing to compute), K split into ``parts`` within
+    a workgroup (q4k_grouped_tile)."""
+    parts = ctypes.c_int(0)
+    rows = library().q4k_grouped_tile(E, P, N, K, int(swiglu), ctypes.byref(parts))
+    if rows < 0:
+        raise Q4KError(rows, "q4k_grouped_tile")
+    return rows, parts.value
 
 
 def matmul_swiglu(w_gate, w_up, x, out=None, stream=None):

@@ -974,12 +974,20 @@ int status(hipError_t err) {
     return err == hipSuccess ? Q4K_OK : Q4K_ERR_LAUNCH;
 }
 
-int check_grouped(const void *w, const void *w2, const float *x, int x_div, const int *offsets, const int *rows,
-                  const float *y, int E, int P, int N, int K) {
-    if (E < 1 || E > Q4K_MAX_EXPERTS || P < 0 || N < 0 || K < 0 || x_div < 1) return Q4K_ERR_BAD_DIM;
+int check_sizes(int E, int P, int N, int K) {
+    if (E < 1 || E > Q4K_MAX_EXPERTS || P < 0 || N < 0 || K < 0) return Q4K_ERR_BAD_DIM;
     if (P == 0 || N == 0) return Q4K_OK;
     // 32 rows of W are addressed as one buffer of 32-bit offsets
     if (K == 0 || K % kBlockWeights != 0 || K > (1 << 26)) return Q4K_ERR_BAD_DIM;
+    return Q4K_OK;
+}
+
+int check_grouped(const void *w, const void *w2, const float *x, int x_div, const int *offsets, const int *rows,
+                  const float *y, int E, int P, int N, int K) {
+    const int rc = check_sizes(E, P, N, K);
+    if (rc != Q4K_OK) return rc;
+    if (x_div < 1) return Q4K_ERR_BAD_DIM;
+    if (P == 0 || N == 0) return Q4K_OK;
     if (!w || !w2 || !x || !offsets || !y) return Q4K_ERR_NULL;
     if (misaligned(w, 16) || misaligned(w2, 16) || misaligned(x, 16) || misaligned(y, 16) || misaligned(offsets, 4) ||
         misaligned(rows, 4))
@@ -987,10 +995,10 @@ int check_grouped(const void *w, const void *w2, const float *x, int x_div, cons
     return Q4K_OK;
 }
 
-enum class Variant { kFew, kThin, kTile, kLargeTile };
+enum class Variant { kFew = kFewRows, kThin = 16, kTile = 32, kLargeTile = 48 };  // the rows of a tile
 
-// The kernel for a call, from what the host knows (the groups' sizes are on
-// the device): P pairs over E experts.  Expected times in us, of a pair of
+// The kernel for a call, and the parts its workgroups split K into, from what
+// the host knows (the groups' sizes are on the device): P pairs over E experts.  Expected times in us, of a pair of
 // expected tile counts: with the pairs spread evenly E (1 - exp(-P / E))
 // experts are in use, and tiles of r rows are that many and one more for every
 // r pairs above half a tile each.  The unit of work is a super-block of one
@@ -1011,18 +1019,22 @@ enum class Variant { kFew, kThin, kTile, kLargeTile };
 //     16 experts of 4096 x 2048: 128 rows each (811 workgroups) 105 / 96, 192
 //         (1152) 134 / 138, 256 rows 165 / 187, 500 rows 302 / 339
 //     2 experts of 2000 x 4096: 1000 rows each 101 / 93
-Variant choose(const Grouped &g, int *groups) {
-    const double P = g.P, E = g.E, KB = g.K / kBlockWeights, columns = g.w2 ? 2.0 * g.N : g.N;
+Variant choose(int pairs, int experts, int N, int K, bool swiglu, int *parts) {
+    const double P = pairs, E = experts, KB = K / kBlockWeights, columns = swiglu ? 2.0 * N : N;
     const double used = P <= E / 8 ? P : E * (1.0 - exp(-P / E));
     const auto tiles = [&](double rows) { return used + fmax(0.0, P / rows - 0.5 * used); };
     const double thin_workgroups = tiles(16) * ceil(columns / 128);
-    *groups = thin_workgroups <= 256 && KB >= 4 ? 4 : thin_workgroups <= 512 && KB >= 2 ? 2 : 1;
+    const int groups = thin_workgroups <= 256 && KB >= 4 ? 4 : thin_workgroups <= 512 && KB >= 2 ? 2 : 1;
     const double few = tiles(4) * ceil(columns / 32) * KB / 750;
-    const double thin = fmax(thin_workgroups * KB / 250, 3.0 * KB / *groups);
+    const double thin = fmax(thin_workgroups * KB / 250, 3.0 * KB / groups);
     const double tile = fmax(tiles(32) * ceil(columns / 128) * KB / 158, 1.9 * KB);
+    *parts = KB > 4 ? 8 : 4;
     if (few < 5 + fmin(thin, tile) && tiles(4) < 16384) return Variant::kFew;
+    *parts = 1;
     if (P >= 64 * E && (P / 48 + 0.5 * E) * columns / 256 >= 1024) return Variant::kLargeTile;
-    return thin <= tile ? Variant::kThin : Variant::kTile;
+    if (thin > tile) return Variant::kTile;
+    *parts = groups;
+    return Variant::kThin;
 }
 
 // No call has more tiles of `rows` rows: every group has at most one that is not
@@ -1068,11 +1080,11 @@ hipError_t launch_thin(const Grouped &g, hipStream_t stream) {
 // Stages x, then the products.  g.x is filled in here.
 hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     const size_t xrows = (static_cast<size_t>(g.P) + g.x_div - 1) / g.x_div, KB = g.K / kBlockWeights;
-    int groups = 1;
-    const Variant variant = choose(g, &groups);
+    int parts = 1;
+    const Variant variant = choose(g.P, g.E, g.N, g.K, g.w2 != nullptr, &parts);
     if (variant == Variant::kFew) {
-        if (g.w2) return KB > 4 ? launch_few<8, true>(g, x, stream) : launch_few<4, true>(g, x, stream);
-        return KB > 4 ? launch_few<8, false>(g, x, stream) : launch_few<4, false>(g, x, stream);
+        if (g.w2) return parts == 8 ? launch_few<8, true>(g, x, stream) : launch_few<4, true>(g, x, stream);
+        return parts == 8 ? launch_few<8, false>(g, x, stream) : launch_few<4, false>(g, x, stream);
     }
     float *ws = nullptr;
     hipError_t err = workspace(stream, xrows * (KB * (kImageBlock + kSumsBlock) + 16), &ws);
@@ -1087,9 +1099,9 @@ hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
     if (err != hipSuccess) return err;
     switch (variant) {
     case Variant::kThin:
-        return groups == 4   ? launch_thin<2, 4>(g, stream)
-               : groups == 2 ? launch_thin<2, 2>(g, stream)
-                             : launch_thin<2, 1>(g, stream);
+        return parts == 4   ? launch_thin<2, 4>(g, stream)
+               : parts == 2 ? launch_thin<2, 2>(g, stream)
+                            : launch_thin<2, 1>(g, stream);
     case Variant::kTile: return launch_tile<2, 2>(g, stream);
     default: return launch_tile<3, 4>(g, stream);
     }
@@ -1097,6 +1109,17 @@ hipError_t run_grouped(Grouped g, const float *x, hipStream_t stream) {
 
 }  // namespace
 }  // namespace q4k
+
+extern "C" int q4k_grouped_tile(int E, int P, int N, int K, int swiglu, int *parts) {
+    using namespace q4k;
+    if (parts) *parts = 0;
+    const int rc = check_sizes(E, P, N, K);
+    if (rc != Q4K_OK || P == 0 || N == 0) return rc;
+    int split = 1;
+    const int rows = static_cast<int>(choose(P, E, N, K, swiglu != 0, &split));
+    if (parts) *parts = split;
+    return rows;
+}
 
 extern "C" int q4k_matmul_grouped(const void *w_packed, const float *x, int x_div, const int *offsets,
                                   const int *rows, float *y, int E, int P, int N, int K, hipStream_t stream) {

@@ -122,6 +122,17 @@ int q4k_matmul_grouped_combine(const void *w_packed, const float *x, const int *
                                const int *offsets, const int *rows, float *out, int E, int M, int top_k, int N,
                                int K, hipStream_t stream);
 
+/* The kernel that a grouped product of these sizes runs, for tests and
+ * benchmarks (as q4k_select_path is for q4k_matmul): the rows of its tiles, 4,
+ * 16, 32 or 48, and in *parts (HOST, may be NULL) the parts into which a
+ * workgroup splits K, one for each of its waves (4 rows: 4 or 8) or of its groups
+ * of four waves (16 rows: 1, 2 or 4; otherwise 1).  swiglu != 0: the gate/up
+ * form.  The weighted sum's product is the plain one of P = M * top_k pairs.
+ * Tiles of 4 rows stage x themselves; the others use workspace slot 0.  Returns 0
+ * (and 0 parts) where P or N is zero, Q4K_ERR_BAD_DIM as q4k_matmul_grouped
+ * does.  No device is needed. */
+int q4k_grouped_tile(int E, int P, int N, int K, int swiglu, int *parts);
+
 #ifdef __cplusplus
 }
 #endif
