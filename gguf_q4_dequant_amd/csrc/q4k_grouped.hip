@@ -49,18 +49,22 @@ constexpr int kSumsBlock = 32;     // eight sub-block sums, hi then lo
 struct Staged {
     const uint8_t *img;   // [rows][K / 256][kImageBlock]
     const uint8_t *sums;  // [rows][K / 256][kSumsBlock]
-    const float *back;    // [rows]: 2^(24 - e)
+    const float *back;    // [rows]: 2^(8 - e)
 };
 
 // The e of the scale 2^e that puts a largest magnitude mx in [2^14, 2^15),
-// limited so that 2^e and 2^(24 - e) are normal (zeros and subnormals: 127,
-// infinity and NaN: 0).
+// limited so that 2^e is a float (zeros and subnormals: 127, infinity and NaN:
+// 0); the largest float has -113.  The way back, 2^(24 - e) with the quants'
+// 2^24, does not fit a float there: it is 2^(8 - e), always a normal one, after
+// 2^16, which the sums take without rounding and without overflow (they stay
+// below 2^43 for any K).
 __device__ __forceinline__ int scale_exponent(float mx) {
     const int E = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu);
     const int e = E == 0 ? 127 : (E == 255 ? 0 : 141 - E);
-    return max(-103, min(127, e));
+    return max(-113, min(127, e));
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+constexpr float kBackFirst = 65536.f;
 
 // Stages eight consecutive values of a row at k (see above); the four threads
 // of a sub-block are neighbours and join its sum.
@@ -127,7 +131,7 @@ __global__ __launch_bounds__(kStageThreads) void stage_rows_kernel(const float *
     for (unsigned w = 0; w < blockDim.x >> 6; ++w) mx = fmaxf(mx, wave_mx[w]);
     const int e = scale_exponent(mx);
     const float up = power_of_two(e);
-    if (threadIdx.x == 0) back[row] = power_of_two(24 - e);
+    if (threadIdx.x == 0) back[row] = power_of_two(8 - e);
     uint8_t *im = img + row * (K / kBlockWeights) * kImageBlock;
     uint8_t *sm = sums + row * (K / kBlockWeights) * kSumsBlock;
 #pragma unroll
@@ -426,8 +430,8 @@ __device__ __forceinline__ void store_row(const Grouped &g, int p, float back, i
     constexpr int kOut = kSwiglu ? NC / 2 : NC;
 #pragma unroll
     for (int c = 0; c < kOut; ++c) {
-        const float v = acc[c] * back;
-        const float out = kSwiglu ? swiglu(v, acc[(c + kOut) % NC] * back) : v;
+        const float v = acc[c] * kBackFirst * back;
+        const float out = kSwiglu ? swiglu(v, acc[(c + kOut) % NC] * kBackFirst * back) : v;
         if (n0 + 16 * c + c16 < g.N) yr[n0 + 16 * c + c16] = out;
     }
 }
@@ -825,7 +829,7 @@ __device__ __forceinline__ void stage_few(const float4 v[4], int lane, uint8_t *
         so[0] = sh;
         so[8] = static_cast<_Float16>(s - static_cast<float>(sh));
     }
-    if (p == 0) reinterpret_cast<float *>(base + FewLds::kBackAt)[r] = power_of_two(24 - e);
+    if (p == 0) reinterpret_cast<float *>(base + FewLds::kBackAt)[r] = power_of_two(8 - e);
 }
 
 template <int WAVES, bool kSwiglu>
@@ -893,11 +897,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Grouped g, const flo
         const float4 back = *reinterpret_cast<const float4 *>(base + FewLds::kBackAt);
         const float bk[4] = {back.x, back.y, back.z, back.w};
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+            const float d = ws[c].d * kBackFirst, nm = ws[c].nm * kBackFirst;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                acc[c][r] = __builtin_fmaf(bk[r], __builtin_fmaf(ws[c].nm, cm[c][r], ws[c].d * (blk[c][0][r] + blk[c][1][r])),
-                                           acc[c][r]);
+                acc[c][r] = __builtin_fmaf(bk[r], __builtin_fmaf(nm, cm[c][r], d * (blk[c][0][r] + blk[c][1][r])), acc[c][r]);
+        }
         asm volatile("" ::: "memory");
     }
     // rows 0..3 of the tile are in lanes 0..15 (column c16): join the waves

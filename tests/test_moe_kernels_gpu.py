@@ -200,6 +200,40 @@ def test_weighted_sum_behind_every_kernel(kernel, holes):
         assert np.all(out[M // 2] == 0.0)
 
 
+@gpu
+@plain_kernels
+def test_rows_up_to_the_largest_float(kernel):
+    """Finite rows give finite products, whatever their magnitude: maxima around
+    the largest that one power of two brings into binary16, and the largest float."""
+    small = dict(d_range=(1e-6, 2e-6), dmin_range=(0.0, 4e-6))  # no sum of magnitudes reaches 2^128
+    w, x, offsets, rows, P, N, K = _case(kernel, 6, scale=1.0, **small)
+    top = np.finfo(np.float32).max
+    magnitudes = [top, 1e38, 2.0 ** 127, 6.7e35, 65520.0 * 2.0 ** 103, np.nextafter(np.float32(2.0 ** 118), np.float32(0)), 1e36]
+    shaped = rows[:len(magnitudes)] if P < 300 else rows[[0, 1, 20, 40, 47, 48, int(offsets[1]) - 1]]
+    for row, m in zip(shaped, magnitudes):
+        shape = x[row].astype(np.float64) / np.abs(x[row]).max()
+        x[row] = shape * float(m)
+        assert np.abs(x[row]).max() == np.float32(m)
+    y = _run(kernel, [to_dev(a) for a in w], to_dev(x), to_dev(offsets), to_dev(rows)).cpu().numpy()
+    want, s = ref.grouped(w[0], x, offsets, rows, 1, P)
+    assert s.max() < top and np.isfinite(y).all()
+    check_close(y, want, s, ref.product_tol(K))
+
+
+@gpu
+@pytest.mark.parametrize("kernel", [k for k in KERNELS if k[2]], ids=name)
+def test_swiglu_of_the_largest_floats(kernel):
+    """A gate of zeros: silu(0) * u is 0 for every finite u."""
+    w, x, offsets, rows, P, N, K = _case(kernel, 7, scale=1.0, d_range=(1e-6, 2e-6), dmin_range=(0.0, 4e-6))
+    # the largest float in every seventh place: over all K = 4352 places the sum of
+    # magnitudes would be 7.2e38, above the largest float; over these it is 1.0e38
+    x[rows[0], ::7], x[rows[P - 1]] = np.finfo(np.float32).max, -1e36
+    w[0][:] = 0
+    out = _run(kernel, [to_dev(a) for a in w], to_dev(x), to_dev(offsets), to_dev(rows)).cpu().numpy()
+    u, s = ref.grouped(w[1], x, offsets, rows, 1, P)
+    assert s.max() < np.finfo(np.float32).max and np.all(out == 0.0)
+
+
 # ---- a layer of them: graphs and streams -------------------------------------------
 
 # rows of a tile: (M, E, top_k, hidden, ffn), both products of the layer on that kernel
