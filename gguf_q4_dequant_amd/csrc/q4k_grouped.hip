@@ -303,17 +303,22 @@ __device__ __forceinline__ uint32_t lds_address(uint8_t *p) {
 // assembly because the compiler waits for every such copy before the next LDS
 // read, whichever buffer that reads; no register is written, and the kernel
 // waits for vmcnt and the barrier before it reads a buffer.
+// m0, which the compiler keeps to itself, is named as clobbered, so that no use
+// of its own is moved across; it remarks that the register is reserved.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
                  "s"(__builtin_amdgcn_readfirstlane(dst))
-                 : "memory");
+                 : "memory", "m0");
 }
 // The same from a buffer (offsets behind its end read zeros).
 __device__ __forceinline__ void copy_to_lds(rsrc_t buffer, uint32_t offset, uint32_t base, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(offset), "s"(buffer),
                  "s"(__builtin_amdgcn_readfirstlane(base)), "s"(__builtin_amdgcn_readfirstlane(dst))
-                 : "memory");
+                 : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // A raw buffer of bytes at p (both uniform).
 __device__ __forceinline__ rsrc_t buffer_at(const uint8_t *p, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
