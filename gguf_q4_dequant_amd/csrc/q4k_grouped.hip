@@ -15,11 +15,13 @@
 //   * x is scaled by a power of two per row, 2^e, that puts the row's largest
 //     magnitude in [2^14, 2^15), and split into two binary16 values, hi =
 //     rn(x'), lo = rn(x' - hi): about 22 bits of every value, and an absolute
-//     error below 2^-40 of the row's maximum where lo is subnormal.  Both
+//     error of at most 2^-39 of the row's maximum where lo is subnormal (half
+//     of its step of 2^-24, against a maximum of 2^14 at least).  Both
 //     enter the same fp32 accumulator: two v_mfma_f32_16x16x32_f16 per 32
 //     weights, half the binary16 matrix rate at fp32 accuracy.
 //   * The min term is one more MFMA per super-block: the eight X_j (hi and lo
-//     in k-quarters 0 and 1) times the eight m_j as subnormals.
+//     in k-quarters 0 and 1) times the eight m_j as subnormals.  X_j is split
+//     after a division by 2^6 that keeps it in range: to 2^-33 of the maximum.
 //
 // k order.  The order of k inside an MFMA is free as long as both operands
 // agree.  Lane quarter c of a wave (lanes 16c .. 16c + 15, one row of W each)

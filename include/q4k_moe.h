@@ -85,9 +85,11 @@ int q4k_moe_group(const int *expert, int P, int E, int *offsets, int *rows, hipS
  *   Entries of rows outside [0, P) are skipped, and offsets are read as if
  *   clamped to [0, P]; a pair of offsets that descends is an empty group.
  *   Numerics: x is split into two binary16 values scaled by a power of two per
- *   row or per 256 values of a row (about 22 significant bits of each value;
- *   2^-40 of the largest magnitude where that is more), the quants times their 6-bit scales are
- *   exact integers, sums and scales are fp32: rounding of the order of
+ *   row or per 256 values of a row (about 22 significant bits of each value, or
+ *   2^-39 of the largest magnitude there where that is more), and so is each sum
+ *   of 32 values, which the min term takes (2^-33 of that magnitude where that is
+ *   more); the quants times their 6-bit scales are exact integers, sums and
+ *   scales are fp32: beside those, rounding of the order of
  *   1e-6 * sum_k |x_k| (|d sc q| + |dmin m|).  A NaN or infinity in a row of x
  *   gives NaN or infinities in that row of y only.
  *   Errors: negative sizes, E outside [1, Q4K_MAX_EXPERTS], x_div < 1, K not a

@@ -234,6 +234,36 @@ def test_swiglu_of_the_largest_floats(kernel):
     assert s.max() < np.finfo(np.float32).max and np.all(out == 0.0)
 
 
+@gpu
+@plain_kernels
+def test_small_values_beside_a_large_one(kernel):
+    """Each value of a row is kept to 2^-22 of itself or 2^-39 of the row's largest
+    magnitude, and each sum of 32 (the min term) to 2^-33 of that magnitude: one
+    large value where W is zero, and one small value elsewhere.  The large one is
+    2^14, which is not scaled; then both limits are half of a binary16's smallest
+    step, 2^-25, the second times the 2^6 that the sums are divided by."""
+    w, x, offsets, rows, P, N, K = _case(kernel, 8)
+    blocks = w[0].reshape(len(offsets) - 1, N, K // 256, 144)
+    blocks[:, :, 0, :4] = 0  # d and dmin of the first super-block
+    g = _rng(9, P)
+    at, v = g.integers(256, K, P), (g.choice([-1, 1], P) * g.uniform(2.0 ** -4, 2.0 ** -3, P)).astype(np.float32)
+    x[:] = 0.0
+    x[:, 17] = 2.0 ** 14
+    x[np.arange(P), at] = v
+    y = _run(kernel, [to_dev(a) for a in w], to_dev(x), to_dev(offsets), to_dev(rows)).cpu().numpy().astype(np.float64)
+    for e in range(len(offsets) - 1):
+        r = rows[offsets[e]:offsets[e + 1]]
+        val, mag = ref.unpack(w[0][e])
+        least = (mag - val)[:, at[r]].T / 2   # dmin * m
+        scaled = (mag + val)[:, at[r]].T / 2  # d * sc * q
+        v64 = np.abs(v[r].astype(np.float64))[:, None]
+        bound = (2.0 ** -22 * v64 + 2.0 ** -25) * scaled + (2.0 ** -22 * v64 + 2.0 ** -19) * least
+        # two products, their factors and the last sum, each off by at most 2^-24 of the two terms
+        bound += 8 * 2.0 ** -24 * v64 * (scaled + least)
+        err = np.abs(y[r] - v[r].astype(np.float64)[:, None] * val[:, at[r]].T)
+        assert np.all(err <= bound), (err / np.maximum(bound, 1e-300)).max()
+
+
 # ---- a layer of them: graphs and streams -------------------------------------------
 
 # rows of a tile: (M, E, top_k, hidden, ffn), both products of the layer on that kernel
