@@ -111,6 +111,13 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 __device__ __forceinline__ float softmax_term(float l, float mx) { return l == mx ? 1.f : expf(l - mx); }
 __device__ __forceinline__ double softmax_term(double l, double mx) { return l == mx ? 1.0 : exp(l - mx); }
 
+// The sigmoid with the exponential of -|l|, which cannot overflow: a low logit's
+// score e^l / (1 + e^l) stays above 0 as long as a double holds e^l.
+__device__ __forceinline__ double sigmoid_of(double l) {
+    const double t = exp(-fabs(l));
+    return (l < 0.0 ? t : 1.0) / (1.0 + t);
+}
+
 // Routes one token; lane j < top_k ends with choice j.
 //   Without a bias the logits decide, which needs no arithmetic.  With one the
 // scores do, and close scores have to be told apart: they are computed in
@@ -195,7 +202,7 @@ __device__ __forceinline__ void route_token(const float *logits, const float *bi
                         float z = l[v];
                         asm volatile("" : "+v"(z));  // keeps the doubles out of the common path (and one at a time)
                         exact[v] = !(z > -INFINITY) ? 0.0
-                                   : sigmoid       ? 1.0 / (1.0 + exp(-static_cast<double>(z)))
+                                   : sigmoid       ? sigmoid_of(static_cast<double>(z))
                                                    : softmax_term(static_cast<double>(z), static_cast<double>(mx));
                         total += exact[v];
                     }
@@ -232,10 +239,11 @@ __device__ __forceinline__ void route_token(const float *logits, const float *bi
         }
     }
     // One value per lane from here: in double, where a sigmoid does not
-    // underflow before -745 and the shares of very low scores stay exact.
+    // underflow before -745 (nor lose bits before -708) and the shares of very
+    // low scores stay exact.
     double w = 0.0;
     if (expert >= 0)
-        w = sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(mine)))
+        w = sigmoid ? sigmoid_of(static_cast<double>(mine))
                     : softmax_term(static_cast<double>(mine), static_cast<double>(mx));
     if (flags & Q4K_ROUTE_NORMALIZE) {
         const double total = wave_sum(w);

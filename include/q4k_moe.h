@@ -61,6 +61,8 @@ enum q4k_route_flags {
  *   behind the last group are set to -1.  Pairs with expert -1 are in no group.
  *   With a bias the compared scores are computed in double, so that close
  *   scores are told apart by their values, not by how they were rounded.
+ *   The weights' sigmoids are computed in double with or without a bias: they
+ *   are 0, and equal, only from logits of about -745 on.
  *   Errors: M < 0, E outside [1, Q4K_MAX_EXPERTS], top_k outside
  *   [1, min(E, Q4K_MAX_TOP_K)], M * top_k > INT_MAX or unknown flags:
  *   Q4K_ERR_BAD_DIM; a NULL pointer (bias excepted): Q4K_ERR_NULL; a pointer
