@@ -20,6 +20,10 @@ CPU fallback.
     a = Adjustment(history=recent, repetition=r, mask=grammar)  # penalties, biases, allowed tokens
     index, value = matmul_argmax(w, x, adjustment=a)  # greedy selection under them
 
+A call runs on the current stream, or on ``stream`` (a torch stream or a raw
+handle); the outputs that it makes come from that stream's memory, as they would
+inside ``torch.cuda.stream(stream)``.
+
 Names and semantics mirror include/q4k.h, include/q4k_moe.h, include/q4k_select.h and include/q4a.h.
 """
 from __future__ import annotations
@@ -165,6 +169,21 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(like, shape, dtype, stream):
+    """An output for a call on ``stream``, on like's device and from that stream's
+    memory: memory of the current stream may be what was freed there a moment
+    ago, and still be in use by kernels that have not run.  (The callers whose
+    kernels take a few microseconds make theirs themselves where ``stream`` is None.)"""
+    import torch
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _check_operands(w, x, y):
     import torch
     if w.dtype != torch.uint8 or x.dtype != torch.float32 or y.dtype != torch.float32:
@@ -196,7 +215,7 @@ def matmul(w, x, y=None, path: int = PATH_AUTO, stream=None):
     if y is None:
         if w.dim() != 2:
             raise ValueError("pass y, or w shaped [N, K/256*144]")
-        y = torch.empty((x.shape[0], w.shape[0]), dtype=torch.float32, device=x.device)
+        y = _new(x, (x.shape[0], w.shape[0]), torch.float32, stream)
     M, N, K = _check_operands(w, x, y)
     lib = library()
     if int(path) == PATH_AUTO:
@@ -244,9 +263,9 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
         raise ValueError(f"w has {w.numel()} bytes, expected N*K/256*144 = "
                          f"{N * (K // BLOCK_WEIGHTS) * BLOCK_BYTES}")
     if index is None:
-        index = torch.empty(M, dtype=torch.int32, device=x.device)
+        index = _new(x, M, torch.int32, stream)
     if value is None:
-        value = torch.empty(M, dtype=torch.float32, device=x.device)
+        value = _new(x, M, torch.float32, stream)
     _check_outputs(x, index, value, M)
     if adjustment is not None:
         dev = x.get_device()
@@ -357,7 +376,7 @@ def logits_adjust(logits, adjustment, out=None, stream=None):
     import torch
     M, N, dev = _checked_logits(logits)
     if out is None:
-        out = torch.empty_like(logits)
+        out = torch.empty_like(logits) if stream is None else _new(logits, (M, N), torch.float32, stream)
     elif out is not logits:
         _checked_tensor("out", out, torch.float32, (M, N), dev)
     rc = library().q4k_logits_adjust(logits.data_ptr(), out.data_ptr(), adjustment._checked(dev, M, N), M, N,
@@ -374,11 +393,11 @@ def logits_argmax(logits, adjustment, index=None, value=None, stream=None):
     not written."""
     import torch
     M, N, dev = _checked_logits(logits)
-    if index is None and value is None:
+    if index is None and value is None and stream is None:
         index, value = logits.new_empty(M, dtype=torch.int32), logits.new_empty(M)
     else:
-        index = logits.new_empty(M, dtype=torch.int32) if index is None else index
-        value = logits.new_empty(M) if value is None else value
+        index = _new(logits, M, torch.int32, stream) if index is None else index
+        value = _new(logits, M, torch.float32, stream) if value is None else value
         _check_outputs(logits, index, value, M)
     rc = library().q4k_logits_argmax(logits.data_ptr(), adjustment._checked(dev, M, N), M, N, index.data_ptr(),
                                      value.data_ptr(), _stream_for(dev, stream))
@@ -416,8 +435,12 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, normalize: b
         raise Q4KError(ERR_BAD_DIM, f"E={E} top_k={k}")
     bias_ptr = None if bias is None else _checked_tensor("bias", bias, torch.float32, (E,), dev)
     if out is None:
-        expert, weight = logits.new_empty((M, k), dtype=torch.int32), logits.new_empty((M, k))
-        out = Routing(expert, weight, expert.new_empty(E + 1), expert.new_empty(M * k))
+        if stream is None:
+            expert, weight = logits.new_empty((M, k), dtype=torch.int32), logits.new_empty((M, k))
+            out = Routing(expert, weight, expert.new_empty(E + 1), expert.new_empty(M * k))
+        else:
+            out = Routing(_new(logits, (M, k), torch.int32, stream), _new(logits, (M, k), torch.float32, stream),
+                          _new(logits, E + 1, torch.int32, stream), _new(logits, M * k, torch.int32, stream))
     else:
         _checked_tensor("expert", out.expert, torch.int32, (M, k), dev)
         _checked_tensor("weight", out.weight, torch.float32, (M, k), dev)
@@ -443,8 +466,7 @@ def moe_group(expert, E: int, stream=None):
     P, E = expert.numel(), int(E)
     if not 1 <= E <= MAX_EXPERTS:
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=expert.device)
-    rows = torch.empty(P, dtype=torch.int32, device=expert.device)
+    offsets, rows = _new(expert, E + 1, torch.int32, stream), _new(expert, P, torch.int32, stream)
     rc = library().q4k_moe_group(expert.data_ptr(), P, E, offsets.data_ptr(), rows.data_ptr(),
                                  _stream_for(expert.get_device(), stream))
     if rc != OK:
@@ -490,7 +512,7 @@ def matmul_grouped(w, x, offsets, rows=None, y=None, x_div: int = 1, stream=None
     import torch
     P, E, N, K, dev, (w_ptr,), offsets_ptr, rows_ptr = _grouped_checked((w,), x, offsets, rows, x_div)
     if y is None:
-        y = x.new_empty((P, N))
+        y = x.new_empty((P, N)) if stream is None else _new(x, (P, N), torch.float32, stream)
     else:
         _checked_tensor("y", y, torch.float32, (P, N), dev)
     rc = library().q4k_matmul_grouped(w_ptr, x.data_ptr(), x_div, offsets_ptr, rows_ptr, y.data_ptr(), E, P, N, K,
@@ -506,7 +528,7 @@ def matmul_grouped_swiglu(w_gate, w_up, x, offsets, rows=None, out=None, x_div: 
     import torch
     P, E, N, K, dev, w_ptrs, offsets_ptr, rows_ptr = _grouped_checked((w_gate, w_up), x, offsets, rows, x_div)
     if out is None:
-        out = x.new_empty((P, N))
+        out = x.new_empty((P, N)) if stream is None else _new(x, (P, N), torch.float32, stream)
     else:
         _checked_tensor("out", out, torch.float32, (P, N), dev)
     rc = library().q4k_matmul_grouped_swiglu(*w_ptrs, x.data_ptr(), x_div, offsets_ptr, rows_ptr, out.data_ptr(),
@@ -530,7 +552,7 @@ def matmul_grouped_combine(w, x, routing: Routing, out=None, stream=None):
     expert_ptr = _checked_tensor("expert", expert, torch.int32, choices, dev)
     weight_ptr = _checked_tensor("weight", weight, torch.float32, choices, dev)
     if out is None:
-        out = x.new_empty((M, N))
+        out = x.new_empty((M, N)) if stream is None else _new(x, (M, N), torch.float32, stream)
     else:
         _checked_tensor("out", out, torch.float32, (M, N), dev)
     rc = library().q4k_matmul_grouped_combine(w_ptr, x.data_ptr(), expert_ptr, weight_ptr, offsets_ptr, rows_ptr,
@@ -557,7 +579,7 @@ def matmul_swiglu(w_gate, w_up, x, out=None, stream=None):
     if out is None:
         if w_gate.dim() != 2:
             raise ValueError("pass out, or w_gate shaped [N, K/256*144]")
-        out = torch.empty((x.shape[0], w_gate.shape[0]), dtype=torch.float32, device=x.device)
+        out = _new(x, (x.shape[0], w_gate.shape[0]), torch.float32, stream)
     M, N, K = _check_operands(w_gate, x, out)
     _check_operands(w_up, x, out)
     rc = library().q4k_matmul_swiglu(w_gate.data_ptr(), w_up.data_ptr(), x.data_ptr(), out.data_ptr(), M, N, K,
@@ -673,7 +695,7 @@ def raw_matmul_batched_noalloc(items: Iterable[Tuple[int, int, int, int, int]], 
 Q4A_GROUP = 64
 
 
-def _q4a_checked(w_q, scales, biases, x, y):
+def _q4a_checked(w_q, scales, biases, x, y, stream=None):
     """Validate one q4a product's tensors (shapes, dtypes, device, contiguity);
     returns (y, M, N, K) with y allocated if None."""
     import torch
@@ -691,7 +713,7 @@ def _q4a_checked(w_q, scales, biases, x, y):
             biases.numel() != N * K // 64:
         raise ValueError(f"w_q must hold N*K/2 = {N * K // 2} bytes and scales/biases N*K/64 = {N * K // 64} values")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _new(x, (M, N), torch.float32, stream)
     if y.dtype != torch.float32 or tuple(y.shape) != (M, N):
         raise ValueError("y must be float32 [M, N]")
     for name, t in (("w_q", w_q), ("scales", scales), ("biases", biases), ("x", x), ("y", y)):
@@ -706,7 +728,7 @@ def q4a_matmul(w_q, scales, biases, x, y=None, stream=None):
     """y[M, N] = x[M, K] . dequant(W)^T for W in the affine 4-bit group layout
     of include/q4a.h: w_q uint32 [N, K/8] (or uint8 [N, K/2]), scales and
     biases float16 [N, K/64], w = s * q + b per group of 64."""
-    y, M, N, K = _q4a_checked(w_q, scales, biases, x, y)
+    y, M, N, K = _q4a_checked(w_q, scales, biases, x, y, stream)
     rc = library().q4a_matmul(w_q.data_ptr(), scales.data_ptr(), biases.data_ptr(), x.data_ptr(), y.data_ptr(),
                               M, N, K, _stream_handle(stream))
     if rc != OK:

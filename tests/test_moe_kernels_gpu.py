@@ -288,6 +288,13 @@ def _layer(tile, tag):
         down=_weights(E, hidden, ffn, 100 * tag + 3, **small)).items()}, k
 
 
+@pytest.fixture(scope="module")
+def streams():
+    """Two streams for all (torch hands out the same 32 in turn)."""
+    import torch
+    return torch.cuda.Stream(), torch.cuda.Stream()
+
+
 def _run_layer(t, k):
     r = q4k.moe_route(t["logits"], k)
     h = q4k.matmul_grouped_swiglu(t["gate"], t["up"], t["x"], r.offsets, r.rows, x_div=k)
@@ -296,11 +303,11 @@ def _run_layer(t, k):
 
 @gpu
 @layers
-def test_graphs_that_share_a_workspace(tile):
+def test_graphs_that_share_a_workspace(tile, streams):
     """Two layers captured on one stream, replayed in turn on changing inputs with
     eager work of the same program between the replays."""
     import torch
-    stream = torch.cuda.Stream()
+    stream = streams[0]
     stream.wait_stream(torch.cuda.current_stream())
     parts = [_layer(tile, tag) for tag in (1, 2)]
     with torch.cuda.stream(stream):
@@ -327,12 +334,11 @@ def test_graphs_that_share_a_workspace(tile):
 
 @gpu
 @layers
-def test_layers_on_two_streams_at_once(tile):
+def test_layers_on_two_streams_at_once(tile, streams):
     import torch
     parts = [_layer(tile, tag) for tag in (3, 4)]
     want = [_run_layer(t, k) for t, k in parts]
     torch.cuda.synchronize()
-    streams = [torch.cuda.Stream() for _ in parts]
     for _ in range(4):
         got = []
         for (t, k), s in zip(parts, streams):
