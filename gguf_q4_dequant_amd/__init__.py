@@ -38,6 +38,7 @@ LIBRARY_PATH = os.path.join(_PKG, "libq4k.so")
 BLOCK_WEIGHTS = 256
 BLOCK_BYTES = 144
 MAX_BATCH = 32
+INT_MAX = 2 ** 31 - 1  # the library counts in int; ctypes would keep a longer number's low 32 bits
 
 OK = 0
 ERR_NULL = -1
@@ -365,6 +366,8 @@ def _checked_logits(logits):
     shape, dev = logits.shape, logits.get_device()
     if len(shape) != 2 or logits.dtype is not torch.float32:
         raise TypeError("logits must be float32 [M, N]")
+    if shape[0] > INT_MAX or shape[1] > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"logits {list(shape)}")
     if dev < 0 or not logits.is_contiguous():
         raise ValueError("logits must be a contiguous device tensor")
     return shape[0], shape[1], dev
@@ -461,6 +464,8 @@ def moe_group(expert, E: int, stream=None):
     import torch
     if expert.dtype != torch.int32:
         raise TypeError("expert must be int32")
+    if expert.numel() > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"P={expert.numel()}")
     if not expert.is_cuda or not expert.is_contiguous():
         raise ValueError("expert must be a contiguous device tensor")
     P, E = expert.numel(), int(E)
@@ -481,13 +486,16 @@ def _grouped_checked(ws, x, offsets, rows, x_div):
     w_shape, x_shape = ws[0].shape, x.shape
     if x.dtype is not torch.float32 or len(x_shape) != 2 or len(w_shape) != 3 or ws[0].dtype is not torch.uint8:
         raise TypeError("expected w uint8 [E, N, K/256*144] and x float32 [rows, K]")
+    E, N, _ = w_shape
+    x_rows, K = x_shape
+    P = x_rows * x_div if rows is None else rows.numel()
+    if P > INT_MAX or N > INT_MAX or x_div > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"P={P} N={N} x_div={x_div}")
+    if K % BLOCK_WEIGHTS != 0 or K == 0 or K > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"K={K}")
     dev = x.get_device()
     if dev < 0 or not x.is_contiguous():
         raise ValueError("x must be a contiguous device tensor")
-    E, N, _ = w_shape
-    x_rows, K = x_shape
-    if K % BLOCK_WEIGHTS != 0 or K == 0:
-        raise Q4KError(ERR_BAD_DIM, f"K={K}")
     if not 1 <= E <= MAX_EXPERTS:
         raise Q4KError(ERR_BAD_DIM, f"E={E}")
     if x_div < 1:
@@ -496,8 +504,7 @@ def _grouped_checked(ws, x, offsets, rows, x_div):
     w_ptrs = [_checked_tensor("w", w, torch.uint8, shape, dev) for w in ws]
     offsets_ptr = _checked_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     if rows is None:
-        return x_rows * x_div, E, N, K, dev, w_ptrs, offsets_ptr, None
-    P = rows.numel()
+        return P, E, N, K, dev, w_ptrs, offsets_ptr, None
     rows_ptr = _checked_tensor("rows", rows, torch.int32, (P,), dev)
     if (P + x_div - 1) // x_div != x_rows:
         raise ValueError(f"x has {x_rows} rows, expected {P} pairs / x_div {x_div}")
@@ -566,6 +573,8 @@ def grouped_tile(E: int, P: int, N: int, K: int, swiglu: bool = False) -> Tuple[
     """(rows, parts) of the kernel that a grouped product of these sizes runs: tiles
     of 4, 16, 32 or 48 rows (0: nothing to compute), K split into ``parts`` within
     a workgroup (q4k_grouped_tile)."""
+    if max(abs(E), abs(P), abs(N), abs(K)) > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"E={E} P={P} N={N} K={K}")
     parts = ctypes.c_int(0)
     rows = library().q4k_grouped_tile(E, P, N, K, int(swiglu), ctypes.byref(parts))
     if rows < 0:

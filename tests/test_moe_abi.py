@@ -147,3 +147,33 @@ def test_binding_refuses_before_any_call():
                 dict(history=torch.zeros((2, 5), dtype=torch.int32))):
         with pytest.raises(ValueError):
             q4k.Adjustment(**bad)._checked(dev, 2, 64)
+
+
+def test_binding_refuses_sizes_that_the_library_cannot_count():
+    """The C functions count in int, and ctypes cuts a longer number to its low 32
+    bits: 2^32 + 8 would run as 8.  (Tensors without memory: sizes only.)"""
+    import torch
+    far = (1 << 32) + 8
+    meta = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    w, offsets = meta(2, 8, 144, dtype=torch.uint8), meta(3, dtype=torch.int32)
+    rows = meta(far, dtype=torch.int32)
+    for call in (lambda: q4k.moe_group(rows, 4),
+                 lambda: q4k.moe_route(meta(far, 1), 1),
+                 lambda: q4k.logits_adjust(meta(far, 1), q4k.Adjustment()),
+                 lambda: q4k.logits_adjust(meta(1, far), q4k.Adjustment()),
+                 lambda: q4k.logits_argmax(meta(1, far), q4k.Adjustment()),
+                 lambda: q4k.matmul_grouped(w, meta(far, 256), offsets, rows),
+                 lambda: q4k.matmul_grouped(w, meta(1, 256), offsets, rows, x_div=far),
+                 lambda: q4k.matmul_grouped(w, meta(1, 256), offsets, meta(9, dtype=torch.int32), x_div=(1 << 32) + 1),
+                 lambda: q4k.matmul_grouped(w, meta(9, 256), offsets, x_div=1 << 30),
+                 lambda: q4k.matmul_grouped_swiglu(w, w, meta(far, 256), offsets, rows),
+                 lambda: q4k.matmul_grouped(meta(2, 8, ((1 << 32) // 256 + 1) * 144, dtype=torch.uint8),
+                                            meta(9, (1 << 32) + 256), offsets),
+                 lambda: q4k.matmul_grouped_combine(w, meta(far, 256), q4k.Routing(
+                     meta(far, 1, dtype=torch.int32), meta(far, 1), offsets, rows))):
+        with pytest.raises(q4k.Q4KError) as refused:
+            call()
+        assert refused.value.code == q4k.ERR_BAD_DIM
+    for sizes in ((2, far, 16, 256), (2, 8, far, 256), (2, 8, 16, (1 << 32) + 256), ((1 << 32) + 2, 8, 16, 256)):
+        with pytest.raises(q4k.Q4KError):
+            q4k.grouped_tile(*sizes)
