@@ -247,7 +247,8 @@ def matmul_argmax(w, x, N: Optional[int] = None, index=None, value=None, stream=
     the largest y[m, n] of y = x . dequant(w)^T, and that value.  The logits stay
     on the device (library workspace).  N defaults to w's leading dimension.
     With an ``Adjustment`` the choice is made under its penalties, biases and
-    mask (as by logits_argmax)."""
+    mask (as by logits_argmax; a row that has nothing but NaN then gives index -1
+    and value -inf, and index 0 and NaN without)."""
     import torch
     if N is None:
         if w.dim() != 2:

@@ -446,7 +446,7 @@ __device__ __forceinline__ void store_row(const Grouped &g, int p, float back, i
 // The arithmetic of one tile over its first RT row tiles of 16.  Every wave
 // reads all of the tile's x from LDS and builds the operands of its own columns
 // of W in registers: RT row tiles share an operand, NC column tiles a fragment
-// of x, and two waves a SIMD (RT = 3, NC = 4, 244 registers) hide each other's
+// of x, and two waves a SIMD (RT = 3, NC = 4, 241 registers) hide each other's
 // waits.  Bound by the power of the matrix cores: 16384 pairs over 64 experts of
 // 2 x 1024 x 2048 take 290 us, 0.95 PFLOP/s of binary16 (1.20 for a large plain
 // product on this card), with the pipes busy half of the cycles at 1.9 GHz; the
@@ -779,9 +779,11 @@ __global__ __launch_bounds__(256 * KS, 4) void thin_kernel(Grouped g) {
 // Four rows of x times 32 rows of W (SwiGLU: 16 gate and the same 16 up rows)
 // per workgroup; the waves split K by super-blocks, each with its own LDS:
 // one super-block of the 32 rows of W, the staged x and its factors.  Without a
-// launch for the staging, and with K in eight parts, a call is about two memory
-// round trips: 8 of 128 experts of 2 x 1024 x 2048 for one token (18.9 MB) 7.7 us,
-// 2 of 16 of 4096 x 2048 (9.4 MB) 5.7 us, of which an empty launch is about 2.
+// launch for the staging, and with K in eight parts, a call is about three memory
+// round trips (the offsets; the rows' numbers, beside the first of W; x): 8 of 128
+// experts of 2 x 1024 x 2048 for one token (18.9 MB) 9.3 us, or 7.5 with the weights
+// still in the L2s, 2 of 16 of 4096 x 2048 (9.4 MB) 5.6 us, of which an empty launch
+// is about 2.
 constexpr int kFewRows = 4;
 struct FewLds {
     static constexpr int kW = 32 * kBlockBytes, kX = kFewRows * kImageBlock, kSums = kFewRows * kSumsBlock;

@@ -42,7 +42,8 @@
  *     valid memory.  Code that captures HIP graphs makes one eager call of
  *     each shape on the capture stream first (no allocation inside a
  *     capture), and does not replay such a graph concurrently with calls on
- *     its capture stream (they share the workspace).  q4k_matmul_batched_noalloc
+ *     its capture stream or with another graph captured there (they share the
+ *     workspace).  q4k_matmul_batched_noalloc
  *     uses a fixed per-GPU array instead and allocates nothing.
  *   - The stream handle is passed to the HIP runtime as given; a handle that
  *     is not a live stream of the current device is undefined behaviour in

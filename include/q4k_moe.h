@@ -23,9 +23,15 @@
  * Conventions are those of q4k.h: device pointers on the current device, the
  * caller's stream, no host synchronization, the library's per-stream
  * workspace (make one eager call of each shape before a graph capture; host
- * threads that share a stream take turns), the same status codes, nothing
- * enqueued on an error.  Empty sizes (M, P or N
- * zero) are successful no-ops.
+ * threads that share a stream take turns, and so do the replays of graphs
+ * captured on one stream, which share its workspace), the same status codes,
+ * nothing enqueued on an error.  Empty sizes (M, P or N zero) are successful
+ * no-ops.
+ *
+ * Workspace.  Grouped products, except those of few pairs (q4k_grouped_tile: 4
+ * rows), keep x's staged form, 1056 bytes for 256 values (1.03 times x) and 16
+ * a row; the weighted sum also keeps the pairs' products, 4 * M * top_k * N
+ * bytes.  Both stay allocated to the stream.
  */
 #ifndef Q4K_MOE_H
 #define Q4K_MOE_H

@@ -18,7 +18,9 @@
  *     z = -inf where the mask's bit of n is clear (whatever z was, NaN too)
  *
  * Conventions are those of q4k.h (device pointers, the caller's stream, no
- * host synchronization, per-stream workspace, status codes).
+ * host synchronization, per-stream workspace, status codes).  The workspace of
+ * a choice is 8 bytes for every 1024 or 4096 logits; behind the lm_head it also
+ * holds the logits, 4 * M * N bytes, which stay allocated to the stream.
  */
 #ifndef Q4K_SELECT_H
 #define Q4K_SELECT_H
@@ -57,7 +59,9 @@ int q4k_logits_adjust(const float *logits, float *out, const q4k_adjustment *adj
 
 /* index[m] = the lowest allowed n with the largest adjusted logit, value[m] =
  * that logit.  NaN logits and masked tokens never win; a row in which nothing
- * is left (every token masked or NaN) gives index -1 and value -inf.
+ * is left (every token masked or NaN) gives index -1 and value -inf.  (A row of
+ * NaN without a mask too, where q4k_matmul_argmax, which has no masks, gives index
+ * 0 and value NaN.)
  *   index: DEVICE int32 [M].  value: DEVICE float32 [M] or NULL.
  *   Errors: as for q4k_logits_adjust, and N == 0 (no maximum):
  *   Q4K_ERR_BAD_DIM. */
