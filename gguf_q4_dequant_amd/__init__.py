@@ -20,11 +20,17 @@ CPU fallback.
     a = Adjustment(history=recent, repetition=r, mask=grammar)  # penalties, biases, allowed tokens
     index, value = matmul_argmax(w, x, adjustment=a)  # greedy selection under them
 
+    h, x = rms_norm(delta, weight, residual=x)  # the residual's addition and the norm in front of a product
+    cache = KVCache(k, v)               # paged: [pages, kv_heads, page_size, head_dim], f16, bf16 or e4m3
+    seqs = Sequences(offsets, lengths, pages)  # packed sequences and the pages that they have
+    q = kv_append(k_new, v_new, cache, seqs, rotation=Rotation(inv_freq), q=q)  # rotated; keys and values stored
+    o = attention(q, cache, seqs)       # prompts, chunks and single tokens; attention_tree for drafted ones
+
 A call runs on the current stream, or on ``stream`` (a torch stream or a raw
 handle); the outputs that it makes come from that stream's memory, as they would
 inside ``torch.cuda.stream(stream)``.
 
-Names and semantics mirror include/q4k.h, include/q4k_moe.h, include/q4k_select.h and include/q4a.h.
+Names and semantics mirror include/q4k.h, include/q4k_moe.h, include/q4k_select.h, include/q4k_layer.h and include/q4a.h.
 """
 from __future__ import annotations
 
@@ -64,7 +70,7 @@ EXPORTED = ("q4k_matmul", "q4k_matmul_batched", "q4k_matmul_path", "q4k_matmul_b
             "q4k_matmul_argmax", "q4k_matmul_swiglu", "q4k_gguf_list", "q4k_select_path", "q4k_strerror",
             "q4k_version", "q4k_moe_route", "q4k_moe_group", "q4k_matmul_grouped", "q4k_matmul_grouped_swiglu",
             "q4k_matmul_grouped_combine", "q4k_grouped_tile", "q4k_logits_adjust", "q4k_logits_argmax",
-            "q4k_matmul_argmax_adjusted")
+            "q4k_matmul_argmax_adjusted", "q4k_rms_norm", "q4k_kv_append", "q4k_attention", "q4k_attention_tree")
 
 
 class Q4KError(RuntimeError):
@@ -82,6 +88,23 @@ class _Adjustment(ctypes.Structure):
     _fields_ = [("history", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
                 ("presence", ctypes.c_void_p), ("bias_id", ctypes.c_void_p), ("bias_value", ctypes.c_void_p),
                 ("mask", ctypes.c_void_p), ("history_len", ctypes.c_int), ("bias_len", ctypes.c_int)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int), ("pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _Sequences(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("count", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("eps", ctypes.c_float), ("rotary", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
 
 
 class GgufTensor(ctypes.Structure):
@@ -139,6 +162,15 @@ def library() -> ctypes.CDLL:
     lib.q4k_logits_argmax.restype = ci
     lib.q4k_matmul_argmax_adjusted.argtypes = [vp, vp, adj, ci, ci, ci, vp, vp, vp]
     lib.q4k_matmul_argmax_adjusted.restype = ci
+    kv, sq, ro = ctypes.POINTER(_Cache), ctypes.POINTER(_Sequences), ctypes.POINTER(_Rotation)
+    lib.q4k_rms_norm.argtypes = [vp, vp, vp, cf, vp, vp, ci, ci, vp]
+    lib.q4k_rms_norm.restype = ci
+    lib.q4k_kv_append.argtypes = [vp, vp, vp, kv, sq, ro, vp, ci, ci, vp]
+    lib.q4k_kv_append.restype = ci
+    lib.q4k_attention.argtypes = [vp, kv, sq, cf, vp, ci, ci, vp]
+    lib.q4k_attention.restype = ci
+    lib.q4k_attention_tree.argtypes = [vp, kv, sq, vp, ci, cf, vp, ci, ci, vp]
+    lib.q4k_attention_tree.restype = ci
     lib.q4k_gguf_list.argtypes = [ctypes.c_char_p, ctypes.POINTER(GgufTensor), ci, ctypes.POINTER(ci)]
     lib.q4k_gguf_list.restype = ci
     lib.q4k_select_path.argtypes = [ci, ci, ci]
@@ -581,6 +613,212 @@ def grouped_tile(E: int, P: int, N: int, K: int, swiglu: bool = False) -> Tuple[
     if rows < 0:
         raise Q4KError(rows, "q4k_grouped_tile")
     return rows, parts.value
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, total=None, out=None, stream=None):
+    """The root-mean-square norm y = t * rsqrt(mean(t^2) + eps) * weight of the rows
+    of t = x + residual (q4k_rms_norm); x and residual float32 [M, N], weight
+    float32 [N].  Returns y without a residual, and (y, t) with one; ``total``
+    (for t) and ``out`` (for y) may be x or residual."""
+    import torch
+    M, N, dev = _checked_rows("x", x, 2)
+    shape = (M, N)
+    weight_ptr = _checked_tensor("weight", weight, torch.float32, (N,), dev)
+    residual_ptr = None if residual is None else _checked_tensor("residual", residual, torch.float32, shape, dev)
+    if out is None:
+        out = torch.empty_like(x) if stream is None else _new(x, shape, torch.float32, stream)
+    else:
+        _checked_tensor("out", out, torch.float32, shape, dev)
+    if total is None:
+        if residual is not None:
+            total = torch.empty_like(x) if stream is None else _new(x, shape, torch.float32, stream)
+    else:
+        _checked_tensor("total", total, torch.float32, shape, dev)
+        if total is out and M and N:
+            raise ValueError("total and out must be two tensors")
+    rc = library().q4k_rms_norm(x.data_ptr(), residual_ptr, weight_ptr, float(eps),
+                                None if total is None else total.data_ptr(), out.data_ptr(), M, N,
+                                _stream_for(dev, stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_rms_norm")
+    return out if residual is None else (out, total)
+
+
+KV_F16 = 0
+KV_BF16 = 1
+KV_E4M3 = 2
+
+
+class KVCache(NamedTuple):
+    """A paged cache: k and v [pages, kv_heads, page_size, head_dim], contiguous, of
+    float16, bfloat16 or float8_e4m3fn; what is kept stands for k * k_scale and
+    v * v_scale.  page_size is a power of two, head_dim a multiple of 16 up to 256."""
+    k: object
+    v: object
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+
+class Sequences(NamedTuple):
+    """The packed sequences of a call: offsets int32 [B + 1] (sequence b's new tokens
+    are rows offsets[b]:offsets[b + 1]), lengths int32 [B] (its tokens, the new
+    ones among them) and pages int32 [B, max_pages] (the cache's pages that it has,
+    in order; -1 behind them)."""
+    offsets: object
+    lengths: object
+    pages: object
+
+
+class Rotation(NamedTuple):
+    """Rotary positions: the angles position * inv_freq, inv_freq float32 [R / 2], of
+    the pairs (i, i + R / 2) of the leading R dimensions, or (2 i, 2 i + 1)."""
+    inv_freq: object
+    interleaved: bool = False
+
+
+def _checked_rows(name, x, dims):
+    """The shape of x, float32 with ``dims`` dimensions, contiguous on a GPU, and that GPU's number."""
+    import torch
+    shape, dev = x.shape, x.get_device()
+    if len(shape) != dims or x.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32 with {dims} dimensions")
+    if max(shape) > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"{name} {list(shape)}")
+    if dev < 0 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    return (*shape, dev)
+
+
+_KV_TYPES = {}
+
+
+def _checked_cache(cache, kv_heads, head_dim, dev):
+    """The C struct of a KVCache on GPU number dev for this many heads of this size (kv_heads None: any)."""
+    import torch
+    if not _KV_TYPES:
+        _KV_TYPES.update({torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3})
+    k, v, k_scale, v_scale = cache
+    shape, dtype = k.shape, k.dtype
+    if dtype not in _KV_TYPES:
+        raise TypeError(f"the cache must be float16, bfloat16 or float8_e4m3fn, not {dtype}")
+    if len(shape) != 4:
+        raise ValueError("the cache must be [pages, kv_heads, page_size, head_dim]")
+    pages, heads, page_size, dim = shape
+    if dim != head_dim or (kv_heads is not None and heads != kv_heads):
+        raise ValueError(f"the cache has {heads} heads of {dim}, the call "
+                         f"{'' if kv_heads is None else f'{kv_heads} '}heads of {head_dim}")
+    if max(shape) > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"cache {list(shape)}")
+    return _Cache(_checked_tensor("cache.k", k, dtype, shape, dev), _checked_tensor("cache.v", v, dtype, shape, dev),
+                  _KV_TYPES[dtype], pages, heads, page_size, dim, k_scale, v_scale)
+
+
+def _checked_sequences(sequences, dev):
+    """The C struct of Sequences on GPU number dev."""
+    import torch
+    offsets, lengths, pages = sequences
+    if len(pages.shape) != 2:
+        raise ValueError("pages must be int32 [B, max_pages]")
+    B, most = pages.shape
+    if B > INT_MAX or most > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"pages {list(pages.shape)}")
+    return _Sequences(_checked_tensor("offsets", offsets, torch.int32, (B + 1,), dev),
+                      _checked_tensor("lengths", lengths, torch.int32, (B,), dev),
+                      _checked_tensor("pages", pages, torch.int32, (B, most), dev), B, most)
+
+
+def kv_append(k, v, cache: KVCache, sequences: Sequences, rotation: Optional[Rotation] = None, q=None, positions=None,
+              q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
+    """Store the new tokens' keys and values, float32 [T, kv_heads, head_dim], at
+    their places in the cache (q4k_kv_append): k under the norm ``k_norm`` (float32
+    [head_dim], each head by itself) and the rotation, both rounded to the cache's
+    type.  With ``q`` float32 [T, q_heads, head_dim] returns it under ``q_norm`` and
+    the rotation, in a new tensor or in ``q_out`` (which may be q).  positions int32
+    [T]: other positions than the tokens' indexes in their sequences (of drafted
+    tokens that form a tree: their depths)."""
+    import torch
+    T, kv_heads, D, dev = _checked_rows("k", k, 3)
+    v_ptr = _checked_tensor("v", v, torch.float32, (T, kv_heads, D), dev)
+    c, s = _checked_cache(cache, kv_heads, D, dev), _checked_sequences(sequences, dev)
+    q_heads, q_ptr, q_out_ptr = 0, None, None
+    if q is not None:
+        t, q_heads, d, q_dev = _checked_rows("q", q, 3)
+        if t != T or d != D or q_dev != dev or q_heads < 1 or q_heads % kv_heads:
+            raise ValueError(f"q must be [{T}, a multiple of {kv_heads}, {D}] on cuda:{dev}, not {list(q.shape)}")
+        q_ptr = q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty_like(q) if stream is None else _new(q, (T, q_heads, D), torch.float32, stream)
+            q_out_ptr = q_out.data_ptr()
+        else:
+            q_out_ptr = _checked_tensor("q_out", q_out, torch.float32, (T, q_heads, D), dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs a q")
+    r = _Rotation(eps=eps)
+    if q_norm is not None:
+        r.q_norm = _checked_tensor("q_norm", q_norm, torch.float32, (D,), dev)
+    if k_norm is not None:
+        r.k_norm = _checked_tensor("k_norm", k_norm, torch.float32, (D,), dev)
+    if rotation is not None:
+        inv_freq, interleaved = rotation
+        if len(inv_freq.shape) != 1:
+            raise ValueError("inv_freq must be float32 [R / 2]")
+        half = inv_freq.shape[0]
+        r.inv_freq = _checked_tensor("inv_freq", inv_freq, torch.float32, (half,), dev)
+        r.rotary, r.interleaved = min(2 * half, INT_MAX - 1), 1 if interleaved else 0
+    if positions is not None:
+        r.positions = _checked_tensor("positions", positions, torch.int32, (T,), dev)
+    rc = library().q4k_kv_append(q_ptr, k.data_ptr(), v_ptr, c, s, r, q_out_ptr, T, q_heads, _stream_for(dev, stream))
+    if rc != OK:
+        raise Q4KError(rc, "q4k_kv_append")
+    return q_out
+
+
+def _attend(q, cache, sequences, mask, scale, out, stream):
+    import torch
+    T, q_heads, D, dev = _checked_rows("q", q, 3)
+    c, s = _checked_cache(cache, None, D, dev), _checked_sequences(sequences, dev)
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _new(q, (T, q_heads, D), torch.float32, stream)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _checked_tensor("out", out, torch.float32, (T, q_heads, D), dev)
+    scale = D ** -0.5 if scale is None else float(scale)
+    if mask is None:
+        rc = library().q4k_attention(q.data_ptr(), c, s, scale, out_ptr, T, q_heads, _stream_for(dev, stream))
+        name = "q4k_attention"
+    else:
+        if len(mask.shape) != 2 or mask.shape[1] > INT_MAX:
+            raise ValueError("mask must be int32 or uint32 [T, words]")
+        dtype = torch.uint32 if mask.dtype == torch.uint32 else torch.int32
+        mask_ptr = _checked_tensor("mask", mask, dtype, (T, mask.shape[1]), dev)
+        rc = library().q4k_attention_tree(q.data_ptr(), c, s, mask_ptr, mask.shape[1], scale, out_ptr, T, q_heads,
+                                          _stream_for(dev, stream))
+        name = "q4k_attention_tree"
+    if rc != OK:
+        raise Q4KError(rc, name)
+    return out
+
+
+def attention(q, cache: KVCache, sequences: Sequences, scale: Optional[float] = None, out=None, stream=None):
+    """Causal attention of the new tokens over their sequences in the cache
+    (q4k_attention): q float32 [T, q_heads, head_dim], as kv_append gives it, query
+    head h on key head h // (q_heads // kv_heads); whole prompts, chunks behind a
+    context and single tokens, packed as ``sequences`` says.  ``scale`` is
+    head_dim ** -0.5 where none is given.  A token that sees nothing has a row of
+    zeros; rows behind the last sequence are left as they were (in an ``out`` made
+    here they hold nothing meaningful)."""
+    return _attend(q, cache, sequences, None, scale, out, stream)
+
+
+def attention_tree(q, cache: KVCache, sequences: Sequences, mask, scale: Optional[float] = None, out=None,
+                   stream=None):
+    """Attention of drafted tokens that form a tree (q4k_attention_tree): every new
+    token sees what was in its sequence before, and the new tokens of its sequence
+    whose bit is set in its row of mask, int32 or uint32 [T, words] (bit i % 32 of
+    word i // 32: the sequence's new token i; its own bit has to be set too)."""
+    if mask is None:
+        raise ValueError("mask must be int32 or uint32 [T, words]")
+    return _attend(q, cache, sequences, mask, scale, out, stream)
 
 
 def matmul_swiglu(w_gate, w_up, x, out=None, stream=None):
