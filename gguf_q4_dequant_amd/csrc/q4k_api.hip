@@ -140,6 +140,35 @@ hipError_t workspace(hipStream_t stream, size_t bytes, float **scratch_out, int 
     return hipSuccess;
 }
 
+namespace {
+constexpr int kCounterSlot = -1;  // beside the workspace's slots
+__global__ __launch_bounds__(256) void clear_words(uint32_t *words) { words[blockIdx.x * 256 + threadIdx.x] = 0; }
+}  // namespace
+
+hipError_t counters(hipStream_t stream, uint32_t **words) {
+    static_assert(kCounters % 256 == 0, "whole workgroups");
+    *words = nullptr;
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return err;
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    Buffer &b = g_ws[std::make_pair(std::make_pair(dev, reinterpret_cast<uintptr_t>(stream)), kCounterSlot)];
+    if (!b.ptr) {
+        Buffer fresh;
+        err = grow(fresh, kCounters * sizeof(uint32_t));
+        if (err != hipSuccess) return err;
+        hipLaunchKernelGGL(clear_words, dim3(kCounters / 256), dim3(256), 0, stream, static_cast<uint32_t *>(fresh.ptr));
+        err = hipGetLastError();
+        if (err != hipSuccess) {
+            (void)hipFree(fresh.ptr);
+            return err;
+        }
+        b = fresh;
+    }
+    *words = static_cast<uint32_t *>(b.ptr);
+    return hipSuccess;
+}
+
 hipError_t allow_dynamic_lds(const void *kernel, int bytes) {
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);

@@ -12,8 +12,9 @@
 // the scores' registers are the second product's operand as they are (the order
 // of the keys within a step is free, as long as V^T is read in the same one).
 // The queries (times scale, log2 e and a power of two per row) and the weights
-// are float32 values split into two of 16 bits, so both products run twice:
-// 8 * head_dim operations per row and key instead of 4, at float32 accuracy.
+// are float32 values split into two binary16 numbers (over a bfloat16 cache, three
+// bfloat16 ones), so both products run twice (three times): 8 (12) * head_dim
+// operations per row and key instead of 4, at float32 accuracy.
 //
 // Copies.  Keys and values go from memory to LDS as they are stored, 16 bytes a
 // lane, one tile ahead of the products; what has no place (behind the sequence,
@@ -28,10 +29,9 @@
 // in part is looked through, and if it holds such a value (never, in earnest)
 // its values are multiplied as zeros and the rows that see one are made NaN.
 //
-// Few tiles are split along the keys (find_unit): the total of key tiles is
-// divided by the workgroups that fill the card, each takes at most that many of
-// one sequence, and a second launch joins the parts.  The lengths stay on the
-// device; every workgroup works the division out by itself.
+// Few row tiles are split along the keys (Piece): the workgroups that fill the
+// card take equal shares of all key tiles, and a second launch joins the parts.
+// The lengths stay on the device; every workgroup works its share out by itself.
 #include <math.h>
 
 #include "q4k_cache.h"
@@ -48,6 +48,10 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
+struct Part {  // a row tile's units
+    int unit0, chunks;
+};
+
 struct Attend {
     Paged p;
     const float *q;
@@ -55,56 +59,76 @@ struct Attend {
     const unsigned *mask;  // null: causal
     float *part;           // split: outputs of the units, [units * kv_heads][rows][head_dim] ...
     float *part_ml;        // ... and their maxima and sums, [units * kv_heads][rows][2]
+    Part *plan;            // split, many rows: [slots], for the launch that joins them
+    uint32_t *counters;    // split, few rows: the units of a row tile that have ended
+    int64_t slots;
     int words;
     int q_heads;
     int group;   // query heads of a key head
-    int target;  // split: workgroups of a key head to aim at; 0: one unit per tile
-    int least;   // split: key tiles of a unit at least
-    int units;   // workgroups of a key head in the grid
-    int tiles;   // row tiles at most
+    int target;  // split: workgroups of a key head; 0: one for every row tile
+    int least;   // split: key tiles of a workgroup at least
+    int units;   // of a key head, at most (without a split: row tiles)
     float scale;
 };
 
 __device__ const __align__(16) uint8_t kZeros[16] = {};
 
+constexpr int kCus = 256;
 constexpr float kBias = 13.f;  // weights are 2^(s - max + 13): binary16's subnormal numbers begin 2^-27 below the largest
+constexpr float kSlack = 2.75f;  // a row's maximum may be this much above the one in use: weights stay below 2^15.75
 constexpr float kLog2e = 1.4426950408889634f;
 
+// x less the lower or upper half of h, exactly: the instruction reads binary16 halves as
+// they are (the compiler would convert each of them first).
+__device__ __forceinline__ float less_low(float x, half2v h) {
+    float y;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(y) : "v"(h), "v"(x));
+    return y;
+}
+__device__ __forceinline__ float less_high(float x, half2v h) {
+    float y;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(y) : "v"(h), "v"(x));
+    return y;
+}
+
+// Float32 values in parts of 16 bits: two of binary16 (22 bits), three of bfloat16 (24).
 template <int kType>
 struct Math {  // binary16 (e4m3 widened to it)
     typedef half8v v8;
+    static constexpr int kParts = 2;
     static constexpr bool kScaled = true;
     __device__ static f32x16 mfma32(v8 a, v8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
     __device__ static f32x4 mfma16(v8 a, v8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-    __device__ static void split(const float *x, v8 &hi, v8 &lo) {
+    __device__ static void split(const float *x, v8 *parts) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
             const half2v h = __builtin_convertvector((f32x2{x[i], x[i + 1]}), half2v);
-            const half2v l = __builtin_convertvector(
-                (f32x2{fmaf(static_cast<float>(h.x), -1.f, x[i]), fmaf(static_cast<float>(h.y), -1.f, x[i + 1])}), half2v);
-            hi[i] = h.x;
-            hi[i + 1] = h.y;
-            lo[i] = l.x;
-            lo[i + 1] = l.y;
+            const half2v l = __builtin_convertvector((f32x2{less_low(x[i], h), less_high(x[i + 1], h)}), half2v);
+            parts[0][i] = h.x;
+            parts[0][i + 1] = h.y;
+            parts[1][i] = l.x;
+            parts[1][i + 1] = l.y;
         }
     }
 };
 template <>
 struct Math<Q4K_KV_BF16> {
     typedef bf8v v8;
+    static constexpr int kParts = 3;
     static constexpr bool kScaled = false;
     __device__ static f32x16 mfma32(v8 a, v8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
     __device__ static f32x4 mfma16(v8 a, v8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-    __device__ static void split(const float *x, v8 &hi, v8 &lo) {
+    __device__ static void split(const float *x, v8 *parts) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const bf2v h = __builtin_convertvector((f32x2{x[i], x[i + 1]}), bf2v);
-            const bf2v l = __builtin_convertvector(
-                (f32x2{x[i] - static_cast<float>(h.x), x[i + 1] - static_cast<float>(h.y)}), bf2v);
-            hi[i] = h.x;
-            hi[i + 1] = h.y;
-            lo[i] = l.x;
-            lo[i + 1] = l.y;
+            f32x2 rest = {x[i], x[i + 1]};
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const bf2v h = __builtin_convertvector(rest, bf2v);
+                parts[k][i] = h.x;
+                parts[k][i + 1] = h.y;
+                rest = f32x2{rest.x - static_cast<float>(h.x), rest.y - static_cast<float>(h.y)};
+            }
         }
     }
 };
@@ -132,6 +156,12 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t *p) {
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory", "m0");
+}
+// The same from base + offset, the base uniform.
+__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t offset, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane(dst))
                  : "memory", "m0");
 }
@@ -171,6 +201,7 @@ struct Pages {
     const int *row;
     const uint8_t *k, *v;  // of the key head
     uint64_t page_bytes;
+    uint64_t missing;  // lanes whose entry is no page
     int first, entry;
     int max_pages, pages, shift, row_bytes;
     int stop;  // keys at and behind it are not there
@@ -188,6 +219,7 @@ struct Pages {
         stop = stop_;
         first = -64;
         entry = -1;
+        missing = ~0ull;
     }
     // Makes the pages of keys j0 .. j0 + 63 at most available.
     __device__ void look_up(int j0, int keys) {
@@ -196,7 +228,13 @@ struct Pages {
             const int at = first + (threadIdx.x & 63);
             entry = at < max_pages ? row[at] : -1;
             if (entry >= pages) entry = -1;
+            missing = __ballot(entry < 0);
         }
+    }
+    // Whether keys j0 .. j0 + keys - 1 are all there.
+    __device__ bool whole(int j0, int keys) const {
+        const int at = (j0 >> shift) - first, more = ((j0 + keys - 1) >> shift) - (j0 >> shift);
+        return j0 + keys <= stop && (missing >> at & (2ull << more) - 1) == 0;
     }
     // The page of key j (of this look_up's keys), -1 if it is not there.
     __device__ int page_of(int j) const {
@@ -211,9 +249,28 @@ struct Pages {
 
 // Copies COPIES KB of a tile's keys and of its values, from byte `at` of the tile on.
 template <int RB, int COPIES>
-__device__ __forceinline__ void copy_rows(const Pages &g, int j0, int at, uint32_t k_lds, uint32_t v_lds) {
+__device__ __forceinline__ void copy_rows(const Pages &g, int j0, bool whole, int at, uint32_t k_lds, uint32_t v_lds) {
     constexpr int kPieces = RB / 16, kRows = 1024 / RB;
     const int lane = threadIdx.x & 63;
+    if (whole && g.row_bytes == RB && 1 << g.shift >= kRows) {
+        // Every copy's rows are in one page: a uniform address, and the lane's place
+        // behind it.  The swizzles are exclusive ors of bits of the row, and the
+        // copy's number has bits of its own in it.
+        static_assert((COPIES & (COPIES - 1)) == 0, "rows of a copy: the first copy's with bits set");
+        const int row = at / RB + lane / kPieces;
+        const uint32_t in_copy = lane / kPieces * RB;
+        uint32_t xk = (lane % kPieces ^ swizzle_k<RB>(row)) * 16, xv = (lane % kPieces ^ swizzle_v<RB>(row)) * 16;
+        asm volatile("" : "+v"(xk), "+v"(xv));  // (two registers kept, not two for every copy)
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            const int j = __builtin_amdgcn_readfirstlane(j0 + (at + i * 1024) / RB);
+            const int page = __builtin_amdgcn_readlane(g.entry, (j >> g.shift) - g.first);
+            const uint64_t off = g.offset(page, j);
+            copy_to_lds(g.k + off, in_copy + (xk ^ swizzle_k<RB>(i * kRows) * 16), k_lds + at + i * 1024);
+            copy_to_lds(g.v + off, in_copy + (xv ^ swizzle_v<RB>(i * kRows) * 16), v_lds + at + i * 1024);
+        }
+        return;
+    }
 #pragma unroll 4
     for (int i = 0; i < COPIES; ++i) {
         const int row = (at + i * 1024) / RB + lane / kPieces, piece = lane % kPieces;
@@ -229,7 +286,8 @@ __device__ __forceinline__ void copy_rows(const Pages &g, int j0, int at, uint32
 }
 
 // Bit l: key j0 + l has a place (keys: 32 or 64).
-__device__ __forceinline__ uint64_t there(const Pages &g, int j0, int keys) {
+__device__ __forceinline__ uint64_t there(const Pages &g, int j0, bool whole, int keys) {
+    if (whole) return ~0ull;
     const int lane = threadIdx.x & 63;
     const int page = g.page_of(j0 + min(lane, keys - 1));
     return __ballot(page >= 0 && lane < keys);
@@ -271,83 +329,144 @@ __device__ __forceinline__ bool set_apart(uint8_t *v, int at, uint8_t *marks) {
 }
 
 // ---- the division of the work ---------------------------------------------------
+//
+// A key head's work is one line of key tiles: those of the first row tile of the
+// first sequence that has new tokens, those of the next one, and so on.  Where
+// there are fewer row tiles than workgroups that the card holds (a.target), the
+// line is cut into that many equal pieces, so that all of them end at the same
+// time whatever the lengths are; workgroup w takes piece w.  What it has of a row
+// tile is a unit, number w + (number of the row tile): either number grows by
+// one from unit to unit, so a row tile's units follow each other.  With as many
+// row tiles or more, every workgroup takes one.
 
 struct Unit {
-    int b, first, n;    // sequence, its first row of q, its new tokens
-    int length;         // its tokens
-    int tile;           // of its row tiles
-    int chunk, chunks;  // of its keys
-    int size;           // key tiles of a chunk
-    int64_t unit0;      // the tile's first unit
+    int b, first, n;  // sequence, its first row of q, its new tokens
+    int length;       // its tokens
+    int tile;         // of its row tiles
+    int begin, end;   // key tiles
+    int64_t number;
+    int unit0, units;  // the row tile's
+    int64_t row_tile;  // its number
 };
 
-// Unit (kByTile: row tile) number id of a key head.  Sequences have
-// tiles_b = ceil(n_b * group / ROWS) tiles of chunks_b = ceil(keys_b / size) units.
-// Every lane returns the same; false where there is no such unit.
-template <int ROWS, int KT, bool kByTile>
-__device__ __forceinline__ bool find_unit(const Attend &a, int64_t id, Unit &u) {
-    const Paged &p = a.p;
-    const int lane = threadIdx.x & 63;
-    const int capacity = p.max_pages << p.shift;
-    int first = 0, n = 0, length = 0;
-    int64_t tiles = 0, key_tiles = 0;
-    const auto load = [&](int b) {
+// Where the plan of a sequence's row tile is kept (below tokens * group / ROWS + count).
+template <int ROWS>
+__device__ __forceinline__ int64_t slot_of(const Attend &a, int b, int first, int64_t tile) {
+    return static_cast<int64_t>(first) * a.group / ROWS + b + tile;
+}
+
+// 64 sequences from b on, one a lane: their row tiles, the key tiles of one (at
+// least 1: a row that sees nothing has its zeros written), and both summed up to
+// and with them.
+template <int ROWS, int KT>
+struct Span {
+    int first, n, length, key_tiles;
+    int64_t tiles, line, tiles_sum, line_sum;
+    __device__ Span(const Attend &a, int b, int64_t tiles_before, int64_t line_before) {
+        const Paged &p = a.p;
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));  // (no addresses kept from one unit to the next)
         first = n = length = 0;
-        if (b < p.count) {
-            first = offset_of(p, b);
-            n = max(offset_of(p, b + 1) - first, 0);
-            length = max(p.lengths[b], 0);  // (without tokens nothing is seen)
+        if (b + lane < p.count) {
+            first = offset_of(p, b + lane);
+            n = max(offset_of(p, b + lane + 1) - first, 0);
+            length = max(p.lengths[b + lane], 0);  // (without tokens nothing is seen)
         }
         tiles = (static_cast<int64_t>(n) * a.group + ROWS - 1) / ROWS;
-        key_tiles = (min(length, capacity) + KT - 1) / KT;
-    };
-    int size = INT_MAX;
-    if (a.target) {
-        int64_t all = 0;
-        for (int b = lane; b < ((p.count + 63) & ~63); b += 64) {
-            load(b);
-            all += tiles * key_tiles;
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
-        size = static_cast<int>(max((all + a.target - 1) / a.target, static_cast<int64_t>(a.least)));
-    }
-    int64_t before = 0, units_before = 0;  // of the sequences looked through
-    for (int b0 = 0; b0 < p.count; b0 += 64) {
-        if (!a.target || p.count > 64) load(b0 + lane);
-        const int64_t chunks = max(key_tiles / size + (key_tiles % size != 0), static_cast<int64_t>(1));
-        const int64_t units = tiles * chunks, mine = kByTile ? tiles : units;
-        int64_t sum = mine, unit_sum = units;
+        key_tiles = max((min(length, p.max_pages << p.shift) + KT - 1) / KT, 1);
+        line = a.target ? tiles * key_tiles : tiles;
+        tiles_sum = tiles;
+        line_sum = line;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const int64_t x = __shfl_up(sum, o), y = __shfl_up(unit_sum, o);
+            const int64_t x = __shfl_up(tiles_sum, o), y = __shfl_up(line_sum, o);
             if (lane >= o) {
-                sum += x;
-                unit_sum += y;
+                tiles_sum += x;
+                line_sum += y;
             }
         }
-        const uint64_t behind = __ballot(before + sum > id);
-        if (behind) {
-            const int l = __builtin_ctzll(behind);
-            const int64_t rest = id - before - (__shfl(sum, l) - __shfl(mine, l));
-            u.b = b0 + l;
-            u.first = __builtin_amdgcn_readfirstlane(__shfl(first, l));
-            u.n = __builtin_amdgcn_readfirstlane(__shfl(n, l));
-            u.length = __builtin_amdgcn_readfirstlane(__shfl(length, l));
-            u.chunks = __builtin_amdgcn_readfirstlane(static_cast<int>(__shfl(chunks, l)));
-            const int kt = __builtin_amdgcn_readfirstlane(static_cast<int>(__shfl(key_tiles, l)));
-            const int r = __builtin_amdgcn_readfirstlane(static_cast<int>(rest));
-            u.tile = kByTile ? r : r / u.chunks;
-            u.chunk = kByTile ? 0 : r % u.chunks;
-            u.size = (kt + u.chunks - 1) / u.chunks;
-            u.unit0 = units_before + (__shfl(unit_sum, l) - __shfl(units, l)) + static_cast<int64_t>(u.tile) * u.chunks;
+        tiles_sum += tiles_before;
+        line_sum += line_before;
+    }
+};
+
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+    const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(high) << 32 | low);
+}
+
+// a / b of uniform numbers that are not negative: nearly always of 32 bits, where
+// a division takes a tenth of the time (four of 64 bits took 2 us of a workgroup's start).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// A workgroup's piece of the line.  kKeep: the 64 sequences last looked through stay
+// in registers; without it (where the products need them) they are looked through
+// again for every unit.
+template <int ROWS, int KT, bool kKeep>
+struct Piece {
+    typedef Span<ROWS, KT> S;
+    const Attend &a;
+    S kept;
+    int kept_b;
+    int64_t at, stop, size, workgroup;
+
+    __device__ Piece(const Attend &a_, int64_t w) : a(a_), kept(a_, 0, 0, 0), kept_b(0), workgroup(w) {
+        size = 1;
+        if (a.target) {
+            int64_t all = __shfl(kept.line_sum, 63);
+            for (int b = 64; b < a.p.count; b += 64) all = __shfl(S(a, b, 0, all).line_sum, 63);
+            size = max(uniform(quotient(uniform(all) + a.target - 1, a.target)), static_cast<int64_t>(a.least));
+        }
+        at = w * size;
+        stop = at + size;
+    }
+    // The piece's next unit; false behind its last.  Every lane has the same.
+    __device__ bool next(Unit &u) {
+        if (at >= stop) return false;
+        if constexpr (!kKeep) {
+            kept = S(a, 0, 0, 0);
+            kept_b = 0;
+        }
+        uint64_t behind;
+        while ((behind = __ballot(kept.line_sum > at)) == 0) {
+            kept_b += 64;
+            if (kept_b >= a.p.count) return false;
+            kept = S(a, kept_b, __shfl(kept.tiles_sum, 63), __shfl(kept.line_sum, 63));
+        }
+        const int l = __builtin_ctzll(behind);
+        u.b = kept_b + l;
+        u.first = __builtin_amdgcn_readlane(kept.first, l);
+        u.n = __builtin_amdgcn_readlane(kept.n, l);
+        u.length = __builtin_amdgcn_readlane(kept.length, l);
+        const int64_t rest = at - uniform(__shfl(kept.line_sum - kept.line, l));
+        if (!a.target) {
+            u.tile = static_cast<int>(rest);
+            u.begin = 0;
+            u.end = INT_MAX;
+            u.number = u.row_tile = at;
+            u.unit0 = static_cast<int>(at);
+            u.units = 1;
+            at += 1;
             return true;
         }
-        before += __shfl(sum, 63);
-        units_before += __shfl(unit_sum, 63);
+        const int keys = __builtin_amdgcn_readlane(kept.key_tiles, l);
+        u.tile = static_cast<int>(uniform(quotient(rest, keys)));
+        u.begin = static_cast<int>(rest - static_cast<int64_t>(u.tile) * keys);
+        u.end = static_cast<int>(min(static_cast<int64_t>(keys), u.begin + (stop - at)));
+        const int64_t begin = at - u.begin;  // the row tile's place on the line
+        u.row_tile = uniform(__shfl(kept.tiles_sum - kept.tiles, l)) + u.tile;
+        u.number = workgroup + u.row_tile;
+        const int64_t w0 = uniform(quotient(begin, size)), w1 = uniform(quotient(begin + keys - 1, size));
+        u.unit0 = static_cast<int>(min(w0 + u.row_tile, static_cast<int64_t>(a.units)));
+        u.units = static_cast<int>(w1 - w0) + 1;
+        at += u.end - u.begin;
+        return true;
     }
-    return false;
-}
+};
 
 // A lane's row: its query, its place in the outputs and what it sees.
 struct Row {
@@ -418,11 +537,12 @@ template <int kType, int DP>
 struct TileShape {
     static constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2;
     static constexpr int RB = DP * kSize;             // bytes of a row
-    static constexpr int KT = DP == 256 ? 32 : 64;    // keys of a tile
+    static constexpr int KT = DP == 256 || (kType == Q4K_KV_BF16 && DP == 128) ? 32 : 64;  // keys of a tile
     static constexpr int kBytes = KT * RB;            // of K, and of V
     static constexpr int kCopies = kBytes / 4096;     // of a wave
     static constexpr int kMarks = KT * DP / 8;        // a bit per value
-    static constexpr int kLds = 4 * kBytes + kMarks + 16;
+    static constexpr int kThird = kType == Q4K_KV_BF16 ? kTileRows * DP * 2 : 0;  // the queries' third parts
+    static constexpr int kLds = 4 * kBytes + kMarks + 16 + kThird;
 };
 
 template <int kType, int DP>
@@ -434,12 +554,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     extern __shared__ __align__(16) uint8_t lds[];
     uint8_t *const marks = lds + 4 * S::kBytes;
     int *const flag = reinterpret_cast<int *>(marks + S::kMarks);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
     const int head = blockIdx.x % a.p.kv_heads;
     // the last tiles of a prompt have the most keys: they go first
-    const int64_t id = a.units - 1 - static_cast<int64_t>(blockIdx.x / a.p.kv_heads);
-    Unit u;
-    if (!find_unit<kTileRows, KT, false>(a, id, u)) return;
+    const int64_t w0 = blockIdx.x / a.p.kv_heads;
+    Piece<kTileRows, KT, false> piece(a, a.target ? w0 : a.units - 1 - w0);
+    for (Unit u; piece.next(u); __syncthreads()) {
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
+    const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 31, half = lane >> 5;
     const int before = u.length - u.n;
     const int row0 = u.tile * kTileRows, rows = u.n * a.group;
     const int capacity = a.p.max_pages << a.p.shift;
@@ -448,7 +570,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     const int most = a.mask ? u.length : before + last + 1;
     const int common = a.mask ? before : before + row0 / a.group + 1;
     const int stop = max(min(most, capacity), 0);
-    const int t0 = u.chunk * u.size, t1 = min((stop + KT - 1) / KT, u.chunks == 1 ? INT_MAX : t0 + u.size);
+    const int t0 = u.begin, t1 = min((stop + KT - 1) / KT, u.end);
+    // the launch behind this one finds the row tile's units here
+    if (a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) {
+        const int64_t slot = slot_of<kTileRows>(a, u.b, u.first, u.tile);
+        if (slot < a.slots) a.plan[slot] = Part{u.unit0, u.units};
+    }
     const Row w = row_of(a, u, row0 + wave * 32 + col, head);
     const bool idle = row0 + wave * 32 >= rows;  // no row of this wave is real
 
@@ -459,12 +586,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     if (threadIdx.x == 0) *flag = -1;
     if (t0 < t1) {
         pages.look_up(t0 * KT, KT);
-        here = there(pages, t0 * KT, KT);
-        copy_rows<RB, S::kCopies>(pages, t0 * KT, piece0, base, base + 2 * S::kBytes);
+        const bool whole = pages.whole(t0 * KT, KT);
+        here = there(pages, t0 * KT, whole, KT);
+        copy_rows<RB, S::kCopies>(pages, t0 * KT, whole, piece0, base, base + 2 * S::kBytes);
     }
 
     // the wave's queries as the second operand of S^T = K Q^T: lane's row, 8 dimensions a step
     v8 qh[NS], ql[NS];
+    u32x4 *const third = reinterpret_cast<u32x4 *>(lds + 4 * S::kBytes + S::kMarks + 16) + wave * NS * 64 + lane;  // (of registers there are too few)
     float factor = 1.f;
     {
         const float by = a.scale * kLog2e * a.p.k_scale;
@@ -495,7 +624,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e);
             }
-            M::split(x, qh[s], ql[s]);
+            v8 parts[M::kParts];
+            M::split(x, parts);
+            qh[s] = parts[0];
+            ql[s] = parts[1];
+            if constexpr (M::kParts == 3) third[s * 64] = __builtin_bit_cast(u32x4, parts[2]);
         }
     }
 
@@ -511,8 +644,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
         v_row = 4 * half + (li >> 2);
         v_c = 2 * dh + ((li & 3) >> 1);
     }
+    constexpr int kEight = 1;  // swizzle_v(row + 8) ^ swizzle_v(row), row below 8
     const int v_at = v_row * RB + 8 * (li & 1), v_x = v_c ^ swizzle_v<RB>(v_row);
-    const int v_at2 = v_at + 8 * RB, v_x2 = v_c ^ swizzle_v<RB>(v_row + 8);
 
     f32x16 acc[ND];
 #pragma unroll
@@ -528,8 +661,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
         const uint64_t now = here;
         if (t + 1 < t1) {
             pages.look_up((t + 1) * KT, KT);
-            here = there(pages, (t + 1) * KT, KT);
-            copy_rows<RB, S::kCopies>(pages, (t + 1) * KT, piece0, base + (buf ^ 1) * S::kBytes,
+            const bool whole = pages.whole((t + 1) * KT, KT);
+            here = there(pages, (t + 1) * KT, whole, KT);
+            copy_rows<RB, S::kCopies>(pages, (t + 1) * KT, whole, piece0, base + (buf ^ 1) * S::kBytes,
                                       base + (2 + (buf ^ 1)) * S::kBytes);
         }
         const uint8_t *kt = lds + buf * S::kBytes;
@@ -547,8 +681,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
         vis &= whole;
         if (__ballot(vis != 0) == 0) continue;  // nothing for this wave
         f32x16 s[KS];
-        int kx = k_x;
-        asm volatile("" : "+v"(kx));  // the pieces' places are worked out again, not kept: registers are short here
+        int kx = k_x, vx = v_x;
+        asm volatile("" : "+v"(kx), "+v"(vx));  // the pieces' places are worked out again, not kept: registers are short here
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
 #pragma unroll
@@ -566,6 +700,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
                     const v8 x0 = __builtin_bit_cast(v8, x);
                     s[k] = M::mfma32(x0, qh[c], s[k]);
                     s[k] = M::mfma32(x0, ql[c], s[k]);
+                    if constexpr (M::kParts == 3) s[k] = M::mfma32(x0, __builtin_bit_cast(v8, third[c * 64]), s[k]);
                 }
             }
         }
@@ -584,11 +719,19 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, s[k][r]);
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float m1 = fmaxf(m, top * factor);
-        const float zero = m1 == -INFINITY ? 0.f : m1;
-        const float fade = __builtin_amdgcn_exp2f(m - zero);
-        m = m1;
-        const float shift = kBias - zero;
+        top *= factor;
+        // The output is corrected only where a maximum has risen by more than kSlack (or from nothing).
+        if (__ballot(!(top - m <= kSlack) && top != -INFINITY) != 0) {
+            const float m1 = fmaxf(m, top);
+            const float fade = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            sum *= fade;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[d][r] *= fade;
+        }
+        const float shift = kBias - (m == -INFINITY ? 0.f : m);
         float part = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
@@ -597,37 +740,31 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
                 s[k][r] = __builtin_amdgcn_exp2f(fmaf(s[k][r], factor, shift));
                 part += s[k][r];
             }
-        sum = fmaf(sum, fade, part);
-        if (__ballot(fade != 1.f) != 0) {
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[d][r] *= fade;
-        }
+        sum += part;
 #pragma unroll
         for (int q = 0; q < KT / 16; ++q) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = s[q >> 1][8 * (q & 1) + i];
-            v8 ph, pl;
-            M::split(x, ph, pl);
+            v8 parts[M::kParts];
+            M::split(x, parts);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 v8 y;
                 const uint8_t *vq = vt + q * 16 * RB;
                 if constexpr (kType == Q4K_KV_E4M3) {
                     const i32x2 z = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (__attribute__((address_space(3))) i32x2 *)(vq + v_at + (((2 * d) ^ v_x) << 4)));
+                        (__attribute__((address_space(3))) i32x2 *)(vq + v_at + (((2 * d) ^ vx) << 4)));
                     y = widened(z.x, z.y);
                 } else {
                     const s16x4 z0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4 *)(vq + v_at + (((4 * d) ^ v_x) << 4)));
+                        (__attribute__((address_space(3))) s16x4 *)(vq + v_at + (((4 * d) ^ vx) << 4)));
                     const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4 *)(vq + v_at2 + (((4 * d) ^ v_x2) << 4)));
+                        (__attribute__((address_space(3))) s16x4 *)(vq + v_at + 8 * RB + (((4 * d) ^ vx ^ kEight) << 4)));
                     y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
                 }
-                acc[d] = M::mfma32(y, ph, acc[d]);
-                acc[d] = M::mfma32(y, pl, acc[d]);
+#pragma unroll
+                for (int i = 0; i < M::kParts; ++i) acc[d] = M::mfma32(y, parts[i], acc[d]);
             }
         }
         if (apart) {  // rows that see a marked value get NaN there
@@ -647,40 +784,35 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     }
 
     sum += __shfl_xor(sum, 32);
-    if (idle || !w.real) return;
-    if (u.chunks == 1) {
-        int r0 = row0 + wave * 32 + col;
-        asm volatile("" : "+v"(r0));  // worked out again rather than kept over the loop
-        float *const out = a.out + row_of(a, u, r0, head).at;
-        const float f = sum == 0.f ? 0.f : a.p.v_scale / sum;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const int at = 32 * d + 2 * r + 4 * half;
-                if (at < a.p.head_dim) {
-                    f32x4 y;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = sum == 0.f ? 0.f : acc[d][r + i] * f;
-                    *reinterpret_cast<f32x4 *>(out + at) = y;
-                }
-            }
-    } else {
-        const int64_t at0 = (id * a.p.kv_heads + head) * kTileRows + wave * 32 + col;
+    int r0 = row0 + wave * 32 + col, D = a.p.head_dim;
+    asm volatile("" : "+v"(r0), "+s"(D));  // worked out again rather than kept over the loops
+    const Row o = row_of(a, u, r0, head);
+    if (!o.real) continue;
+    float *to = a.out + o.at;
+    float f = sum == 0.f ? 0.f : a.p.v_scale / sum;
+    if (u.units > 1) {
+        if (u.number >= a.units) continue;  // (offsets out of order)
+        const int64_t at = (u.number * a.p.kv_heads + head) * kTileRows + wave * 32 + col;
         if (half == 0) {
-            a.part_ml[2 * at0] = m;
-            a.part_ml[2 * at0 + 1] = sum;
+            a.part_ml[2 * at] = m;
+            a.part_ml[2 * at + 1] = sum;
         }
-        if (t0 >= t1) return;
+        if (m == -INFINITY && sum == 0.f) continue;  // the output is not read
+        to = a.part + at * D;
+        f = 1.f;
+    }
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const int at = 32 * d + 2 * r + 4 * half;
-                if (at < a.p.head_dim)
-                    *reinterpret_cast<f32x4 *>(a.part + at0 * a.p.head_dim + at) =
-                        f32x4{acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]};
+        for (int r = 0; r < 16; r += 4) {
+            const int at = 32 * d + 2 * r + 4 * half;
+            if (at < D) {
+                f32x4 y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = f == 0.f ? 0.f : acc[d][r + i] * f;
+                *reinterpret_cast<f32x4 *>(to + at) = y;
             }
+        }
     }
 }
 
@@ -690,20 +822,37 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
 // own two buffers in LDS and its own maximum, sum and output, and nothing to
 // wait for but its own copies; the waves' parts are joined at the end.
 // Products of 16 x 16 x 32.
+//
+// Units of one row tile are joined by the workgroup of the last one to end,
+// without a second launch (3 to 5 us of 12 over a short context).  Their parts
+// go past the L2s, which the card's eight dies do not share: stores and loads of
+// the agent's scope, each wave's stores waited for before the workgroup counts
+// its unit as ended.  They are added in the units' order whichever came last.
 
 constexpr int kFewRows = 16;
+
+// Two numbers to and from memory that all dies see.
+__device__ __forceinline__ void share(float *at, float x, float y) {
+    const uint64_t pair = static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x);
+    __hip_atomic_store(reinterpret_cast<uint64_t *>(at), pair, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 shared_pair(const float *at) {
+    const uint64_t pair = __hip_atomic_load(reinterpret_cast<const uint64_t *>(at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return f32x2{__uint_as_float(static_cast<uint32_t>(pair)), __uint_as_float(static_cast<uint32_t>(pair >> 32))};
+}
 
 template <int kType, int DP>
 struct FewShape {
     static constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2;
     static constexpr int RB = DP * kSize;
-    static constexpr int kWaves = RB == 512 ? 2 : 4;
+    static constexpr int kWaves = RB == 512 ? 2 : RB == 256 ? 4 : 8;  // 128 KB of LDS
     static constexpr int kBytes = 32 * RB;  // of a tile's K, and of its V
     static constexpr int kCopies = kBytes / 1024;
     static constexpr int kJoin = kWaves * kFewRows * (DP + 4) * 4;
     static constexpr int kMarks = 32 * DP / 8;  // a bit per value
     static constexpr int kOwn = 4 * kBytes + kMarks;
-    static constexpr int kLds = kWaves * kOwn > kJoin ? kWaves * kOwn : kJoin;
+    static constexpr int kEnded = kWaves * kOwn > kJoin ? kWaves * kOwn : kJoin;
+    static constexpr int kLds = kEnded + 16;
 };
 
 template <int kType, int DP>
@@ -712,12 +861,15 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     typedef Math<kType> M;
     typedef typename M::v8 v8;
     constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16;
+    static_assert((kCus + 1) * kFewRows * 8 <= S::kEnded, "the maxima and sums of every unit of a row tile");
     extern __shared__ __align__(16) uint8_t lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quarter = lane >> 4;
+    int *const ended = reinterpret_cast<int *>(lds + S::kEnded);
     const int head = blockIdx.x % a.p.kv_heads;
-    const int64_t id = blockIdx.x / a.p.kv_heads;
-    Unit u;
-    if (!find_unit<kFewRows, KT, false>(a, id, u)) return;
+    Piece<kFewRows, KT, true> piece(a, blockIdx.x / a.p.kv_heads);
+    for (Unit u; piece.next(u); __syncthreads()) {
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
+    const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 15, quarter = lane >> 4;
     const int before = u.length - u.n;
     const int row0 = u.tile * kFewRows;
     const int capacity = a.p.max_pages << a.p.shift;
@@ -726,8 +878,8 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     const int common = a.mask ? before : before + row0 / a.group + 1;
     const int stop = max(min(most, capacity), 0);
     // tiles of 32 keys: this wave's are first, first + kWaves, ...
-    const int t0 = u.chunk * u.size * S::kWaves + wave;
-    const int t1 = min((stop + 31) / 32, u.chunks == 1 ? INT_MAX : (u.chunk + 1) * u.size * S::kWaves);
+    const int t0 = u.begin * S::kWaves + wave;
+    const int t1 = u.end == INT_MAX ? (stop + 31) / 32 : min((stop + 31) / 32, u.end * S::kWaves);
     const Row w = row_of(a, u, row0 + col, head);
 
     Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
@@ -735,14 +887,15 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     const uint32_t base = lds_address(own);
     const auto copy = [&](int t, int buf) {
         pages.look_up(t * 32, 32);
-        const uint64_t is = there(pages, t * 32, 32);
-        copy_rows<RB, S::kCopies>(pages, t * 32, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
+        const bool whole = pages.whole(t * 32, 32);
+        const uint64_t is = there(pages, t * 32, whole, 32);
+        copy_rows<RB, S::kCopies>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
         return is;
     };
     uint64_t here = 0;
     if (t0 < t1) here = copy(t0, 0);
 
-    v8 qh[NS], ql[NS];
+    v8 query[NS][M::kParts];
     float factor = 1.f;
     {
         const float by = a.scale * kLog2e * a.p.k_scale;
@@ -773,7 +926,7 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e);
             }
-            M::split(x, qh[s], ql[s]);
+            M::split(x, query[s]);
         }
     }
 
@@ -816,14 +969,14 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
                 const u32x4 x = *reinterpret_cast<const u32x4 *>(kt + k * 16 * RB + k_at + (((4 * c) ^ k_x) << 4));
                 if constexpr (kType == Q4K_KV_E4M3) {
                     const half8v x0 = widened(x.x, x.y), x1 = widened(x.z, x.w);
-                    s[k] = M::mfma16(x0, qh[2 * c], s[k]);
-                    s[k] = M::mfma16(x0, ql[2 * c], s[k]);
-                    s[k] = M::mfma16(x1, qh[2 * c + 1], s[k]);
-                    s[k] = M::mfma16(x1, ql[2 * c + 1], s[k]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        s[k] = M::mfma16(x0, query[2 * c][i], s[k]);
+                        s[k] = M::mfma16(x1, query[2 * c + 1][i], s[k]);
+                    }
                 } else {
-                    const v8 x0 = __builtin_bit_cast(v8, x);
-                    s[k] = M::mfma16(x0, qh[c], s[k]);
-                    s[k] = M::mfma16(x0, ql[c], s[k]);
+#pragma unroll
+                    for (int i = 0; i < M::kParts; ++i) s[k] = M::mfma16(__builtin_bit_cast(v8, x), query[c][i], s[k]);
                 }
             }
         }
@@ -854,8 +1007,8 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
             part += x[i];
         }
         sum = fmaf(sum, fade, part);
-        v8 ph, pl;
-        M::split(x, ph, pl);
+        v8 parts[M::kParts];
+        M::split(x, parts);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
             acc[d] *= fade;
@@ -871,8 +1024,8 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
                     __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(at + 16 * RB));
                 y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
             }
-            acc[d] = M::mfma16(y, ph, acc[d]);
-            acc[d] = M::mfma16(y, pl, acc[d]);
+#pragma unroll
+            for (int i = 0; i < M::kParts; ++i) acc[d] = M::mfma16(y, parts[i], acc[d]);
         }
         if (apart) {
 #pragma unroll 1
@@ -908,6 +1061,9 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     }
     __syncthreads();
     const int quads = a.p.head_dim / 4;
+    // (offsets out of order can give more units or row tiles than there is room for)
+    const int64_t counter = u.row_tile * a.p.kv_heads + head;
+    const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && counter < kCounters;
     for (int i = threadIdx.x; i < kFewRows * quads; i += S::kWaves * 64) {
         const int r = i / quads, d = (i - r * quads) * 4;
         const Row o = row_of(a, u, row0 + r, head);
@@ -926,105 +1082,195 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
             total = fmaf(from[DP + 1], f, total);
             y += *reinterpret_cast<const f32x4 *>(from + d) * f;
         }
-        if (u.chunks == 1) {
+        if (u.units == 1) {
             const float f = a.p.v_scale / total;
             if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
             else y *= f;
             *reinterpret_cast<f32x4 *>(a.out + o.at + d) = y;
-        } else {
-            const int64_t at = (id * a.p.kv_heads + head) * kFewRows + r;
-            *reinterpret_cast<f32x4 *>(a.part + at * a.p.head_dim + d) = y;
-            if (d == 0) {
-                a.part_ml[2 * at] = top;
-                a.part_ml[2 * at + 1] = total;
-            }
+        } else if (shared) {
+            const int64_t at = (u.number * a.p.kv_heads + head) * kFewRows + r;
+            share(a.part + at * a.p.head_dim + d, y.x, y.y);
+            share(a.part + at * a.p.head_dim + d + 2, y.z, y.w);
+            if (d == 0) share(a.part_ml + 2 * at, top, total);
         }
+    }
+    if (!shared) continue;
+    // the row tile's last unit to end joins them all
+    wait_copies<0>();  // what this wave has shared is there for the others
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool last = __hip_atomic_fetch_add(a.counters + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                          static_cast<uint32_t>(u.units - 1);
+        if (last) __hip_atomic_store(a.counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *ended = last;
+    }
+    __syncthreads();
+    if (!*ended) continue;
+    const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kFewRows + r; };
+    f32x2 *const ml = reinterpret_cast<f32x2 *>(lds);  // [unit][row] maxima and sums (the parts in LDS have been read)
+    for (int i = threadIdx.x; i < u.units * kFewRows; i += S::kWaves * 64)
+        ml[i] = shared_pair(a.part_ml + 2 * place(i / kFewRows, i % kFewRows));
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFewRows * quads; i += S::kWaves * 64) {
+        const int r = i / quads, d = (i - r * quads) * 4;
+        const Row o = row_of(a, u, row0 + r, head);
+        if (!o.real) continue;
+        float top = -INFINITY, total = 0.f;
+        for (int c = 0; c < u.units; ++c) top = fmaxf(top, ml[c * kFewRows + r].x);
+        const float zero = top == -INFINITY ? 0.f : top;
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        const float *from = a.part + place(0, r) * a.p.head_dim + d;
+        const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kFewRows * a.p.head_dim;
+#pragma unroll 8
+        for (int c = 0; c < u.units; ++c) {
+            const float f = __builtin_amdgcn_exp2f(ml[c * kFewRows + r].x - zero);
+            const f32x2 y0 = shared_pair(from + c * step), y1 = shared_pair(from + c * step + 2);
+            total = fmaf(ml[c * kFewRows + r].y, f, total);
+            y += f32x4{y0.x, y0.y, y1.x, y1.y} * f;
+        }
+        const float f = a.p.v_scale / total;
+        if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
+        else y *= f;
+        *reinterpret_cast<f32x4 *>(a.out + o.at + d) = y;
+    }
     }
 }
 
 // ---- the units' parts joined -------------------------------------------------------
 //
-// A wave per row: its units' maxima and sums by lanes, then their outputs in
-// ascending order.  A unit whose maximum is -inf has seen nothing (and may have
-// written no output).
+// A row's units: their maxima and sums by lanes, then their outputs, four values
+// a lane; the lanes that one unit's output leaves free take the next units, and
+// their sums are added in a fixed order.  A unit whose maximum is -inf has seen
+// nothing (and may have written no output).  kThreads a row: a workgroup where
+// there are few rows (and many units), else a wave.
 
-template <int ROWS, int KT>
+template <int ROWS, int kThreads>
 __global__ __launch_bounds__(256) void join_units(const Attend a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int head = blockIdx.x % a.p.kv_heads;
-    const int rest = blockIdx.x / a.p.kv_heads;
-    const int tile = rest / (ROWS / 4), r = rest % (ROWS / 4) * 4 + wave;
-    Unit u;
-    if (!find_unit<ROWS, KT, true>(a, tile, u) || u.chunks == 1 || u.unit0 + u.chunks > a.units) return;
-    const Row w = row_of(a, u, u.tile * ROWS + r, head);
-    if (!w.real) return;
-    const int D = a.p.head_dim;
-    const auto place = [&](int c) { return ((u.unit0 + c) * a.p.kv_heads + head) * ROWS + r; };
+    constexpr int kRows = 256 / kThreads;
+    __shared__ float weights[256];
+    __shared__ __align__(16) f32x4 sums[256];
+    __shared__ float tops[4], totals[4];
+    const int mine = threadIdx.x / kThreads, tid = threadIdx.x % kThreads, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kRows + mine;  // query t, head h: uniform in a wave
+    const int t = static_cast<int>(id / a.q_heads), h = static_cast<int>(id - static_cast<int64_t>(t) * a.q_heads);
+    const Paged &p = a.p;
+    Part part = {0, 0};
+    int head = 0, r = 0;
+    if (t < p.tokens) {
+        const int b = last_started(p.count, t, [&](int i) { return offset_of(p, i); });
+        const int first = offset_of(p, b), end = offset_of(p, b + 1);
+        if (t >= first && t < end) {
+            head = h / a.group;
+            const int64_t row = static_cast<int64_t>(t - first) * a.group + h % a.group;
+            r = static_cast<int>(row % ROWS);
+            const int64_t slot = slot_of<ROWS>(a, b, first, row / ROWS);
+            if (slot < a.slots) part = a.plan[slot];
+        }
+    }
+    // (what offsets out of order left in the plan is not followed)
+    const bool here = part.chunks > 1 && part.unit0 >= 0 && part.chunks <= a.units - part.unit0;
+    const int chunks = here ? part.chunks : 0;
+    const int D = p.head_dim, quads = D / 4, streams = kThreads / quads;
+    const int quad = tid % quads, stream = tid / quads;
+    const auto place = [&](int c) { return (static_cast<int64_t>(part.unit0 + c) * p.kv_heads + head) * ROWS + r; };
+    const auto sync = [&] {
+        if (kThreads > 64) __syncthreads();
+        else __builtin_amdgcn_wave_barrier();
+    };
     float top = -INFINITY;
-    for (int c = lane; c < u.chunks; c += 64) top = fmaxf(top, a.part_ml[2 * place(c)]);
+    for (int c = tid; c < chunks; c += kThreads) top = fmaxf(top, a.part_ml[2 * place(c)]);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (kThreads > 64) {
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    }
     const float zero = top == -INFINITY ? 0.f : top;
+    float *const weight = weights + mine * kThreads;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
     float total = 0.f;
-    for (int c0 = 0; c0 < u.chunks; c0 += 64) {
-        float f = 0.f;
-        bool any = false;
-        if (c0 + lane < u.chunks) {
-            const float mc = a.part_ml[2 * place(c0 + lane)];
-            any = mc != -INFINITY;
-            f = __builtin_amdgcn_exp2f(mc - zero);
-            total = fmaf(a.part_ml[2 * place(c0 + lane) + 1], f, total);
+    for (int c0 = 0; c0 < chunks; c0 += kThreads) {
+        sync();
+        const int n = min(chunks - c0, kThreads);
+        if (tid < n) {
+            const float m = a.part_ml[2 * place(c0 + tid)];
+            // -1: nothing to add, and nothing to read
+            const float f = m == -INFINITY ? -1.f : __builtin_amdgcn_exp2f(m - zero);
+            weight[tid] = f;
+            if (m != -INFINITY) total = fmaf(a.part_ml[2 * place(c0 + tid) + 1], f, total);
         }
-        uint64_t with = __ballot(any);
-        while (with) {
-            const int l = __builtin_ctzll(with);
-            with &= with - 1;
-            const float fc = __shfl(f, l);
-            if (lane * 4 < D) y += *reinterpret_cast<const f32x4 *>(a.part + place(c0 + l) * D + lane * 4) * fc;
+        sync();
+        if (stream < streams) {
+            const float *from = a.part + place(c0) * D + quad * 4;
+            const int64_t step = static_cast<int64_t>(p.kv_heads) * ROWS * D;
+#pragma unroll 8
+            for (int c = stream; c < n; c += streams) {
+                const float f = weight[c];
+                if (!(f < 0.f)) y += *reinterpret_cast<const f32x4 *>(from + c * step) * f;
+            }
         }
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
-    const float f = a.p.v_scale / total;
+    sums[threadIdx.x] = y;
+    if (kThreads > 64) {
+        if (lane == 0) totals[wave] = total;
+        __syncthreads();
+        total = (totals[0] + totals[1]) + (totals[2] + totals[3]);
+    } else {
+        sync();
+    }
+    if (!here || tid >= quads) return;
+    for (int k = 1; k < streams; ++k) y += sums[mine * kThreads + k * quads + tid];
+    const float f = p.v_scale / total;
     if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
     else y *= f;
-    if (lane * 4 < D) *reinterpret_cast<f32x4 *>(a.out + w.at + lane * 4) = y;
+    *reinterpret_cast<f32x4 *>(a.out + id * D + tid * 4) = y;
 }
 
 // ---- launches ------------------------------------------------------------------------
 
-constexpr int kCus = 256;
-
-// Row tiles of a key head at most: sum of ceil(n_b * group / rows) <= T * group / rows + count.
+// Row tiles of a key head at most: the sum of ceil(n_b * group / rows) over the
+// sequences that have new tokens (at most T of them).
 int64_t tiles_at_most(const Attend &a, int rows) {
-    return static_cast<int64_t>(a.p.tokens) * a.group / rows + min(a.p.count, a.p.tokens);
+    return (static_cast<int64_t>(a.p.tokens) * a.group + static_cast<int64_t>(min(a.p.count, a.p.tokens)) * (rows - 1)) / rows;
 }
 
 template <int ROWS, int KT, class Kernel>
 int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least, hipStream_t stream) {
     const int64_t tiles = tiles_at_most(a, ROWS), heads = a.p.kv_heads;
     int64_t target = (static_cast<int64_t>(kCus) * per_cu + heads - 1) / heads;
-    if (tiles >= target) target = 0;
+    // (as many row tiles, or not two workgroups' worth of keys in the longest sequence that can be)
+    if (tiles >= target || (static_cast<int64_t>(a.p.max_pages) << a.p.shift) <= static_cast<int64_t>(least) * KT) target = 0;
     a.target = static_cast<int>(target);
     a.least = least;
     const int64_t units = tiles + target;
-    if (units * heads > INT_MAX || tiles * heads * (ROWS / 4) > INT_MAX) return Q4K_ERR_LAUNCH;
+    if (units * heads > INT_MAX || static_cast<int64_t>(a.p.tokens) * a.q_heads > INT_MAX) return Q4K_ERR_LAUNCH;
     a.units = static_cast<int>(units);
-    a.tiles = static_cast<int>(tiles);
     if (target) {
         const size_t rows = static_cast<size_t>(units) * heads * ROWS;
         float *ws = nullptr;
-        if (workspace(stream, rows * (a.p.head_dim + 2) * sizeof(float), &ws, 0) != hipSuccess) return Q4K_ERR_ALLOC;
+        a.slots = static_cast<int64_t>(a.p.tokens) * a.group / ROWS + a.p.count;
+        const size_t bytes = rows * (a.p.head_dim + 2) * sizeof(float) + a.slots * sizeof(Part);
+        if (workspace(stream, bytes, &ws, 0) != hipSuccess) return Q4K_ERR_ALLOC;
         a.part = ws;
         a.part_ml = ws + rows * a.p.head_dim;
+        a.plan = reinterpret_cast<Part *>(a.part_ml + 2 * rows);
+        if (ROWS == kFewRows && counters(stream, &a.counters) != hipSuccess) return Q4K_ERR_ALLOC;
     }
     if (lds > 65536 && allow_dynamic_lds(reinterpret_cast<const void *>(kernel), lds) != hipSuccess) return Q4K_ERR_LAUNCH;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(units * heads)), dim3(threads), lds, stream, a);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((target ? target : tiles) * heads)), dim3(threads), lds, stream, a);
     if (hipGetLastError() != hipSuccess) return Q4K_ERR_LAUNCH;
-    if (target) {
-        hipLaunchKernelGGL((join_units<ROWS, KT>), dim3(static_cast<unsigned>(tiles * heads * (ROWS / 4))), dim3(256), 0, stream, a);
-        if (hipGetLastError() != hipSuccess) return Q4K_ERR_LAUNCH;
+    if constexpr (ROWS != kFewRows) {
+        if (target) {
+            const int outputs = a.p.tokens * a.q_heads;
+            if (outputs <= 2048)
+                hipLaunchKernelGGL((join_units<ROWS, 256>), dim3(outputs), dim3(256), 0, stream, a);
+            else
+                hipLaunchKernelGGL((join_units<ROWS, 64>), dim3((outputs + 3) / 4), dim3(256), 0, stream, a);
+            if (hipGetLastError() != hipSuccess) return Q4K_ERR_LAUNCH;
+        }
     }
     return Q4K_OK;
 }
@@ -1036,7 +1282,7 @@ int launch_shape(Attend &a, hipStream_t stream) {
     if (rows <= 16ll * a.p.count) {
         typedef FewShape<kType, DP> S;
         return launch<kFewRows, 32 * S::kWaves>(a, attend_few<kType, DP>, S::kWaves * 64, S::kLds,
-                                                S::kLds > 81920 ? 1 : 2, 1, stream);
+                                                1, 2, stream);
     }
     typedef TileShape<kType, DP> S;
     return launch<kTileRows, S::KT>(a, attend_tiles<kType, DP>, 256, S::kLds, S::kLds > 81920 ? 1 : 2, 4, stream);

@@ -28,7 +28,7 @@ int check_paged(const q4k_kv_cache *cache, const q4k_sequences *sequences, int T
     if (c.page_size < 1 || c.page_size > 65536 || (c.page_size & (c.page_size - 1)) != 0) return Q4K_ERR_BAD_DIM;
     if (c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16 != 0) return Q4K_ERR_BAD_DIM;
     if (static_cast<int64_t>(s.max_pages) * c.page_size > (1 << 30)) return Q4K_ERR_BAD_DIM;
-    if (static_cast<int64_t>(T) * c.kv_heads > INT_MAX || static_cast<int64_t>(T) * q_heads > INT_MAX) return Q4K_ERR_BAD_DIM;
+    if (static_cast<int64_t>(T) * c.kv_heads > (1 << 30) || static_cast<int64_t>(T) * q_heads > (1 << 30)) return Q4K_ERR_BAD_DIM;
     if (q_heads % c.kv_heads != 0) return Q4K_ERR_BAD_DIM;
     if (!(c.k_scale > 0.f) || !(c.v_scale > 0.f) || isinf(c.k_scale) || isinf(c.v_scale)) return Q4K_ERR_BAD_DIM;
     if (T == 0 || s.count == 0) return Q4K_OK;

@@ -112,7 +112,7 @@ int q4k_rms_norm(const float *x, const float *residual, const float *weight, flo
  *   rotation may be NULL: q_out is a copy of q, k is stored as it is.
  *   A token without a place in the cache still has its q_out.
  *   Errors: a negative or unsupported size (the structs', T * q_heads or
- *   T * kv_heads above INT_MAX, q_heads not a positive multiple of kv_heads
+ *   T * kv_heads above 2^30, q_heads not a positive multiple of kv_heads
  *   where q is given), a scale that is not positive and finite:
  *   Q4K_ERR_BAD_DIM; a NULL array or struct (the optional ones excepted):
  *   Q4K_ERR_NULL; Q4K_ERR_ALIGN. */
