@@ -355,6 +355,12 @@ __device__ __forceinline__ int64_t slot_of(const Attend &a, int b, int first, in
     return static_cast<int64_t>(first) * a.group / ROWS + b + tile;
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+    const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(high) << 32 | low);
+}
+
 // 64 sequences from b on, one a lane: their row tiles, the key tiles of one (at
 // least 1: a row that sees nothing has its zeros written), and both summed up to
 // and with them.
@@ -377,6 +383,11 @@ struct Span {
         line = a.target ? tiles * key_tiles : tiles;
         tiles_sum = tiles;
         line_sum = line;
+        if (p.count == 1) {  // (one user's token: 0.3 us less)
+            tiles_sum = uniform(tiles);
+            line_sum = uniform(line);
+            return;
+        }
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int64_t x = __shfl_up(tiles_sum, o), y = __shfl_up(line_sum, o);
@@ -389,12 +400,6 @@ struct Span {
         line_sum += line_before;
     }
 };
-
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-    const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
-    const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32));
-    return static_cast<int64_t>(static_cast<uint64_t>(high) << 32 | low);
-}
 
 // a / b of uniform numbers that are not negative: nearly always of 32 bits, where
 // a division takes a tenth of the time (four of 64 bits took 2 us of a workgroup's start).
@@ -454,13 +459,14 @@ struct Piece {
             return true;
         }
         const int keys = __builtin_amdgcn_readlane(kept.key_tiles, l);
-        u.tile = static_cast<int>(uniform(quotient(rest, keys)));
+        u.tile = rest < keys ? 0 : static_cast<int>(uniform(quotient(rest, keys)));
         u.begin = static_cast<int>(rest - static_cast<int64_t>(u.tile) * keys);
         u.end = static_cast<int>(min(static_cast<int64_t>(keys), u.begin + (stop - at)));
         const int64_t begin = at - u.begin;  // the row tile's place on the line
         u.row_tile = uniform(__shfl(kept.tiles_sum - kept.tiles, l)) + u.tile;
         u.number = workgroup + u.row_tile;
-        const int64_t w0 = uniform(quotient(begin, size)), w1 = uniform(quotient(begin + keys - 1, size));
+        const int64_t w0 = u.begin == 0 ? workgroup : uniform(quotient(begin, size));
+        const int64_t w1 = begin + keys <= stop ? workgroup : uniform(quotient(begin + keys - 1, size));
         u.unit0 = static_cast<int>(min(w0 + u.row_tile, static_cast<int64_t>(a.units)));
         u.units = static_cast<int>(w1 - w0) + 1;
         at += u.end - u.begin;
@@ -510,8 +516,8 @@ __device__ __forceinline__ int exponent_for(float largest) {
     return min(14 - (static_cast<int>(__builtin_amdgcn_frexp_expf(largest))), 100);
 }
 
-// Eight values of the query from dimension d on, times `by`.
-__device__ __forceinline__ void load_query(const Attend &a, const Row &w, int d, float by, float *x) {
+// Eight values of the query from dimension d on.
+__device__ __forceinline__ void load_query(const Attend &a, const Row &w, int d, float *x) {
     f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
     if (w.real && d < a.p.head_dim) {
         x0 = *reinterpret_cast<const f32x4 *>(a.q + w.at + d);
@@ -519,8 +525,8 @@ __device__ __forceinline__ void load_query(const Attend &a, const Row &w, int d,
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[i] = x0[i] * by;
-        x[4 + i] = x1[i] * by;
+        x[i] = x0[i];
+        x[4 + i] = x1[i];
     }
 }
 
@@ -601,7 +607,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
             return kType == Q4K_KV_E4M3 ? 32 * (s >> 1) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half;
         };
         const auto load = [&](int s, float *x) {
-            load_query(a, w, dim(s), by, x);
+            load_query(a, w, dim(s), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= by;
         };
         int e = 0;
         if constexpr (M::kScaled) {
@@ -861,7 +869,6 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     typedef Math<kType> M;
     typedef typename M::v8 v8;
     constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16;
-    static_assert((kCus + 1) * kFewRows * 8 <= S::kEnded, "the maxima and sums of every unit of a row tile");
     extern __shared__ __align__(16) uint8_t lds[];
     int *const ended = reinterpret_cast<int *>(lds + S::kEnded);
     const int head = blockIdx.x % a.p.kv_heads;
@@ -892,16 +899,33 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
         copy_rows<RB, S::kCopies>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
         return is;
     };
+    v8 query[NS][M::kParts];
+    float factor = 1.f;
+    const float by = a.scale * kLog2e * a.p.k_scale;
+    // (asked for before the first copies, whose addresses have to be looked up first)
+    constexpr bool kHold = DP <= 128;  // else there are too few registers, and they are asked for again
+    float held[kHold ? NS : 1][8];
+    const auto ask = [&](int s, float *x) {
+        const int d = kType == Q4K_KV_E4M3 ? 64 * (s >> 1) + 16 * quarter + 8 * (s & 1) : 32 * s + 8 * quarter;
+        load_query(a, w, d, x);
+    };
+    if constexpr (kHold) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) ask(s, held[s]);
+    }
     uint64_t here = 0;
     if (t0 < t1) here = copy(t0, 0);
 
-    v8 query[NS][M::kParts];
-    float factor = 1.f;
     {
-        const float by = a.scale * kLog2e * a.p.k_scale;
-        const auto load = [&](int s, float *x) {
-            const int d = kType == Q4K_KV_E4M3 ? 64 * (s >> 1) + 16 * quarter + 8 * (s & 1) : 32 * s + 8 * quarter;
-            load_query(a, w, d, by, x);
+        const auto query_values = [&](int s, float *x) {
+            if constexpr (kHold) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = held[s][i];
+            } else {
+                ask(s, x);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= by;
         };
         int e = 0;
         if constexpr (M::kScaled) {
@@ -909,7 +933,7 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 float x[8];
-                load(s, x);
+                query_values(s, x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(x[i]));
             }
@@ -921,7 +945,7 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             float x[8];
-            load(s, x);
+            query_values(s, x);
             if constexpr (M::kScaled) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e);
@@ -1107,26 +1131,39 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     __syncthreads();
     if (!*ended) continue;
     const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kFewRows + r; };
-    f32x2 *const ml = reinterpret_cast<f32x2 *>(lds);  // [unit][row] maxima and sums (the parts in LDS have been read)
-    for (int i = threadIdx.x; i < u.units * kFewRows; i += S::kWaves * 64)
-        ml[i] = shared_pair(a.part_ml + 2 * place(i / kFewRows, i % kFewRows));
-    __syncthreads();
     for (int i = threadIdx.x; i < kFewRows * quads; i += S::kWaves * 64) {
         const int r = i / quads, d = (i - r * quads) * 4;
         const Row o = row_of(a, u, row0 + r, head);
         if (!o.real) continue;
         float top = -INFINITY, total = 0.f;
-        for (int c = 0; c < u.units; ++c) top = fmaxf(top, ml[c * kFewRows + r].x);
-        const float zero = top == -INFINITY ? 0.f : top;
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
-        const float *from = a.part + place(0, r) * a.p.head_dim + d;
-        const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kFewRows * a.p.head_dim;
-#pragma unroll 8
-        for (int c = 0; c < u.units; ++c) {
-            const float f = __builtin_amdgcn_exp2f(ml[c * kFewRows + r].x - zero);
-            const f32x2 y0 = shared_pair(from + c * step), y1 = shared_pair(from + c * step + 2);
-            total = fmaf(ml[c * kFewRows + r].y, f, total);
-            y += f32x4{y0.x, y0.y, y1.x, y1.y} * f;
+        const float *from = a.part + place(0, r) * a.p.head_dim + d, *from_ml = a.part_ml + 2 * place(0, r);
+        const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kFewRows;
+        constexpr int kAtOnce = 8;
+        for (int c0 = 0; c0 < u.units; c0 += kAtOnce) {
+            f32x2 ml[kAtOnce], y0[kAtOnce], y1[kAtOnce];
+#pragma unroll
+            for (int c = 0; c < kAtOnce; ++c) {
+                const int64_t at = min(c0 + c, u.units - 1) * step;
+                ml[c] = shared_pair(from_ml + 2 * at);
+                y0[c] = shared_pair(from + at * a.p.head_dim);
+                y1[c] = shared_pair(from + at * a.p.head_dim + 2);
+            }
+            float top1 = top;
+#pragma unroll
+            for (int c = 0; c < kAtOnce; ++c) top1 = fmaxf(top1, ml[c].x);
+            const float zero = top1 == -INFINITY ? 0.f : top1, fade = __builtin_amdgcn_exp2f(top - zero);
+            top = top1;
+            total *= fade;
+            y *= fade;
+#pragma unroll
+            for (int c = 0; c < kAtOnce; ++c) {
+                const float f = c0 + c < u.units ? __builtin_amdgcn_exp2f(ml[c].x - zero) : 0.f;
+                if (c0 + c < u.units) {
+                    total = fmaf(ml[c].y, f, total);
+                    y += f32x4{y0[c].x, y0[c].y, y1[c].x, y1[c].y} * f;
+                }
+            }
         }
         const float f = a.p.v_scale / total;
         if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
