@@ -355,6 +355,13 @@ __device__ __forceinline__ int64_t slot_of(const Attend &a, int b, int first, in
     return static_cast<int64_t>(first) * a.group / ROWS + b + tile;
 }
 
+// The launch behind this one finds the row tile's units there.
+template <int ROWS>
+__device__ __forceinline__ void note_units(const Attend &a, const Unit &u) {
+    const int64_t slot = slot_of<ROWS>(a, u.b, u.first, u.tile);
+    if (slot < a.slots) a.plan[slot] = Part{u.unit0, u.units};
+}
+
 __device__ __forceinline__ int64_t uniform(int64_t x) {
     const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
     const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32));
@@ -495,19 +502,23 @@ __device__ __forceinline__ Row row_of(const Attend &a, const Unit &u, int r, int
 
 // Bit k: the row sees key j0 + k, for 64 keys (before: the index of the first new token).
 __device__ __forceinline__ uint64_t seen(const Attend &a, const Row &w, int before, int j0) {
-    if (!a.mask || !w.real) {
-        const int left = w.stop - j0;
-        return left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
-    }
-    // new tokens of the window: bits from word (j0 - before) / 32 on
-    const int64_t from = static_cast<int64_t>(j0) - before;
+    const int left = w.stop - j0;
+    const uint64_t below = left >= 64 ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1;
+    if (!a.mask) return below;
+    const int64_t from = static_cast<int64_t>(j0) - before;  // the new token of bit 0
     if (from <= -64) return ~0ull;
-    const auto word = [&](int64_t i) { return i >= 0 && i < a.words ? static_cast<uint64_t>(w.mask[i]) : 0ull; };
-    if (from < 0) return (word(0) | word(1) << 32) << -from | ((1ull << -from) - 1);
-    const int64_t i = from >> 5;
+    // bits from word first on, all three words asked for at once
+    const int64_t first = from < 0 ? 0 : from >> 5;
+    uint64_t word[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t x = w.mask[min(first + i, static_cast<int64_t>(a.words - 1))];
+        word[i] = first + i < a.words ? x : 0u;
+    }
+    const uint64_t low = word[0] | word[1] << 32;
     const int s = static_cast<int>(from & 31);
-    const uint64_t low = word(i) | word(i + 1) << 32;
-    return s ? low >> s | word(i + 2) << (64 - s) : low;
+    const uint64_t bits = from < 0 ? low << -from | ((1ull << -from) - 1) : s ? low >> s | word[2] << (64 - s) : low;
+    return w.real ? bits : below;
 }
 
 // The query's power of two: |x| * 2^e of the largest is in [2^13, 2^14).
@@ -577,17 +588,19 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     const int common = a.mask ? before : before + row0 / a.group + 1;
     const int stop = max(min(most, capacity), 0);
     const int t0 = u.begin, t1 = min((stop + KT - 1) / KT, u.end);
-    // the launch behind this one finds the row tile's units here
-    if (a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) {
-        const int64_t slot = slot_of<kTileRows>(a, u.b, u.first, u.tile);
-        if (slot < a.slots) a.plan[slot] = Part{u.unit0, u.units};
-    }
+    if (a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) note_units<kTileRows>(a, u);
     const Row w = row_of(a, u, row0 + wave * 32 + col, head);
     const bool idle = row0 + wave * 32 >= rows;  // no row of this wave is real
 
     Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
     const uint32_t base = lds_address(lds);
     const int piece0 = wave * S::kCopies * 1024;
+    // the wave's queries as the second operand of S^T = K Q^T: lane's row, 8 dimensions a
+    // step; asked for before the first copies, whose addresses have to be looked up first
+    float held[NS][8];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+        load_query(a, w, kType == Q4K_KV_E4M3 ? 32 * (s >> 1) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half, held[s]);
     uint64_t here = 0;
     if (threadIdx.x == 0) *flag = -1;
     if (t0 < t1) {
@@ -597,40 +610,28 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
         copy_rows<RB, S::kCopies>(pages, t0 * KT, whole, piece0, base, base + 2 * S::kBytes);
     }
 
-    // the wave's queries as the second operand of S^T = K Q^T: lane's row, 8 dimensions a step
     v8 qh[NS], ql[NS];
     u32x4 *const third = reinterpret_cast<u32x4 *>(lds + 4 * S::kBytes + S::kMarks + 16) + wave * NS * 64 + lane;  // (of registers there are too few)
     float factor = 1.f;
     {
         const float by = a.scale * kLog2e * a.p.k_scale;
-        const auto dim = [&](int s) {
-            return kType == Q4K_KV_E4M3 ? 32 * (s >> 1) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half;
-        };
-        const auto load = [&](int s, float *x) {
-            load_query(a, w, dim(s), x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= by;
-        };
         int e = 0;
         if constexpr (M::kScaled) {
             float largest = 0.f;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                float x[8];
-                load(s, x);
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(x[i]));
-            }
+                for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(held[s][i] * by));
             e = exponent_for(fmaxf(largest, __shfl_xor(largest, 32)));
             factor = ldexpf(1.f, -e);
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             float x[8];
-            load(s, x);
-            if constexpr (M::kScaled) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e);
+            for (int i = 0; i < 8; ++i) {
+                x[i] = held[s][i] * by;
+                if constexpr (M::kScaled) x[i] = ldexpf(x[i], e);
             }
             v8 parts[M::kParts];
             M::split(x, parts);
@@ -826,18 +827,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
 
 // ---- few rows --------------------------------------------------------------------
 //
-// 16 rows per workgroup; its waves take key tiles of 32 in turn, each with its
-// own two buffers in LDS and its own maximum, sum and output, and nothing to
-// wait for but its own copies; the waves' parts are joined at the end.
-// Products of 16 x 16 x 32.
+// 16, 32 or 64 rows per workgroup, all of them in every wave; the waves take key
+// tiles of 32 in turn, each with its own two buffers in LDS and its own maxima,
+// sums and outputs, and nothing to wait for but its own copies; the waves' parts
+// are joined at the end.  Products of 16 x 16 x 32, blocks of 16 rows: every
+// value that is read from LDS serves all blocks.
 //
-// Units of one row tile are joined by the workgroup of the last one to end,
-// without a second launch (3 to 5 us of 12 over a short context).  Their parts
+// Units of one row tile of 16 are joined by the workgroup of the last one to end,
+// without a second launch (which takes 4 to 5 us; with 64 rows it was this
+// workgroup's work that took long, 20 us of 38 over 16 units).  Their parts
 // go past the L2s, which the card's eight dies do not share: stores and loads of
 // the agent's scope, each wave's stores waited for before the workgroup counts
 // its unit as ended.  They are added in the units' order whichever came last.
-
-constexpr int kFewRows = 16;
 
 // Two numbers to and from memory that all dies see.
 __device__ __forceinline__ void share(float *at, float x, float y) {
@@ -849,45 +850,52 @@ __device__ __forceinline__ f32x2 shared_pair(const float *at) {
     return f32x2{__uint_as_float(static_cast<uint32_t>(pair)), __uint_as_float(static_cast<uint32_t>(pair >> 32))};
 }
 
-template <int kType, int DP>
+template <int kType, int DP, int NB>
 struct FewShape {
+    static constexpr int kRows = 16 * NB;
     static constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2;
     static constexpr int RB = DP * kSize;
-    static constexpr int kWaves = RB == 512 ? 2 : RB == 256 ? 4 : 8;  // 128 KB of LDS
+    // 128 KB of LDS; four waves have the registers of a whole SIMD each
+    static constexpr int kWaves = RB == 512 ? 2 : RB == 256 || NB > 1 ? 4 : 8;
     static constexpr int kBytes = 32 * RB;  // of a tile's K, and of its V
     static constexpr int kCopies = kBytes / 1024;
-    static constexpr int kJoin = kWaves * kFewRows * (DP + 4) * 4;
+    static constexpr int kJoin = kWaves * kRows * (DP + 4) * 4;
     static constexpr int kMarks = 32 * DP / 8;  // a bit per value
     static constexpr int kOwn = 4 * kBytes + kMarks;
     static constexpr int kEnded = kWaves * kOwn > kJoin ? kWaves * kOwn : kJoin;
-    static constexpr int kLds = kEnded + 16;
+    static constexpr bool kLow = NB * DP > 256;  // the queries' second parts in LDS: there are too few registers
+    static constexpr int kLds = kEnded + 16 + (kLow ? kRows * DP * 2 : 0);
+    static constexpr bool kJoined = NB == 1;  // in the same launch
 };
 
-template <int kType, int DP>
-__global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few(const Attend a) {
-    typedef FewShape<kType, DP> S;
+template <int kType, int DP, int NB>
+__global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<kType, DP, NB>::kWaves == 8 ? 2 : 1)) void attend_few(const Attend a) {
+    typedef FewShape<kType, DP, NB> S;
     typedef Math<kType> M;
     typedef typename M::v8 v8;
-    constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16;
+    constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16, kRows = S::kRows;
     extern __shared__ __align__(16) uint8_t lds[];
     int *const ended = reinterpret_cast<int *>(lds + S::kEnded);
     const int head = blockIdx.x % a.p.kv_heads;
-    Piece<kFewRows, KT, true> piece(a, blockIdx.x / a.p.kv_heads);
+    Piece<kRows, KT, true> piece(a, blockIdx.x / a.p.kv_heads);
     for (Unit u; piece.next(u); __syncthreads()) {
     int thread = threadIdx.x;
     asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
     const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 15, quarter = lane >> 4;
     const int before = u.length - u.n;
-    const int row0 = u.tile * kFewRows;
+    const int row0 = u.tile * kRows;
     const int capacity = a.p.max_pages << a.p.shift;
-    const int last = min((row0 + kFewRows - 1) / a.group, u.n - 1);
+    const int last = min((row0 + kRows - 1) / a.group, u.n - 1);
     const int most = a.mask ? u.length : before + last + 1;
     const int common = a.mask ? before : before + row0 / a.group + 1;
     const int stop = max(min(most, capacity), 0);
     // tiles of 32 keys: this wave's are first, first + kWaves, ...
     const int t0 = u.begin * S::kWaves + wave;
     const int t1 = u.end == INT_MAX ? (stop + 31) / 32 : min((stop + 31) / 32, u.end * S::kWaves);
-    const Row w = row_of(a, u, row0 + col, head);
+    if (!S::kJoined && a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) note_units<kRows>(a, u);
+    Row w[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) w[n] = row_of(a, u, row0 + 16 * n + col, head);
 
     Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
     uint8_t *const own = lds + wave * S::kOwn;
@@ -899,58 +907,55 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
         copy_rows<RB, S::kCopies>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
         return is;
     };
-    v8 query[NS][M::kParts];
-    float factor = 1.f;
+    static_assert(!S::kLow || M::kParts == 2, "one part in LDS");
+    v8 query[NB][NS][S::kLow ? 1 : M::kParts];
+    u32x4 *const low = reinterpret_cast<u32x4 *>(lds + S::kEnded + 16) + lane;  // (every wave writes the same)
+    float factor[NB];
     const float by = a.scale * kLog2e * a.p.k_scale;
     // (asked for before the first copies, whose addresses have to be looked up first)
-    constexpr bool kHold = DP <= 128;  // else there are too few registers, and they are asked for again
-    float held[kHold ? NS : 1][8];
-    const auto ask = [&](int s, float *x) {
-        const int d = kType == Q4K_KV_E4M3 ? 64 * (s >> 1) + 16 * quarter + 8 * (s & 1) : 32 * s + 8 * quarter;
-        load_query(a, w, d, x);
-    };
-    if constexpr (kHold) {
+    float held[NB][NS][8];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) ask(s, held[s]);
-    }
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const int d = kType == Q4K_KV_E4M3 ? 64 * (s >> 1) + 16 * quarter + 8 * (s & 1) : 32 * s + 8 * quarter;
+            load_query(a, w[n], d, held[n][s]);
+        }
     uint64_t here = 0;
     if (t0 < t1) here = copy(t0, 0);
 
-    {
-        const auto query_values = [&](int s, float *x) {
-            if constexpr (kHold) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = held[s][i];
-            } else {
-                ask(s, x);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= by;
-        };
+    for (int n = 0; n < NB; ++n) {
         int e = 0;
+        factor[n] = 1.f;
         if constexpr (M::kScaled) {
             float largest = 0.f;
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                float x[8];
-                query_values(s, x);
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(x[i]));
-            }
+                for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(held[n][s][i] * by));
             largest = fmaxf(largest, __shfl_xor(largest, 16));
             largest = fmaxf(largest, __shfl_xor(largest, 32));
             e = exponent_for(largest);
-            factor = ldexpf(1.f, -e);
+            factor[n] = ldexpf(1.f, -e);
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             float x[8];
-            query_values(s, x);
-            if constexpr (M::kScaled) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = ldexpf(x[i], e);
+            for (int i = 0; i < 8; ++i) {
+                x[i] = held[n][s][i] * by;
+                if constexpr (M::kScaled) x[i] = ldexpf(x[i], e);
             }
-            M::split(x, query[s]);
+            v8 split[M::kParts];
+            M::split(x, split);
+            query[n][s][0] = split[0];
+            if constexpr (S::kLow) {
+                low[(n * NS + s) * 64] = __builtin_bit_cast(u32x4, split[1]);
+            } else {
+#pragma unroll
+                for (int i = 1; i < M::kParts; ++i) query[n][s][i] = split[i];
+            }
         }
     }
 
@@ -966,10 +971,15 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     }
     const int v_at = v_row * RB + 8 * (col & 1), v_x = v_c ^ swizzle_v<RB>(v_row);
 
-    f32x4 acc[ND];
+    f32x4 acc[NB][ND];
+    float m[NB], sum[NB];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) acc[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, sum = 0.f;
+    for (int n = 0; n < NB; ++n) {
+        m[n] = -INFINITY;
+        sum[n] = 0.f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     int buf = 0;
     for (int t = t0; t < t1; t += S::kWaves, buf ^= 1) {
         const uint64_t now = here;
@@ -982,60 +992,79 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
         const uint8_t *kt = own + buf * 2 * S::kBytes;
         uint8_t *vt = own + (buf * 2 + 1) * S::kBytes, *marks = own + 4 * S::kBytes;
         const bool apart = t * 32 + 32 > common && set_apart<kType, RB, S::kBytes>(vt, 0, marks);
-        const uint32_t vis = static_cast<uint32_t>(seen(a, w, before, t * 32) & now);
-        if (__ballot(vis != 0) == 0) continue;
-        f32x4 s[2];
+        uint32_t vis[NB], any = 0;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            vis[n] = static_cast<uint32_t>(seen(a, w[n], before, t * 32) & now);
+            any |= vis[n];
+        }
+        if (__ballot(any != 0) == 0) continue;
+        const auto part_of = [&](int n, int s, int i) {
+            if constexpr (S::kLow)
+                if (i == 1) return __builtin_bit_cast(v8, low[(n * NS + s) * 64]);
+            return query[n][s][S::kLow ? 0 : i];
+        };
+        f32x4 s[NB][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            s[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < NB; ++n) s[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < RB / 64; ++c) {
                 const u32x4 x = *reinterpret_cast<const u32x4 *>(kt + k * 16 * RB + k_at + (((4 * c) ^ k_x) << 4));
                 if constexpr (kType == Q4K_KV_E4M3) {
                     const half8v x0 = widened(x.x, x.y), x1 = widened(x.z, x.w);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        s[k] = M::mfma16(x0, query[2 * c][i], s[k]);
-                        s[k] = M::mfma16(x1, query[2 * c + 1][i], s[k]);
-                    }
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            s[n][k] = M::mfma16(x0, part_of(n, 2 * c, i), s[n][k]);
+                            s[n][k] = M::mfma16(x1, part_of(n, 2 * c + 1, i), s[n][k]);
+                        }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < M::kParts; ++i) s[k] = M::mfma16(__builtin_bit_cast(v8, x), query[c][i], s[k]);
+                    for (int i = 0; i < M::kParts; ++i)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            s[n][k] = M::mfma16(__builtin_bit_cast(v8, x), part_of(n, c, i), s[n][k]);
                 }
             }
         }
-        const uint32_t mine = vis >> (4 * quarter);
-        if (__ballot(vis != 0xFFFFFFFFu) != 0) {
+        v8 parts[NB][M::kParts];
+        float fade[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const uint32_t mine = vis[n] >> (4 * quarter);
+            if (__ballot(vis[n] != 0xFFFFFFFFu) != 0) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!((mine >> (16 * k + r)) & 1)) s[n][k][r] = -INFINITY;
+            }
+            float top = s[n][0][0];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (!((mine >> (16 * k + r)) & 1)) s[k][r] = -INFINITY;
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[n][k][r]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m1 = fmaxf(m[n], top * factor[n]);
+            const float zero = m1 == -INFINITY ? 0.f : m1;
+            fade[n] = __builtin_amdgcn_exp2f(m[n] - zero);
+            m[n] = m1;
+            const float shift = kBias - zero;
+            float x[8], part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = __builtin_amdgcn_exp2f(fmaf(s[n][i >> 2][i & 3], factor[n], shift));
+                part += x[i];
+            }
+            sum[n] = fmaf(sum[n], fade[n], part);
+            M::split(x, parts[n]);
         }
-        float top = s[0][0];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) top = fmaxf(top, s[k][r]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m1 = fmaxf(m, top * factor);
-        const float zero = m1 == -INFINITY ? 0.f : m1;
-        const float fade = __builtin_amdgcn_exp2f(m - zero);
-        m = m1;
-        const float shift = kBias - zero;
-        float x[8], part = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(fmaf(s[i >> 2][i & 3], factor, shift));
-            part += x[i];
-        }
-        sum = fmaf(sum, fade, part);
-        v8 parts[M::kParts];
-        M::split(x, parts);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            acc[d] *= fade;
             v8 y;
             if constexpr (kType == Q4K_KV_E4M3) {
                 const i32x2 z = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
@@ -1049,58 +1078,71 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
                 y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
             }
 #pragma unroll
-            for (int i = 0; i < M::kParts; ++i) acc[d] = M::mfma16(y, parts[i], acc[d]);
+            for (int n = 0; n < NB; ++n) acc[n][d] *= fade[n];
+#pragma unroll
+            for (int i = 0; i < M::kParts; ++i)
+#pragma unroll
+                for (int n = 0; n < NB; ++n) acc[n][d] = M::mfma16(y, parts[n][i], acc[n][d]);
         }
         if (apart) {
 #pragma unroll 1
             for (int i = 0; i < 32 * DP / 8; ++i) {
-                uint32_t bits = marks[i];
-                if (!((vis >> (i / (DP / 8))) & 1)) bits = 0;
+                const uint32_t marked = marks[i];
+                if (marked == 0) continue;
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
+                for (int n = 0; n < NB; ++n) {
+                    const uint32_t bits = (vis[n] >> (i / (DP / 8))) & 1 ? marked : 0;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int at = 16 * d + 4 * quarter + r - i % (DP / 8) * 8;
-                        if (static_cast<unsigned>(at) < 8u && ((bits >> at) & 1)) acc[d][r] = nan_value();
-                    }
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int at = 16 * d + 4 * quarter + r - i % (DP / 8) * 8;
+                            if (static_cast<unsigned>(at) < 8u && ((bits >> at) & 1)) acc[n][d][r] = nan_value();
+                        }
+                }
             }
         }
     }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        sum[n] += __shfl_xor(sum[n], 16);
+        sum[n] += __shfl_xor(sum[n], 32);
+    }
 
     // the waves' parts: [wave][row][DP] and [wave][row] maxima and sums (row stride DP + 4 words)
     wait_copies<0>();
     barrier();
     float *const po = reinterpret_cast<float *>(lds);
     constexpr int kStride = DP + 4;
-    {
-        float *mine = po + (wave * kFewRows + col) * kStride;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(mine + 16 * d + 4 * quarter) = acc[d];
+    for (int n = 0; n < NB; ++n) {
+        float *mine = po + (wave * kRows + 16 * n + col) * kStride;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(mine + 16 * d + 4 * quarter) = acc[n][d];
         if (quarter == 0) {
-            mine[DP] = m;
-            mine[DP + 1] = sum;
+            mine[DP] = m[n];
+            mine[DP + 1] = sum[n];
         }
     }
     __syncthreads();
     const int quads = a.p.head_dim / 4;
     // (offsets out of order can give more units or row tiles than there is room for)
     const int64_t counter = u.row_tile * a.p.kv_heads + head;
-    const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && counter < kCounters;
-    for (int i = threadIdx.x; i < kFewRows * quads; i += S::kWaves * 64) {
-        const int r = i / quads, d = (i - r * quads) * 4;
+    const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && (!S::kJoined || counter < kCounters);
+    const int at_once = S::kWaves * 64 / quads;  // rows
+    const int real = min(u.n * a.group - row0, kRows), d = (thread % quads) * 4;
+    for (int r = thread / quads; r < real; r += at_once) {
+        if (thread >= at_once * quads) break;
         const Row o = row_of(a, u, row0 + r, head);
-        if (!o.real) continue;
         float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < S::kWaves; ++k) top = fmaxf(top, po[(k * kFewRows + r) * kStride + DP]);
+        for (int k = 0; k < S::kWaves; ++k) top = fmaxf(top, po[(k * kRows + r) * kStride + DP]);
         const float zero = top == -INFINITY ? 0.f : top;
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
         float total = 0.f;
 #pragma unroll
         for (int k = 0; k < S::kWaves; ++k) {
-            const float *from = po + (k * kFewRows + r) * kStride;
+            const float *from = po + (k * kRows + r) * kStride;
             // a wave without keys has nothing to add (its maximum is -inf)
             const float f = __builtin_amdgcn_exp2f(from[DP] - zero);
             total = fmaf(from[DP + 1], f, total);
@@ -1112,13 +1154,18 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
             else y *= f;
             *reinterpret_cast<f32x4 *>(a.out + o.at + d) = y;
         } else if (shared) {
-            const int64_t at = (u.number * a.p.kv_heads + head) * kFewRows + r;
-            share(a.part + at * a.p.head_dim + d, y.x, y.y);
-            share(a.part + at * a.p.head_dim + d + 2, y.z, y.w);
-            if (d == 0) share(a.part_ml + 2 * at, top, total);
+            const int64_t at = (u.number * a.p.kv_heads + head) * kRows + r;
+            if constexpr (S::kJoined) {
+                share(a.part + at * a.p.head_dim + d, y.x, y.y);
+                share(a.part + at * a.p.head_dim + d + 2, y.z, y.w);
+                if (d == 0) share(a.part_ml + 2 * at, top, total);
+            } else {
+                *reinterpret_cast<f32x4 *>(a.part + at * a.p.head_dim + d) = y;
+                if (d == 0) *reinterpret_cast<f32x2 *>(a.part_ml + 2 * at) = f32x2{top, total};
+            }
         }
     }
-    if (!shared) continue;
+    if (!S::kJoined || !shared) continue;
     // the row tile's last unit to end joins them all
     wait_copies<0>();  // what this wave has shared is there for the others
     __syncthreads();
@@ -1130,15 +1177,14 @@ __global__ __launch_bounds__((FewShape<kType, DP>::kWaves * 64)) void attend_few
     }
     __syncthreads();
     if (!*ended) continue;
-    const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kFewRows + r; };
-    for (int i = threadIdx.x; i < kFewRows * quads; i += S::kWaves * 64) {
-        const int r = i / quads, d = (i - r * quads) * 4;
+    const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kRows + r; };
+    for (int r = thread / quads; r < real; r += at_once) {
+        if (thread >= at_once * quads) break;
         const Row o = row_of(a, u, row0 + r, head);
-        if (!o.real) continue;
         float top = -INFINITY, total = 0.f;
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
         const float *from = a.part + place(0, r) * a.p.head_dim + d, *from_ml = a.part_ml + 2 * place(0, r);
-        const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kFewRows;
+        const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kRows;
         constexpr int kAtOnce = 8;
         for (int c0 = 0; c0 < u.units; c0 += kAtOnce) {
             f32x2 ml[kAtOnce], y0[kAtOnce], y1[kAtOnce];
@@ -1274,7 +1320,7 @@ int64_t tiles_at_most(const Attend &a, int rows) {
     return (static_cast<int64_t>(a.p.tokens) * a.group + static_cast<int64_t>(min(a.p.count, a.p.tokens)) * (rows - 1)) / rows;
 }
 
-template <int ROWS, int KT, class Kernel>
+template <int ROWS, int KT, bool kJoined, class Kernel>
 int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least, hipStream_t stream) {
     const int64_t tiles = tiles_at_most(a, ROWS), heads = a.p.kv_heads;
     int64_t target = (static_cast<int64_t>(kCus) * per_cu + heads - 1) / heads;
@@ -1294,12 +1340,12 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
         a.part = ws;
         a.part_ml = ws + rows * a.p.head_dim;
         a.plan = reinterpret_cast<Part *>(a.part_ml + 2 * rows);
-        if (ROWS == kFewRows && counters(stream, &a.counters) != hipSuccess) return Q4K_ERR_ALLOC;
+        if (kJoined && counters(stream, &a.counters) != hipSuccess) return Q4K_ERR_ALLOC;
     }
     if (lds > 65536 && allow_dynamic_lds(reinterpret_cast<const void *>(kernel), lds) != hipSuccess) return Q4K_ERR_LAUNCH;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((target ? target : tiles) * heads)), dim3(threads), lds, stream, a);
     if (hipGetLastError() != hipSuccess) return Q4K_ERR_LAUNCH;
-    if constexpr (ROWS != kFewRows) {
+    if constexpr (!kJoined) {
         if (target) {
             const int outputs = a.p.tokens * a.q_heads;
             if (outputs <= 2048)
@@ -1312,17 +1358,24 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
     return Q4K_OK;
 }
 
+template <int kType, int DP, int NB>
+int launch_few(Attend &a, hipStream_t stream) {
+    typedef FewShape<kType, DP, NB> S;
+    return launch<S::kRows, 32 * S::kWaves, S::kJoined>(a, attend_few<kType, DP, NB>, S::kWaves * 64, S::kLds, 1, 2, stream);
+}
+
 template <int kType, int DP>
 int launch_shape(Attend &a, hipStream_t stream) {
-    // Rows of a sequence on average: the smaller tiles where they would be the emptier ones.
-    const int64_t rows = static_cast<int64_t>(a.p.tokens) * a.group;
-    if (rows <= 16ll * a.p.count) {
-        typedef FewShape<kType, DP> S;
-        return launch<kFewRows, 32 * S::kWaves>(a, attend_few<kType, DP>, S::kWaves * 64, S::kLds,
-                                                1, 2, stream);
-    }
+    // Rows of a sequence on average: the smallest tiles that hold them (as far as the registers go).
+    constexpr bool kBf16 = kType == Q4K_KV_BF16;
+    const int64_t rows = (static_cast<int64_t>(a.p.tokens) * a.group + a.p.count - 1) / a.p.count;
+    if (rows <= 16) return launch_few<kType, DP, 1>(a, stream);
+    if constexpr (DP <= (kBf16 ? 128 : 256))
+        if (rows <= 32) return launch_few<kType, DP, 2>(a, stream);
+    if constexpr (DP <= (kBf16 ? 64 : 128))
+        if (rows <= 64) return launch_few<kType, DP, 4>(a, stream);
     typedef TileShape<kType, DP> S;
-    return launch<kTileRows, S::KT>(a, attend_tiles<kType, DP>, 256, S::kLds, S::kLds > 81920 ? 1 : 2, 4, stream);
+    return launch<kTileRows, S::KT, false>(a, attend_tiles<kType, DP>, 256, S::kLds, S::kLds > 81920 ? 1 : 2, 4, stream);
 }
 
 template <int kType>
