@@ -248,7 +248,7 @@ struct Pages {
 };
 
 // Copies COPIES KB of a tile's keys and of its values, from byte `at` of the tile on.
-template <int RB, int COPIES>
+template <int RB, int COPIES, int UNROLL>
 __device__ __forceinline__ void copy_rows(const Pages &g, int j0, bool whole, int at, uint32_t k_lds, uint32_t v_lds) {
     constexpr int kPieces = RB / 16, kRows = 1024 / RB;
     const int lane = threadIdx.x & 63;
@@ -271,7 +271,7 @@ __device__ __forceinline__ void copy_rows(const Pages &g, int j0, bool whole, in
         }
         return;
     }
-#pragma unroll 4
+#pragma unroll UNROLL
     for (int i = 0; i < COPIES; ++i) {
         const int row = (at + i * 1024) / RB + lane / kPieces, piece = lane % kPieces;
         const int j = j0 + row, page = g.page_of(j);
@@ -300,7 +300,7 @@ template <int kType, int RB, int BYTES>
 __device__ __forceinline__ bool set_apart(uint8_t *v, int at, uint8_t *marks) {
     constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2, kPieces = RB / 16;
     uint32_t any = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = at + (threadIdx.x & 63) * 16; i < at + BYTES; i += 1024) {
         u32x4 w = *reinterpret_cast<const u32x4 *>(v + i);
         const int row = i / RB, piece = i / 16 % kPieces ^ swizzle_v<RB>(row);
@@ -408,11 +408,18 @@ struct Span {
     }
 };
 
-// a / b of uniform numbers that are not negative: nearly always of 32 bits, where
-// a division takes a tenth of the time (four of 64 bits took 2 us of a workgroup's start).
+// a / b of uniform numbers, a not negative, b positive, by way of a double (the
+// compiler's four divisions of 64 bits took 2 us of a workgroup's start).  The
+// double is off by one where the quotient is below 2^52, and the remainder says so.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
+    int64_t q = static_cast<int64_t>(static_cast<double>(a) * __builtin_amdgcn_rcp(static_cast<double>(b)));
+    int64_t rest = a - q * b;
+    while (rest < 0 || rest >= b) {
+        const int64_t more = static_cast<int64_t>(floor(static_cast<double>(rest) / static_cast<double>(b)));
+        q += more;
+        rest -= more * b;
+    }
+    return q;
 }
 
 // A workgroup's piece of the line.  kKeep: the 64 sequences last looked through stay
@@ -607,7 +614,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
         pages.look_up(t0 * KT, KT);
         const bool whole = pages.whole(t0 * KT, KT);
         here = there(pages, t0 * KT, whole, KT);
-        copy_rows<RB, S::kCopies>(pages, t0 * KT, whole, piece0, base, base + 2 * S::kBytes);
+        copy_rows<RB, S::kCopies, 4>(pages, t0 * KT, whole, piece0, base, base + 2 * S::kBytes);
     }
 
     v8 qh[NS], ql[NS];
@@ -672,7 +679,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
             pages.look_up((t + 1) * KT, KT);
             const bool whole = pages.whole((t + 1) * KT, KT);
             here = there(pages, (t + 1) * KT, whole, KT);
-            copy_rows<RB, S::kCopies>(pages, (t + 1) * KT, whole, piece0, base + (buf ^ 1) * S::kBytes,
+            copy_rows<RB, S::kCopies, 4>(pages, (t + 1) * KT, whole, piece0, base + (buf ^ 1) * S::kBytes,
                                       base + (2 + (buf ^ 1)) * S::kBytes);
         }
         const uint8_t *kt = lds + buf * S::kBytes;
@@ -850,13 +857,13 @@ __device__ __forceinline__ f32x2 shared_pair(const float *at) {
     return f32x2{__uint_as_float(static_cast<uint32_t>(pair)), __uint_as_float(static_cast<uint32_t>(pair >> 32))};
 }
 
-template <int kType, int DP, int NB>
+template <int kType, int DP, int NB, bool kShort>
 struct FewShape {
     static constexpr int kRows = 16 * NB;
     static constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2;
     static constexpr int RB = DP * kSize;
-    // 128 KB of LDS; four waves have the registers of a whole SIMD each
-    static constexpr int kWaves = RB == 512 ? 2 : RB == 256 || NB > 1 ? 4 : 8;
+    // Four waves, or as many as have room in LDS; two workgroups on a CU where that is 64 KB.
+    static constexpr int kWaves = RB == 512 || kShort ? 2 : 4;
     static constexpr int kBytes = 32 * RB;  // of a tile's K, and of its V
     static constexpr int kCopies = kBytes / 1024;
     static constexpr int kJoin = kWaves * kRows * (DP + 4) * 4;
@@ -866,11 +873,13 @@ struct FewShape {
     static constexpr bool kLow = NB * DP > 256;  // the queries' second parts in LDS: there are too few registers
     static constexpr int kLds = kEnded + 16 + (kLow ? kRows * DP * 2 : 0);
     static constexpr bool kJoined = NB == 1;  // in the same launch
+    static constexpr int kPerCu = NB < 4 && kLds <= 81920 ? 2 : 1;
+    static constexpr int kPerSimd = kPerCu * kWaves > 4 ? 2 : 1;  // waves
 };
 
-template <int kType, int DP, int NB>
-__global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<kType, DP, NB>::kWaves == 8 ? 2 : 1)) void attend_few(const Attend a) {
-    typedef FewShape<kType, DP, NB> S;
+template <int kType, int DP, int NB, bool kShort>
+__global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (FewShape<kType, DP, NB, kShort>::kPerSimd)) void attend_few(const Attend a) {
+    typedef FewShape<kType, DP, NB, kShort> S;
     typedef Math<kType> M;
     typedef typename M::v8 v8;
     constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16, kRows = S::kRows;
@@ -900,11 +909,11 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
     Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
     uint8_t *const own = lds + wave * S::kOwn;
     const uint32_t base = lds_address(own);
-    const auto copy = [&](int t, int buf) {
+    const auto copy = [&](int t, int buf) __attribute__((always_inline)) {
         pages.look_up(t * 32, 32);
         const bool whole = pages.whole(t * 32, 32);
         const uint64_t is = there(pages, t * 32, whole, 32);
-        copy_rows<RB, S::kCopies>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
+        copy_rows<RB, S::kCopies, NB == 1 ? 4 : 1>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
         return is;
     };
     static_assert(!S::kLow || M::kParts == 2, "one part in LDS");
@@ -1109,7 +1118,7 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
         sum[n] += __shfl_xor(sum[n], 32);
     }
 
-    // the waves' parts: [wave][row][DP] and [wave][row] maxima and sums (row stride DP + 4 words)
+    // the waves' parts: [wave][row][DP] and behind them maximum, sum and the row's place (stride DP + 4 words)
     wait_copies<0>();
     barrier();
     float *const po = reinterpret_cast<float *>(lds);
@@ -1122,6 +1131,7 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
         if (quarter == 0) {
             mine[DP] = m[n];
             mine[DP + 1] = sum[n];
+            *reinterpret_cast<int64_t *>(mine + DP + 2) = w[n].at;
         }
     }
     __syncthreads();
@@ -1130,10 +1140,10 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
     const int64_t counter = u.row_tile * a.p.kv_heads + head;
     const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && (!S::kJoined || counter < kCounters);
     const int at_once = S::kWaves * 64 / quads;  // rows
+    const auto at_of = [&](int r) { return *reinterpret_cast<const int64_t *>(po + r * kStride + DP + 2); };
     const int real = min(u.n * a.group - row0, kRows), d = (thread % quads) * 4;
     for (int r = thread / quads; r < real; r += at_once) {
         if (thread >= at_once * quads) break;
-        const Row o = row_of(a, u, row0 + r, head);
         float top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < S::kWaves; ++k) top = fmaxf(top, po[(k * kRows + r) * kStride + DP]);
@@ -1152,7 +1162,7 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
             const float f = a.p.v_scale / total;
             if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
             else y *= f;
-            *reinterpret_cast<f32x4 *>(a.out + o.at + d) = y;
+            *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
         } else if (shared) {
             const int64_t at = (u.number * a.p.kv_heads + head) * kRows + r;
             if constexpr (S::kJoined) {
@@ -1180,12 +1190,11 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
     const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kRows + r; };
     for (int r = thread / quads; r < real; r += at_once) {
         if (thread >= at_once * quads) break;
-        const Row o = row_of(a, u, row0 + r, head);
         float top = -INFINITY, total = 0.f;
         f32x4 y = {0.f, 0.f, 0.f, 0.f};
         const float *from = a.part + place(0, r) * a.p.head_dim + d, *from_ml = a.part_ml + 2 * place(0, r);
         const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kRows;
-        constexpr int kAtOnce = 8;
+        constexpr int kAtOnce = 8;  // all asked for together (behind the last unit: that one again)
         for (int c0 = 0; c0 < u.units; c0 += kAtOnce) {
             f32x2 ml[kAtOnce], y0[kAtOnce], y1[kAtOnce];
 #pragma unroll
@@ -1214,7 +1223,7 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB>::kWaves * 64), (FewShape<k
         const float f = a.p.v_scale / total;
         if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
         else y *= f;
-        *reinterpret_cast<f32x4 *>(a.out + o.at + d) = y;
+        *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
     }
     }
 }
@@ -1358,10 +1367,11 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
     return Q4K_OK;
 }
 
-template <int kType, int DP, int NB>
+template <int kType, int DP, int NB, bool kShort = false>
 int launch_few(Attend &a, hipStream_t stream) {
-    typedef FewShape<kType, DP, NB> S;
-    return launch<S::kRows, 32 * S::kWaves, S::kJoined>(a, attend_few<kType, DP, NB>, S::kWaves * 64, S::kLds, 1, 2, stream);
+    typedef FewShape<kType, DP, NB, kShort> S;
+    return launch<S::kRows, 32 * S::kWaves, S::kJoined>(a, attend_few<kType, DP, NB, kShort>, S::kWaves * 64, S::kLds,
+                                                        S::kPerCu, 2, stream);
 }
 
 template <int kType, int DP>
@@ -1369,7 +1379,15 @@ int launch_shape(Attend &a, hipStream_t stream) {
     // Rows of a sequence on average: the smallest tiles that hold them (as far as the registers go).
     constexpr bool kBf16 = kType == Q4K_KV_BF16;
     const int64_t rows = (static_cast<int64_t>(a.p.tokens) * a.group + a.p.count - 1) / a.p.count;
-    if (rows <= 16) return launch_few<kType, DP, 1>(a, stream);
+    if (rows <= 16) {
+        // 128 KB of LDS are one workgroup of four waves on a CU, or two of two: with several
+        // row tiles to a workgroup one's start hides behind the other's copies (48 sequences
+        // of 4096 keys on average, 128 x 16 bits: 105 -> 87 us), with a few long ones there would
+        // be twice the parts to join (one of 131072 keys: 102 -> 119 us).
+        if constexpr (FewShape<kType, DP, 1, false>::RB == 256)
+            if (2 * tiles_at_most(a, 16) * a.p.kv_heads > kCus) return launch_few<kType, DP, 1, true>(a, stream);
+        return launch_few<kType, DP, 1>(a, stream);
+    }
     if constexpr (DP <= (kBf16 ? 128 : 256))
         if (rows <= 32) return launch_few<kType, DP, 2>(a, stream);
     if constexpr (DP <= (kBf16 ? 64 : 128))
