@@ -583,252 +583,253 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     const int64_t w0 = blockIdx.x / a.p.kv_heads;
     Piece<kTileRows, KT, false> piece(a, a.target ? w0 : a.units - 1 - w0);
     for (Unit u; piece.next(u); __syncthreads()) {
-    int thread = threadIdx.x;
-    asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
-    const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 31, half = lane >> 5;
-    const int before = u.length - u.n;
-    const int row0 = u.tile * kTileRows, rows = u.n * a.group;
-    const int capacity = a.p.max_pages << a.p.shift;
-    // keys that some row of the tile may see, and those that every one sees
-    const int last = min((row0 + kTileRows - 1) / a.group, u.n - 1);
-    const int most = a.mask ? u.length : before + last + 1;
-    const int common = a.mask ? before : before + row0 / a.group + 1;
-    const int stop = max(min(most, capacity), 0);
-    const int t0 = u.begin, t1 = min((stop + KT - 1) / KT, u.end);
-    if (a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) note_units<kTileRows>(a, u);
-    const Row w = row_of(a, u, row0 + wave * 32 + col, head);
-    const bool idle = row0 + wave * 32 >= rows;  // no row of this wave is real
+        int thread = threadIdx.x;
+        asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
+        const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 31, half = lane >> 5;
+        const int before = u.length - u.n;
+        const int row0 = u.tile * kTileRows, rows = u.n * a.group;
+        const int capacity = a.p.max_pages << a.p.shift;
+        // keys that some row of the tile may see, and those that every one sees
+        const int last = min((row0 + kTileRows - 1) / a.group, u.n - 1);
+        const int most = a.mask ? u.length : before + last + 1;
+        const int common = a.mask ? before : before + row0 / a.group + 1;
+        const int stop = max(min(most, capacity), 0);
+        const int t0 = u.begin, t1 = min((stop + KT - 1) / KT, u.end);
+        if (a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) note_units<kTileRows>(a, u);
+        const Row w = row_of(a, u, row0 + wave * 32 + col, head);
+        const bool idle = row0 + wave * 32 >= rows;  // no row of this wave is real
 
-    Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
-    const uint32_t base = lds_address(lds);
-    const int piece0 = wave * S::kCopies * 1024;
-    // the wave's queries as the second operand of S^T = K Q^T: lane's row, 8 dimensions a
-    // step; asked for before the first copies, whose addresses have to be looked up first
-    float held[NS][8];
+        Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
+        const uint32_t base = lds_address(lds);
+        const int piece0 = wave * S::kCopies * 1024;
+        // the wave's queries as the second operand of S^T = K Q^T: lane's row, 8 dimensions a
+        // step; asked for before the first copies, whose addresses have to be looked up first
+        float held[NS][8];
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
-        load_query(a, w, kType == Q4K_KV_E4M3 ? 32 * (s >> 1) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half, held[s]);
-    uint64_t here = 0;
-    if (threadIdx.x == 0) *flag = -1;
-    if (t0 < t1) {
-        pages.look_up(t0 * KT, KT);
-        const bool whole = pages.whole(t0 * KT, KT);
-        here = there(pages, t0 * KT, whole, KT);
-        copy_rows<RB, S::kCopies, 4>(pages, t0 * KT, whole, piece0, base, base + 2 * S::kBytes);
-    }
-
-    v8 qh[NS], ql[NS];
-    u32x4 *const third = reinterpret_cast<u32x4 *>(lds + 4 * S::kBytes + S::kMarks + 16) + wave * NS * 64 + lane;  // (of registers there are too few)
-    float factor = 1.f;
-    {
-        const float by = a.scale * kLog2e * a.p.k_scale;
-        int e = 0;
-        if constexpr (M::kScaled) {
-            float largest = 0.f;
-#pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(held[s][i] * by));
-            e = exponent_for(fmaxf(largest, __shfl_xor(largest, 32)));
-            factor = ldexpf(1.f, -e);
+        for (int s = 0; s < NS; ++s)
+            load_query(a, w, kType == Q4K_KV_E4M3 ? 32 * (s >> 1) + 16 * half + 8 * (s & 1) : 16 * s + 8 * half, held[s]);
+        uint64_t here = 0;
+        if (threadIdx.x == 0) *flag = -1;
+        if (t0 < t1) {
+            pages.look_up(t0 * KT, KT);
+            const bool whole = pages.whole(t0 * KT, KT);
+            here = there(pages, t0 * KT, whole, KT);
+            copy_rows<RB, S::kCopies, 4>(pages, t0 * KT, whole, piece0, base, base + 2 * S::kBytes);
         }
+
+        v8 qh[NS], ql[NS];
+        // (for the third parts there are too few registers)
+        u32x4 *const third = reinterpret_cast<u32x4 *>(lds + 4 * S::kBytes + S::kMarks + 16) + wave * NS * 64 + lane;
+        float factor = 1.f;
+        {
+            const float by = a.scale * kLog2e * a.p.k_scale;
+            int e = 0;
+            if constexpr (M::kScaled) {
+                float largest = 0.f;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            float x[8];
+                for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = held[s][i] * by;
-                if constexpr (M::kScaled) x[i] = ldexpf(x[i], e);
+                    for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(held[s][i] * by));
+                e = exponent_for(fmaxf(largest, __shfl_xor(largest, 32)));
+                factor = ldexpf(1.f, -e);
             }
-            v8 parts[M::kParts];
-            M::split(x, parts);
-            qh[s] = parts[0];
-            ql[s] = parts[1];
-            if constexpr (M::kParts == 3) third[s * 64] = __builtin_bit_cast(u32x4, parts[2]);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = held[s][i] * by;
+                    if constexpr (M::kScaled) x[i] = ldexpf(x[i], e);
+                }
+                v8 parts[M::kParts];
+                M::split(x, parts);
+                qh[s] = parts[0];
+                ql[s] = parts[1];
+                if constexpr (M::kParts == 3) third[s * 64] = __builtin_bit_cast(u32x4, parts[2]);
+            }
         }
-    }
 
-    // where this lane reads: K by pieces of its row, V by halves of pieces, four keys (e4m3: eight) at a time
-    const int k_at = col * RB, k_x = half ^ swizzle_k<RB>(col);
-    const int li = lane & 15, dh = (lane >> 4) & 1;
-    int v_row, v_c;
-    if constexpr (kType == Q4K_KV_E4M3) {
-        const int r = li >> 1;
-        v_row = (r < 4 ? 0 : 4) + 4 * half + r;
-        v_c = dh;
-    } else {
-        v_row = 4 * half + (li >> 2);
-        v_c = 2 * dh + ((li & 3) >> 1);
-    }
-    constexpr int kEight = 1;  // swizzle_v(row + 8) ^ swizzle_v(row), row below 8
-    const int v_at = v_row * RB + 8 * (li & 1), v_x = v_c ^ swizzle_v<RB>(v_row);
-
-    f32x16 acc[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
-    float m = -INFINITY, sum = 0.f;
-
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
-        wait_copies<0>();
-        barrier();
-        const uint64_t now = here;
-        if (t + 1 < t1) {
-            pages.look_up((t + 1) * KT, KT);
-            const bool whole = pages.whole((t + 1) * KT, KT);
-            here = there(pages, (t + 1) * KT, whole, KT);
-            copy_rows<RB, S::kCopies, 4>(pages, (t + 1) * KT, whole, piece0, base + (buf ^ 1) * S::kBytes,
-                                      base + (2 + (buf ^ 1)) * S::kBytes);
+        // where this lane reads: K by pieces of its row, V by halves of pieces, four keys (e4m3: eight) at a time
+        const int k_at = col * RB, k_x = half ^ swizzle_k<RB>(col);
+        const int li = lane & 15, dh = (lane >> 4) & 1;
+        int v_row, v_c;
+        if constexpr (kType == Q4K_KV_E4M3) {
+            const int r = li >> 1;
+            v_row = (r < 4 ? 0 : 4) + 4 * half + r;
+            v_c = dh;
+        } else {
+            v_row = 4 * half + (li >> 2);
+            v_c = 2 * dh + ((li & 3) >> 1);
         }
-        const uint8_t *kt = lds + buf * S::kBytes;
-        uint8_t *vt = lds + (2 + buf) * S::kBytes;
-        // rows that see different parts of the tile: is there a value to be kept from some?
-        bool apart = false;
-        if (t * KT + KT > common) {
-            if (set_apart<kType, RB, S::kBytes / 4>(vt, wave * (S::kBytes / 4), marks) && lane == 0) *flag = t;
-            __syncthreads();
-            apart = *flag == t;
-        }
-        if (idle) continue;
-        uint64_t vis = seen(a, w, before, t * KT) & now;
-        const uint64_t whole = KT == 64 ? ~0ull : 0xFFFFFFFFull;
-        vis &= whole;
-        if (__ballot(vis != 0) == 0) continue;  // nothing for this wave
-        f32x16 s[KS];
-        int kx = k_x, vx = v_x;
-        asm volatile("" : "+v"(kx), "+v"(vx));  // the pieces' places are worked out again, not kept: registers are short here
+        constexpr int kEight = 1;  // swizzle_v(row + 8) ^ swizzle_v(row), row below 8
+        const int v_at = v_row * RB + 8 * (li & 1), v_x = v_c ^ swizzle_v<RB>(v_row);
+
+        f32x16 acc[ND];
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[k][r] = 0.f;
+            for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
+        float m = -INFINITY, sum = 0.f;
+
+        for (int t = t0; t < t1; ++t) {
+            const int buf = (t - t0) & 1;
+            wait_copies<0>();
+            barrier();
+            const uint64_t now = here;
+            if (t + 1 < t1) {
+                pages.look_up((t + 1) * KT, KT);
+                const bool whole = pages.whole((t + 1) * KT, KT);
+                here = there(pages, (t + 1) * KT, whole, KT);
+                copy_rows<RB, S::kCopies, 4>(pages, (t + 1) * KT, whole, piece0, base + (buf ^ 1) * S::kBytes,
+                                          base + (2 + (buf ^ 1)) * S::kBytes);
+            }
+            const uint8_t *kt = lds + buf * S::kBytes;
+            uint8_t *vt = lds + (2 + buf) * S::kBytes;
+            // rows that see different parts of the tile: is there a value to be kept from some?
+            bool apart = false;
+            if (t * KT + KT > common) {
+                if (set_apart<kType, RB, S::kBytes / 4>(vt, wave * (S::kBytes / 4), marks) && lane == 0) *flag = t;
+                __syncthreads();
+                apart = *flag == t;
+            }
+            if (idle) continue;
+            uint64_t vis = seen(a, w, before, t * KT) & now;
+            const uint64_t whole = KT == 64 ? ~0ull : 0xFFFFFFFFull;
+            vis &= whole;
+            if (__ballot(vis != 0) == 0) continue;  // nothing for this wave
+            f32x16 s[KS];
+            int kx = k_x, vx = v_x;
+            asm volatile("" : "+v"(kx), "+v"(vx));  // the pieces' places are worked out again, not kept: registers are short here
 #pragma unroll
-            for (int c = 0; c < RB / 32; ++c) {
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(kt + k * 32 * RB + k_at + (((2 * c) ^ kx) << 4));
-                if constexpr (kType == Q4K_KV_E4M3) {
-                    const half8v x0 = widened(x.x, x.y), x1 = widened(x.z, x.w);
-                    s[k] = M::mfma32(x0, qh[2 * c], s[k]);
-                    s[k] = M::mfma32(x0, ql[2 * c], s[k]);
-                    s[k] = M::mfma32(x1, qh[2 * c + 1], s[k]);
-                    s[k] = M::mfma32(x1, ql[2 * c + 1], s[k]);
-                } else {
-                    const v8 x0 = __builtin_bit_cast(v8, x);
-                    s[k] = M::mfma32(x0, qh[c], s[k]);
-                    s[k] = M::mfma32(x0, ql[c], s[k]);
-                    if constexpr (M::kParts == 3) s[k] = M::mfma32(x0, __builtin_bit_cast(v8, third[c * 64]), s[k]);
+            for (int k = 0; k < KS; ++k) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[k][r] = 0.f;
+#pragma unroll
+                for (int c = 0; c < RB / 32; ++c) {
+                    const u32x4 x = *reinterpret_cast<const u32x4 *>(kt + k * 32 * RB + k_at + (((2 * c) ^ kx) << 4));
+                    if constexpr (kType == Q4K_KV_E4M3) {
+                        const half8v x0 = widened(x.x, x.y), x1 = widened(x.z, x.w);
+                        s[k] = M::mfma32(x0, qh[2 * c], s[k]);
+                        s[k] = M::mfma32(x0, ql[2 * c], s[k]);
+                        s[k] = M::mfma32(x1, qh[2 * c + 1], s[k]);
+                        s[k] = M::mfma32(x1, ql[2 * c + 1], s[k]);
+                    } else {
+                        const v8 x0 = __builtin_bit_cast(v8, x);
+                        s[k] = M::mfma32(x0, qh[c], s[k]);
+                        s[k] = M::mfma32(x0, ql[c], s[k]);
+                        if constexpr (M::kParts == 3) s[k] = M::mfma32(x0, __builtin_bit_cast(v8, third[c * 64]), s[k]);
+                    }
                 }
             }
-        }
-        const bool masked = __ballot(vis != whole) != 0;
-        const uint64_t mine = vis >> (4 * half);
-        if (masked) {
+            const bool masked = __ballot(vis != whole) != 0;
+            const uint64_t mine = vis >> (4 * half);
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!((mine >> (32 * k + 8 * (r >> 2) + (r & 3))) & 1)) s[k][r] = -INFINITY;
+            }
+            float top = s[0][0];
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!((mine >> (32 * k + 8 * (r >> 2) + (r & 3))) & 1)) s[k][r] = -INFINITY;
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[k][r]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        top *= factor;
-        // The output is corrected only where a maximum has risen by more than kSlack (or from nothing).
-        if (__ballot(!(top - m <= kSlack) && top != -INFINITY) != 0) {
-            const float m1 = fmaxf(m, top);
-            const float fade = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
-            m = m1;
-            sum *= fade;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[d][r] *= fade;
-        }
-        const float shift = kBias - (m == -INFINITY ? 0.f : m);
-        float part = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[k][r] = __builtin_amdgcn_exp2f(fmaf(s[k][r], factor, shift));
-                part += s[k][r];
-            }
-        sum += part;
-#pragma unroll
-        for (int q = 0; q < KT / 16; ++q) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = s[q >> 1][8 * (q & 1) + i];
-            v8 parts[M::kParts];
-            M::split(x, parts);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                v8 y;
-                const uint8_t *vq = vt + q * 16 * RB;
-                if constexpr (kType == Q4K_KV_E4M3) {
-                    const i32x2 z = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (__attribute__((address_space(3))) i32x2 *)(vq + v_at + (((2 * d) ^ vx) << 4)));
-                    y = widened(z.x, z.y);
-                } else {
-                    const s16x4 z0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4 *)(vq + v_at + (((4 * d) ^ vx) << 4)));
-                    const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4 *)(vq + v_at + 8 * RB + (((4 * d) ^ vx ^ kEight) << 4)));
-                    y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
-                }
-#pragma unroll
-                for (int i = 0; i < M::kParts; ++i) acc[d] = M::mfma32(y, parts[i], acc[d]);
-            }
-        }
-        if (apart) {  // rows that see a marked value get NaN there
-#pragma unroll 1
-            for (int i = 0; i < KT * DP / 8; ++i) {
-                uint32_t bits = marks[i];
-                if (!((vis >> (i / (DP / 8))) & 1)) bits = 0;
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[k][r]);
+            top = fmaxf(top, __shfl_xor(top, 32));
+            top *= factor;
+            // The output is corrected only where a maximum has risen by more than kSlack (or from nothing).
+            if (__ballot(!(top - m <= kSlack) && top != -INFINITY) != 0) {
+                const float m1 = fmaxf(m, top);
+                const float fade = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
+                m = m1;
+                sum *= fade;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int at = 32 * d + 8 * (r >> 2) + 4 * half + (r & 3) - i % (DP / 8) * 8;
-                        if (static_cast<unsigned>(at) < 8u && ((bits >> at) & 1)) acc[d][r] = nan_value();
+                    for (int r = 0; r < 16; ++r) acc[d][r] *= fade;
+            }
+            const float shift = kBias - (m == -INFINITY ? 0.f : m);
+            float part = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    s[k][r] = __builtin_amdgcn_exp2f(fmaf(s[k][r], factor, shift));
+                    part += s[k][r];
+                }
+            sum += part;
+#pragma unroll
+            for (int q = 0; q < KT / 16; ++q) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = s[q >> 1][8 * (q & 1) + i];
+                v8 parts[M::kParts];
+                M::split(x, parts);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    v8 y;
+                    const uint8_t *vq = vt + q * 16 * RB;
+                    if constexpr (kType == Q4K_KV_E4M3) {
+                        const i32x2 z = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                            (__attribute__((address_space(3))) i32x2 *)(vq + v_at + (((2 * d) ^ vx) << 4)));
+                        y = widened(z.x, z.y);
+                    } else {
+                        const s16x4 z0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4 *)(vq + v_at + (((4 * d) ^ vx) << 4)));
+                        const s16x4 z1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4 *)(vq + v_at + 8 * RB + (((4 * d) ^ vx ^ kEight) << 4)));
+                        y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
                     }
+#pragma unroll
+                    for (int i = 0; i < M::kParts; ++i) acc[d] = M::mfma32(y, parts[i], acc[d]);
+                }
+            }
+            if (apart) {  // rows that see a marked value get NaN there
+#pragma unroll 1
+                for (int i = 0; i < KT * DP / 8; ++i) {
+                    uint32_t bits = marks[i];
+                    if (!((vis >> (i / (DP / 8))) & 1)) bits = 0;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int at = 32 * d + 8 * (r >> 2) + 4 * half + (r & 3) - i % (DP / 8) * 8;
+                            if (static_cast<unsigned>(at) < 8u && ((bits >> at) & 1)) acc[d][r] = nan_value();
+                        }
+                }
             }
         }
-    }
 
-    sum += __shfl_xor(sum, 32);
-    int r0 = row0 + wave * 32 + col, D = a.p.head_dim;
-    asm volatile("" : "+v"(r0), "+s"(D));  // worked out again rather than kept over the loops
-    const Row o = row_of(a, u, r0, head);
-    if (!o.real) continue;
-    float *to = a.out + o.at;
-    float f = sum == 0.f ? 0.f : a.p.v_scale / sum;
-    if (u.units > 1) {
-        if (u.number >= a.units) continue;  // (offsets out of order)
-        const int64_t at = (u.number * a.p.kv_heads + head) * kTileRows + wave * 32 + col;
-        if (half == 0) {
-            a.part_ml[2 * at] = m;
-            a.part_ml[2 * at + 1] = sum;
-        }
-        if (m == -INFINITY && sum == 0.f) continue;  // the output is not read
-        to = a.part + at * D;
-        f = 1.f;
-    }
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            const int at = 32 * d + 2 * r + 4 * half;
-            if (at < D) {
-                f32x4 y;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = f == 0.f ? 0.f : acc[d][r + i] * f;
-                *reinterpret_cast<f32x4 *>(to + at) = y;
+        sum += __shfl_xor(sum, 32);
+        int r0 = row0 + wave * 32 + col, D = a.p.head_dim;
+        asm volatile("" : "+v"(r0), "+s"(D));  // worked out again rather than kept over the loops
+        const Row o = row_of(a, u, r0, head);
+        if (!o.real) continue;
+        float *to = a.out + o.at;
+        float f = sum == 0.f ? 0.f : a.p.v_scale / sum;
+        if (u.units > 1) {
+            if (u.number >= a.units) continue;  // (offsets out of order)
+            const int64_t at = (u.number * a.p.kv_heads + head) * kTileRows + wave * 32 + col;
+            if (half == 0) {
+                a.part_ml[2 * at] = m;
+                a.part_ml[2 * at + 1] = sum;
             }
+            if (m == -INFINITY && sum == 0.f) continue;  // the output is not read
+            to = a.part + at * D;
+            f = 1.f;
         }
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int at = 32 * d + 2 * r + 4 * half;
+                if (at < D) {
+                    f32x4 y;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = f == 0.f ? 0.f : acc[d][r + i] * f;
+                    *reinterpret_cast<f32x4 *>(to + at) = y;
+                }
+            }
     }
 }
 
@@ -878,7 +879,8 @@ struct FewShape {
 };
 
 template <int kType, int DP, int NB, bool kShort>
-__global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (FewShape<kType, DP, NB, kShort>::kPerSimd)) void attend_few(const Attend a) {
+__global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (FewShape<kType, DP, NB, kShort>::kPerSimd))
+    void attend_few(const Attend a) {
     typedef FewShape<kType, DP, NB, kShort> S;
     typedef Math<kType> M;
     typedef typename M::v8 v8;
@@ -888,343 +890,344 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (Fe
     const int head = blockIdx.x % a.p.kv_heads;
     Piece<kRows, KT, true> piece(a, blockIdx.x / a.p.kv_heads);
     for (Unit u; piece.next(u); __syncthreads()) {
-    int thread = threadIdx.x;
-    asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
-    const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 15, quarter = lane >> 4;
-    const int before = u.length - u.n;
-    const int row0 = u.tile * kRows;
-    const int capacity = a.p.max_pages << a.p.shift;
-    const int last = min((row0 + kRows - 1) / a.group, u.n - 1);
-    const int most = a.mask ? u.length : before + last + 1;
-    const int common = a.mask ? before : before + row0 / a.group + 1;
-    const int stop = max(min(most, capacity), 0);
-    // tiles of 32 keys: this wave's are first, first + kWaves, ...
-    const int t0 = u.begin * S::kWaves + wave;
-    const int t1 = u.end == INT_MAX ? (stop + 31) / 32 : min((stop + 31) / 32, u.end * S::kWaves);
-    if (!S::kJoined && a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) note_units<kRows>(a, u);
-    Row w[NB];
+        int thread = threadIdx.x;
+        asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
+        const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6), col = lane & 15, quarter = lane >> 4;
+        const int before = u.length - u.n;
+        const int row0 = u.tile * kRows;
+        const int capacity = a.p.max_pages << a.p.shift;
+        const int last = min((row0 + kRows - 1) / a.group, u.n - 1);
+        const int most = a.mask ? u.length : before + last + 1;
+        const int common = a.mask ? before : before + row0 / a.group + 1;
+        const int stop = max(min(most, capacity), 0);
+        // tiles of 32 keys: this wave's are first, first + kWaves, ...
+        const int t0 = u.begin * S::kWaves + wave;
+        const int t1 = u.end == INT_MAX ? (stop + 31) / 32 : min((stop + 31) / 32, u.end * S::kWaves);
+        if (!S::kJoined && a.target && u.begin == 0 && head == 0 && threadIdx.x == 0) note_units<kRows>(a, u);
+        Row w[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) w[n] = row_of(a, u, row0 + 16 * n + col, head);
+        for (int n = 0; n < NB; ++n) w[n] = row_of(a, u, row0 + 16 * n + col, head);
 
-    Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
-    uint8_t *const own = lds + wave * S::kOwn;
-    const uint32_t base = lds_address(own);
-    const auto copy = [&](int t, int buf) __attribute__((always_inline)) {
-        pages.look_up(t * 32, 32);
-        const bool whole = pages.whole(t * 32, 32);
-        const uint64_t is = there(pages, t * 32, whole, 32);
-        copy_rows<RB, S::kCopies, NB == 1 ? 4 : 1>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes, base + (buf * 2 + 1) * S::kBytes);
-        return is;
-    };
-    static_assert(!S::kLow || M::kParts == 2, "one part in LDS");
-    v8 query[NB][NS][S::kLow ? 1 : M::kParts];
-    u32x4 *const low = reinterpret_cast<u32x4 *>(lds + S::kEnded + 16) + lane;  // (every wave writes the same)
-    float factor[NB];
-    const float by = a.scale * kLog2e * a.p.k_scale;
-    // (asked for before the first copies, whose addresses have to be looked up first)
-    float held[NB][NS][8];
+        Pages pages(a.p, u.b, head, min(u.length, capacity), S::kSize);
+        uint8_t *const own = lds + wave * S::kOwn;
+        const uint32_t base = lds_address(own);
+        const auto copy = [&](int t, int buf) __attribute__((always_inline)) {
+            pages.look_up(t * 32, 32);
+            const bool whole = pages.whole(t * 32, 32);
+            const uint64_t is = there(pages, t * 32, whole, 32);
+            copy_rows<RB, S::kCopies, NB == 1 ? 4 : 1>(pages, t * 32, whole, 0, base + buf * 2 * S::kBytes,
+                                                       base + (buf * 2 + 1) * S::kBytes);
+            return is;
+        };
+        static_assert(!S::kLow || M::kParts == 2, "one part in LDS");
+        v8 query[NB][NS][S::kLow ? 1 : M::kParts];
+        u32x4 *const low = reinterpret_cast<u32x4 *>(lds + S::kEnded + 16) + lane;  // (every wave writes the same)
+        float factor[NB];
+        const float by = a.scale * kLog2e * a.p.k_scale;
+        // (asked for before the first copies, whose addresses have to be looked up first)
+        float held[NB][NS][8];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const int d = kType == Q4K_KV_E4M3 ? 64 * (s >> 1) + 16 * quarter + 8 * (s & 1) : 32 * s + 8 * quarter;
-            load_query(a, w[n], d, held[n][s]);
-        }
-    uint64_t here = 0;
-    if (t0 < t1) here = copy(t0, 0);
-
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        int e = 0;
-        factor[n] = 1.f;
-        if constexpr (M::kScaled) {
-            float largest = 0.f;
-#pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(held[n][s][i] * by));
-            largest = fmaxf(largest, __shfl_xor(largest, 16));
-            largest = fmaxf(largest, __shfl_xor(largest, 32));
-            e = exponent_for(largest);
-            factor[n] = ldexpf(1.f, -e);
-        }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = held[n][s][i] * by;
-                if constexpr (M::kScaled) x[i] = ldexpf(x[i], e);
+            for (int s = 0; s < NS; ++s) {
+                const int d = kType == Q4K_KV_E4M3 ? 64 * (s >> 1) + 16 * quarter + 8 * (s & 1) : 32 * s + 8 * quarter;
+                load_query(a, w[n], d, held[n][s]);
             }
-            v8 split[M::kParts];
-            M::split(x, split);
-            query[n][s][0] = split[0];
-            if constexpr (S::kLow) {
-                low[(n * NS + s) * 64] = __builtin_bit_cast(u32x4, split[1]);
-            } else {
-#pragma unroll
-                for (int i = 1; i < M::kParts; ++i) query[n][s][i] = split[i];
-            }
-        }
-    }
+        uint64_t here = 0;
+        if (t0 < t1) here = copy(t0, 0);
 
-    const int k_at = col * RB, k_x = quarter ^ swizzle_k<RB>(col);
-    int v_row, v_c;
-    if constexpr (kType == Q4K_KV_E4M3) {
-        const int r = col >> 1;
-        v_row = (r < 4 ? 0 : 12) + 4 * quarter + r;
-        v_c = 0;
-    } else {
-        v_row = 4 * quarter + (col >> 2);
-        v_c = (col & 3) >> 1;
-    }
-    const int v_at = v_row * RB + 8 * (col & 1), v_x = v_c ^ swizzle_v<RB>(v_row);
-
-    f32x4 acc[NB][ND];
-    float m[NB], sum[NB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        m[n] = -INFINITY;
-        sum[n] = 0.f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    int buf = 0;
-    for (int t = t0; t < t1; t += S::kWaves, buf ^= 1) {
-        const uint64_t now = here;
-        if (t + S::kWaves < t1) {
-            here = copy(t + S::kWaves, buf ^ 1);
-            wait_copies<2 * S::kCopies>();
-        } else {
-            wait_copies<0>();
-        }
-        const uint8_t *kt = own + buf * 2 * S::kBytes;
-        uint8_t *vt = own + (buf * 2 + 1) * S::kBytes, *marks = own + 4 * S::kBytes;
-        const bool apart = t * 32 + 32 > common && set_apart<kType, RB, S::kBytes>(vt, 0, marks);
-        uint32_t vis[NB], any = 0;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            vis[n] = static_cast<uint32_t>(seen(a, w[n], before, t * 32) & now);
-            any |= vis[n];
-        }
-        if (__ballot(any != 0) == 0) continue;
-        const auto part_of = [&](int n, int s, int i) {
-            if constexpr (S::kLow)
-                if (i == 1) return __builtin_bit_cast(v8, low[(n * NS + s) * 64]);
-            return query[n][s][S::kLow ? 0 : i];
-        };
-        f32x4 s[NB][2];
+            int e = 0;
+            factor[n] = 1.f;
+            if constexpr (M::kScaled) {
+                float largest = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+                for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) s[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < 8; ++i) largest = fmaxf(largest, __builtin_fabsf(held[n][s][i] * by));
+                largest = fmaxf(largest, __shfl_xor(largest, 16));
+                largest = fmaxf(largest, __shfl_xor(largest, 32));
+                e = exponent_for(largest);
+                factor[n] = ldexpf(1.f, -e);
+            }
 #pragma unroll
-            for (int c = 0; c < RB / 64; ++c) {
-                const u32x4 x = *reinterpret_cast<const u32x4 *>(kt + k * 16 * RB + k_at + (((4 * c) ^ k_x) << 4));
-                if constexpr (kType == Q4K_KV_E4M3) {
-                    const half8v x0 = widened(x.x, x.y), x1 = widened(x.z, x.w);
+            for (int s = 0; s < NS; ++s) {
+                float x[8];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n) {
-                            s[n][k] = M::mfma16(x0, part_of(n, 2 * c, i), s[n][k]);
-                            s[n][k] = M::mfma16(x1, part_of(n, 2 * c + 1, i), s[n][k]);
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = held[n][s][i] * by;
+                    if constexpr (M::kScaled) x[i] = ldexpf(x[i], e);
+                }
+                v8 split[M::kParts];
+                M::split(x, split);
+                query[n][s][0] = split[0];
+                if constexpr (S::kLow) {
+                    low[(n * NS + s) * 64] = __builtin_bit_cast(u32x4, split[1]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < M::kParts; ++i)
-#pragma unroll
-                        for (int n = 0; n < NB; ++n)
-                            s[n][k] = M::mfma16(__builtin_bit_cast(v8, x), part_of(n, c, i), s[n][k]);
+                    for (int i = 1; i < M::kParts; ++i) query[n][s][i] = split[i];
                 }
             }
         }
-        v8 parts[NB][M::kParts];
-        float fade[NB];
+
+        const int k_at = col * RB, k_x = quarter ^ swizzle_k<RB>(col);
+        int v_row, v_c;
+        if constexpr (kType == Q4K_KV_E4M3) {
+            const int r = col >> 1;
+            v_row = (r < 4 ? 0 : 12) + 4 * quarter + r;
+            v_c = 0;
+        } else {
+            v_row = 4 * quarter + (col >> 2);
+            v_c = (col & 3) >> 1;
+        }
+        const int v_at = v_row * RB + 8 * (col & 1), v_x = v_c ^ swizzle_v<RB>(v_row);
+
+        f32x4 acc[NB][ND];
+        float m[NB], sum[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            const uint32_t mine = vis[n] >> (4 * quarter);
-            if (__ballot(vis[n] != 0xFFFFFFFFu) != 0) {
+            m[n] = -INFINITY;
+            sum[n] = 0.f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        int buf = 0;
+        for (int t = t0; t < t1; t += S::kWaves, buf ^= 1) {
+            const uint64_t now = here;
+            if (t + S::kWaves < t1) {
+                here = copy(t + S::kWaves, buf ^ 1);
+                wait_copies<2 * S::kCopies>();
+            } else {
+                wait_copies<0>();
+            }
+            const uint8_t *kt = own + buf * 2 * S::kBytes;
+            uint8_t *vt = own + (buf * 2 + 1) * S::kBytes, *marks = own + 4 * S::kBytes;
+            const bool apart = t * 32 + 32 > common && set_apart<kType, RB, S::kBytes>(vt, 0, marks);
+            uint32_t vis[NB], any = 0;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                vis[n] = static_cast<uint32_t>(seen(a, w[n], before, t * 32) & now);
+                any |= vis[n];
+            }
+            if (__ballot(any != 0) == 0) continue;
+            const auto part_of = [&](int n, int s, int i) {
+                if constexpr (S::kLow)
+                    if (i == 1) return __builtin_bit_cast(v8, low[(n * NS + s) * 64]);
+                return query[n][s][S::kLow ? 0 : i];
+            };
+            f32x4 s[NB][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n) s[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < RB / 64; ++c) {
+                    const u32x4 x = *reinterpret_cast<const u32x4 *>(kt + k * 16 * RB + k_at + (((4 * c) ^ k_x) << 4));
+                    if constexpr (kType == Q4K_KV_E4M3) {
+                        const half8v x0 = widened(x.x, x.y), x1 = widened(x.z, x.w);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int n = 0; n < NB; ++n) {
+                                s[n][k] = M::mfma16(x0, part_of(n, 2 * c, i), s[n][k]);
+                                s[n][k] = M::mfma16(x1, part_of(n, 2 * c + 1, i), s[n][k]);
+                            }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < M::kParts; ++i)
+#pragma unroll
+                            for (int n = 0; n < NB; ++n)
+                                s[n][k] = M::mfma16(__builtin_bit_cast(v8, x), part_of(n, c, i), s[n][k]);
+                    }
+                }
+            }
+            v8 parts[NB][M::kParts];
+            float fade[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const uint32_t mine = vis[n] >> (4 * quarter);
+                if (__ballot(vis[n] != 0xFFFFFFFFu) != 0) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (!((mine >> (16 * k + r)) & 1)) s[n][k][r] = -INFINITY;
+                }
+                float top = s[n][0][0];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (!((mine >> (16 * k + r)) & 1)) s[n][k][r] = -INFINITY;
-            }
-            float top = s[n][0][0];
+                    for (int r = 0; r < 4; ++r) top = fmaxf(top, s[n][k][r]);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float m1 = fmaxf(m[n], top * factor[n]);
+                const float zero = m1 == -INFINITY ? 0.f : m1;
+                fade[n] = __builtin_amdgcn_exp2f(m[n] - zero);
+                m[n] = m1;
+                const float shift = kBias - zero;
+                float x[8], part = 0.f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[n][k][r]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m1 = fmaxf(m[n], top * factor[n]);
-            const float zero = m1 == -INFINITY ? 0.f : m1;
-            fade[n] = __builtin_amdgcn_exp2f(m[n] - zero);
-            m[n] = m1;
-            const float shift = kBias - zero;
-            float x[8], part = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = __builtin_amdgcn_exp2f(fmaf(s[n][i >> 2][i & 3], factor[n], shift));
-                part += x[i];
-            }
-            sum[n] = fmaf(sum[n], fade[n], part);
-            M::split(x, parts[n]);
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            v8 y;
-            if constexpr (kType == Q4K_KV_E4M3) {
-                const i32x2 z = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (__attribute__((address_space(3))) i32x2 *)(vt + v_at + ((d ^ v_x) << 4)));
-                y = widened(z.x, z.y);
-            } else {
-                const uint8_t *at = vt + v_at + (((2 * d) ^ v_x) << 4);
-                const s16x4 z0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
-                const s16x4 z1 =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(at + 16 * RB));
-                y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = __builtin_amdgcn_exp2f(fmaf(s[n][i >> 2][i & 3], factor[n], shift));
+                    part += x[i];
+                }
+                sum[n] = fmaf(sum[n], fade[n], part);
+                M::split(x, parts[n]);
             }
 #pragma unroll
-            for (int n = 0; n < NB; ++n) acc[n][d] *= fade[n];
+            for (int d = 0; d < ND; ++d) {
+                v8 y;
+                if constexpr (kType == Q4K_KV_E4M3) {
+                    const i32x2 z = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        (__attribute__((address_space(3))) i32x2 *)(vt + v_at + ((d ^ v_x) << 4)));
+                    y = widened(z.x, z.y);
+                } else {
+                    const uint8_t *at = vt + v_at + (((2 * d) ^ v_x) << 4);
+                    const s16x4 z0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
+                    const s16x4 z1 =
+                        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(at + 16 * RB));
+                    y = __builtin_bit_cast(v8, __builtin_shufflevector(z0, z1, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
 #pragma unroll
-            for (int i = 0; i < M::kParts; ++i)
+                for (int n = 0; n < NB; ++n) acc[n][d] *= fade[n];
 #pragma unroll
-                for (int n = 0; n < NB; ++n) acc[n][d] = M::mfma16(y, parts[n][i], acc[n][d]);
-        }
-        if (apart) {
+                for (int i = 0; i < M::kParts; ++i)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) acc[n][d] = M::mfma16(y, parts[n][i], acc[n][d]);
+            }
+            if (apart) {
 #pragma unroll 1
-            for (int i = 0; i < 32 * DP / 8; ++i) {
-                const uint32_t marked = marks[i];
-                if (marked == 0) continue;
+                for (int i = 0; i < 32 * DP / 8; ++i) {
+                    const uint32_t marked = marks[i];
+                    if (marked == 0) continue;
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    const uint32_t bits = (vis[n] >> (i / (DP / 8))) & 1 ? marked : 0;
+                    for (int n = 0; n < NB; ++n) {
+                        const uint32_t bits = (vis[n] >> (i / (DP / 8))) & 1 ? marked : 0;
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
+                        for (int d = 0; d < ND; ++d)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int at = 16 * d + 4 * quarter + r - i % (DP / 8) * 8;
-                            if (static_cast<unsigned>(at) < 8u && ((bits >> at) & 1)) acc[n][d][r] = nan_value();
-                        }
+                            for (int r = 0; r < 4; ++r) {
+                                const int at = 16 * d + 4 * quarter + r - i % (DP / 8) * 8;
+                                if (static_cast<unsigned>(at) < 8u && ((bits >> at) & 1)) acc[n][d][r] = nan_value();
+                            }
+                    }
                 }
             }
         }
-    }
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        sum[n] += __shfl_xor(sum[n], 16);
-        sum[n] += __shfl_xor(sum[n], 32);
-    }
+        for (int n = 0; n < NB; ++n) {
+            sum[n] += __shfl_xor(sum[n], 16);
+            sum[n] += __shfl_xor(sum[n], 32);
+        }
 
-    // the waves' parts: [wave][row][DP] and behind them maximum, sum and the row's place (stride DP + 4 words)
-    wait_copies<0>();
-    barrier();
-    float *const po = reinterpret_cast<float *>(lds);
-    constexpr int kStride = DP + 4;
+        // the waves' parts: [wave][row][DP] and behind them maximum, sum and the row's place (stride DP + 4 words)
+        wait_copies<0>();
+        barrier();
+        float *const po = reinterpret_cast<float *>(lds);
+        constexpr int kStride = DP + 4;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        float *mine = po + (wave * kRows + 16 * n + col) * kStride;
+        for (int n = 0; n < NB; ++n) {
+            float *mine = po + (wave * kRows + 16 * n + col) * kStride;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(mine + 16 * d + 4 * quarter) = acc[n][d];
-        if (quarter == 0) {
-            mine[DP] = m[n];
-            mine[DP + 1] = sum[n];
-            *reinterpret_cast<int64_t *>(mine + DP + 2) = w[n].at;
+            for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4 *>(mine + 16 * d + 4 * quarter) = acc[n][d];
+            if (quarter == 0) {
+                mine[DP] = m[n];
+                mine[DP + 1] = sum[n];
+                *reinterpret_cast<int64_t *>(mine + DP + 2) = w[n].at;
+            }
         }
-    }
-    __syncthreads();
-    const int quads = a.p.head_dim / 4;
-    // (offsets out of order can give more units or row tiles than there is room for)
-    const int64_t counter = u.row_tile * a.p.kv_heads + head;
-    const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && (!S::kJoined || counter < kCounters);
-    const int at_once = S::kWaves * 64 / quads;  // rows
-    const auto at_of = [&](int r) { return *reinterpret_cast<const int64_t *>(po + r * kStride + DP + 2); };
-    const int real = min(u.n * a.group - row0, kRows), d = (thread % quads) * 4;
-    for (int r = thread / quads; r < real; r += at_once) {
-        if (thread >= at_once * quads) break;
-        float top = -INFINITY;
+        __syncthreads();
+        const int quads = a.p.head_dim / 4;
+        // (offsets out of order can give more units or row tiles than there is room for)
+        const int64_t counter = u.row_tile * a.p.kv_heads + head;
+        const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && (!S::kJoined || counter < kCounters);
+        const int at_once = S::kWaves * 64 / quads;  // rows
+        const auto at_of = [&](int r) { return *reinterpret_cast<const int64_t *>(po + r * kStride + DP + 2); };
+        const int real = min(u.n * a.group - row0, kRows), d = (thread % quads) * 4;
+        for (int r = thread / quads; r < real; r += at_once) {
+            if (thread >= at_once * quads) break;
+            float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < S::kWaves; ++k) top = fmaxf(top, po[(k * kRows + r) * kStride + DP]);
-        const float zero = top == -INFINITY ? 0.f : top;
-        f32x4 y = {0.f, 0.f, 0.f, 0.f};
-        float total = 0.f;
+            for (int k = 0; k < S::kWaves; ++k) top = fmaxf(top, po[(k * kRows + r) * kStride + DP]);
+            const float zero = top == -INFINITY ? 0.f : top;
+            f32x4 y = {0.f, 0.f, 0.f, 0.f};
+            float total = 0.f;
 #pragma unroll
-        for (int k = 0; k < S::kWaves; ++k) {
-            const float *from = po + (k * kRows + r) * kStride;
-            // a wave without keys has nothing to add (its maximum is -inf)
-            const float f = __builtin_amdgcn_exp2f(from[DP] - zero);
-            total = fmaf(from[DP + 1], f, total);
-            y += *reinterpret_cast<const f32x4 *>(from + d) * f;
+            for (int k = 0; k < S::kWaves; ++k) {
+                const float *from = po + (k * kRows + r) * kStride;
+                // a wave without keys has nothing to add (its maximum is -inf)
+                const float f = __builtin_amdgcn_exp2f(from[DP] - zero);
+                total = fmaf(from[DP + 1], f, total);
+                y += *reinterpret_cast<const f32x4 *>(from + d) * f;
+            }
+            if (u.units == 1) {
+                const float f = a.p.v_scale / total;
+                if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
+                else y *= f;
+                *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
+            } else if (shared) {
+                const int64_t at = (u.number * a.p.kv_heads + head) * kRows + r;
+                if constexpr (S::kJoined) {
+                    share(a.part + at * a.p.head_dim + d, y.x, y.y);
+                    share(a.part + at * a.p.head_dim + d + 2, y.z, y.w);
+                    if (d == 0) share(a.part_ml + 2 * at, top, total);
+                } else {
+                    *reinterpret_cast<f32x4 *>(a.part + at * a.p.head_dim + d) = y;
+                    if (d == 0) *reinterpret_cast<f32x2 *>(a.part_ml + 2 * at) = f32x2{top, total};
+                }
+            }
         }
-        if (u.units == 1) {
+        if (!S::kJoined || !shared) continue;
+        // the row tile's last unit to end joins them all
+        wait_copies<0>();  // what this wave has shared is there for the others
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const bool last = __hip_atomic_fetch_add(a.counters + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                              static_cast<uint32_t>(u.units - 1);
+            if (last) __hip_atomic_store(a.counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            *ended = last;
+        }
+        __syncthreads();
+        if (!*ended) continue;
+        const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kRows + r; };
+        for (int r = thread / quads; r < real; r += at_once) {
+            if (thread >= at_once * quads) break;
+            float top = -INFINITY, total = 0.f;
+            f32x4 y = {0.f, 0.f, 0.f, 0.f};
+            const float *from = a.part + place(0, r) * a.p.head_dim + d, *from_ml = a.part_ml + 2 * place(0, r);
+            const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kRows;
+            constexpr int kAtOnce = 8;  // all asked for together (behind the last unit: that one again)
+            for (int c0 = 0; c0 < u.units; c0 += kAtOnce) {
+                f32x2 ml[kAtOnce], y0[kAtOnce], y1[kAtOnce];
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c) {
+                    const int64_t at = min(c0 + c, u.units - 1) * step;
+                    ml[c] = shared_pair(from_ml + 2 * at);
+                    y0[c] = shared_pair(from + at * a.p.head_dim);
+                    y1[c] = shared_pair(from + at * a.p.head_dim + 2);
+                }
+                float top1 = top;
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c) top1 = fmaxf(top1, ml[c].x);
+                const float zero = top1 == -INFINITY ? 0.f : top1, fade = __builtin_amdgcn_exp2f(top - zero);
+                top = top1;
+                total *= fade;
+                y *= fade;
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c) {
+                    const float f = c0 + c < u.units ? __builtin_amdgcn_exp2f(ml[c].x - zero) : 0.f;
+                    if (c0 + c < u.units) {
+                        total = fmaf(ml[c].y, f, total);
+                        y += f32x4{y0[c].x, y0[c].y, y1[c].x, y1[c].y} * f;
+                    }
+                }
+            }
             const float f = a.p.v_scale / total;
             if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
             else y *= f;
             *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
-        } else if (shared) {
-            const int64_t at = (u.number * a.p.kv_heads + head) * kRows + r;
-            if constexpr (S::kJoined) {
-                share(a.part + at * a.p.head_dim + d, y.x, y.y);
-                share(a.part + at * a.p.head_dim + d + 2, y.z, y.w);
-                if (d == 0) share(a.part_ml + 2 * at, top, total);
-            } else {
-                *reinterpret_cast<f32x4 *>(a.part + at * a.p.head_dim + d) = y;
-                if (d == 0) *reinterpret_cast<f32x2 *>(a.part_ml + 2 * at) = f32x2{top, total};
-            }
         }
-    }
-    if (!S::kJoined || !shared) continue;
-    // the row tile's last unit to end joins them all
-    wait_copies<0>();  // what this wave has shared is there for the others
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const bool last = __hip_atomic_fetch_add(a.counters + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                          static_cast<uint32_t>(u.units - 1);
-        if (last) __hip_atomic_store(a.counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *ended = last;
-    }
-    __syncthreads();
-    if (!*ended) continue;
-    const auto place = [&](int c, int r) { return (static_cast<int64_t>(u.unit0 + c) * a.p.kv_heads + head) * kRows + r; };
-    for (int r = thread / quads; r < real; r += at_once) {
-        if (thread >= at_once * quads) break;
-        float top = -INFINITY, total = 0.f;
-        f32x4 y = {0.f, 0.f, 0.f, 0.f};
-        const float *from = a.part + place(0, r) * a.p.head_dim + d, *from_ml = a.part_ml + 2 * place(0, r);
-        const int64_t step = static_cast<int64_t>(a.p.kv_heads) * kRows;
-        constexpr int kAtOnce = 8;  // all asked for together (behind the last unit: that one again)
-        for (int c0 = 0; c0 < u.units; c0 += kAtOnce) {
-            f32x2 ml[kAtOnce], y0[kAtOnce], y1[kAtOnce];
-#pragma unroll
-            for (int c = 0; c < kAtOnce; ++c) {
-                const int64_t at = min(c0 + c, u.units - 1) * step;
-                ml[c] = shared_pair(from_ml + 2 * at);
-                y0[c] = shared_pair(from + at * a.p.head_dim);
-                y1[c] = shared_pair(from + at * a.p.head_dim + 2);
-            }
-            float top1 = top;
-#pragma unroll
-            for (int c = 0; c < kAtOnce; ++c) top1 = fmaxf(top1, ml[c].x);
-            const float zero = top1 == -INFINITY ? 0.f : top1, fade = __builtin_amdgcn_exp2f(top - zero);
-            top = top1;
-            total *= fade;
-            y *= fade;
-#pragma unroll
-            for (int c = 0; c < kAtOnce; ++c) {
-                const float f = c0 + c < u.units ? __builtin_amdgcn_exp2f(ml[c].x - zero) : 0.f;
-                if (c0 + c < u.units) {
-                    total = fmaf(ml[c].y, f, total);
-                    y += f32x4{y0[c].x, y0[c].y, y1[c].x, y1[c].y} * f;
-                }
-            }
-        }
-        const float f = a.p.v_scale / total;
-        if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
-        else y *= f;
-        *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
-    }
     }
 }
 
@@ -1233,8 +1236,8 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (Fe
 // A row's units: their maxima and sums by lanes, then their outputs, four values
 // a lane; the lanes that one unit's output leaves free take the next units, and
 // their sums are added in a fixed order.  A unit whose maximum is -inf has seen
-// nothing (and may have written no output).  kThreads a row: a workgroup where
-// there are few rows (and many units), else a wave.
+// nothing, or NaN only (and may have written no output).  kThreads a row: a
+// workgroup where there are few rows (and many units), else a wave.
 
 template <int ROWS, int kThreads>
 __global__ __launch_bounds__(256) void join_units(const Attend a) {
@@ -1287,10 +1290,9 @@ __global__ __launch_bounds__(256) void join_units(const Attend a) {
         const int n = min(chunks - c0, kThreads);
         if (tid < n) {
             const float m = a.part_ml[2 * place(c0 + tid)];
-            // -1: nothing to add, and nothing to read
-            const float f = m == -INFINITY ? -1.f : __builtin_amdgcn_exp2f(m - zero);
-            weight[tid] = f;
-            if (m != -INFINITY) total = fmaf(a.part_ml[2 * place(c0 + tid) + 1], f, total);
+            const float f = __builtin_amdgcn_exp2f(m - zero);
+            weight[tid] = m == -INFINITY ? -1.f : f;  // -1: nothing to add, and nothing to read
+            total = fmaf(a.part_ml[2 * place(c0 + tid) + 1], f, total);  // (a sum of NaN only has no maximum)
         }
         sync();
         if (stream < streams) {
@@ -1338,7 +1340,7 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
     a.target = static_cast<int>(target);
     a.least = least;
     const int64_t units = tiles + target;
-    if (units * heads > INT_MAX || static_cast<int64_t>(a.p.tokens) * a.q_heads > INT_MAX) return Q4K_ERR_LAUNCH;
+    if (units * heads * threads > UINT32_MAX) return Q4K_ERR_LAUNCH;
     a.units = static_cast<int>(units);
     if (target) {
         const size_t rows = static_cast<size_t>(units) * heads * ROWS;
@@ -1399,7 +1401,9 @@ int launch_shape(Attend &a, hipStream_t stream) {
 template <int kType>
 int launch_type(Attend &a, hipStream_t stream) {
     const int D = a.p.head_dim;
-    return D <= 64 ? launch_shape<kType, 64>(a, stream) : D <= 128 ? launch_shape<kType, 128>(a, stream) : launch_shape<kType, 256>(a, stream);
+    return D <= 64    ? launch_shape<kType, 64>(a, stream)
+           : D <= 128 ? launch_shape<kType, 128>(a, stream)
+                      : launch_shape<kType, 256>(a, stream);
 }
 
 bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }

@@ -27,14 +27,23 @@
  *   - An index that has no page (below 0, or at or behind
  *     max_pages * page_size, or a page number outside [0, cache->pages)) is
  *     not stored, and read as if masked: it takes no part in any softmax.
- *   - Sequences may share pages (a common prefix).  Two new tokens of one call
- *     whose places are the same store one of the two.
+ *   - Sequences may share pages (a common prefix).  Where two new tokens of one
+ *     call have the same place it holds values of either.
  *
  * Conventions are those of q4k.h: device pointers on the current device, the
  * caller's stream, no host synchronization, the library's per-stream
- * workspace (make one eager call of each shape before a graph capture), the
- * same status codes, nothing enqueued on an error.  T == 0 or count == 0 (M or
- * N zero) is a successful no-op.
+ * workspace, the same status codes, nothing enqueued on an error.  T == 0 or
+ * count == 0 (M or N zero) is a successful no-op.  The arrays are not to be
+ * changed while a call that reads them runs.
+ *
+ * Workspace.  Attention over few row tiles (256 workgroups on the card or
+ * less: single tokens, short chunks, trees) is split along the keys and keeps
+ * its parts there, for each part 4 * (head_dim + 2) bytes a row of its tile (16
+ * to 128 rows), at most 3 * 512 parts, and 16 KB of counters that every call
+ * leaves at zero.  So make one eager call of each shape before a graph
+ * capture; and host threads that share a stream take turns, and so do the
+ * replays of graphs captured on one stream: two at once can leave the counters
+ * wrong for every later call on that stream.
  */
 #ifndef Q4K_LAYER_H
 #define Q4K_LAYER_H
@@ -93,15 +102,15 @@ typedef struct q4k_rotation {
  *   total may be NULL.  weight: DEVICE float32 [N].  total may be x or residual
  *   and y may be x or residual (any other overlap is not allowed).
  *   The sum of squares is held in double.
- *   Errors: M or N negative: Q4K_ERR_BAD_DIM; x, weight or y NULL:
- *   Q4K_ERR_NULL; Q4K_ERR_ALIGN. */
+ *   Errors: M or N negative, N above 2^30: Q4K_ERR_BAD_DIM; x, weight or y NULL:
+ *   Q4K_ERR_NULL; Q4K_ERR_ALIGN; M of 2^24 or more: Q4K_ERR_LAUNCH. */
 int q4k_rms_norm(const float *x, const float *residual, const float *weight, float eps, float *total, float *y,
                  int M, int N, hipStream_t stream);
 
 /* Stores the new tokens' keys and values, and gives the queries: k is normed
- * (k_norm) and rotated by the angles position * inv_freq[i], divided by
- * k_scale and rounded to the cache's type; v is divided by v_scale and
- * rounded; q_out is q normed (q_norm) and rotated.
+ * (k_norm) and rotated by the angles position * inv_freq[i], multiplied by
+ * 1 / k_scale and rounded to the cache's type; v is multiplied by 1 / v_scale
+ * and rounded; q_out is q normed (q_norm) and rotated.
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  * Angles are reduced in double (a position of 2^31 - 1 loses nothing), the
  * rest is float32 with one rounding to the cache's type: to the nearest, ties
@@ -115,7 +124,7 @@ int q4k_rms_norm(const float *x, const float *residual, const float *weight, flo
  *   T * kv_heads above 2^30, q_heads not a positive multiple of kv_heads
  *   where q is given), a scale that is not positive and finite:
  *   Q4K_ERR_BAD_DIM; a NULL array or struct (the optional ones excepted):
- *   Q4K_ERR_NULL; Q4K_ERR_ALIGN. */
+ *   Q4K_ERR_NULL; Q4K_ERR_ALIGN; more than 2^26 tokens: Q4K_ERR_LAUNCH. */
 int q4k_kv_append(const float *q, const float *k, const float *v, const q4k_kv_cache *cache,
                   const q4k_sequences *sequences, const q4k_rotation *rotation, float *q_out, int T, int q_heads,
                   hipStream_t stream);
@@ -128,14 +137,16 @@ int q4k_kv_append(const float *q, const float *k, const float *v, const q4k_kv_c
  *   q, out: DEVICE float32 [T, q_heads, head_dim], 16-byte aligned; out must
  *   not overlap the inputs.
  *   Numerics: the query times scale, and the softmax's unnormalised weights,
- *   are split into two binary16 values (two bfloat16 values for a bfloat16
- *   cache), so that each product with the stored values is good to about 2^-22
- *   (2^-17) of its size; products, maxima, sums and outputs are float32.
+ *   are split into two binary16 values (scaled by powers of two; three bfloat16
+ *   values over a bfloat16 cache), so that each product with the stored values
+ *   is good to about 2^-22 of its size; a weight below 2^-38 of its row's
+ *   largest is dropped; products, maxima, sums and outputs are float32.
  *   What a token does not see never reaches its row, NaN and infinities
  *   included (keys and values behind a sequence's end may hold anything).  A
  *   NaN or infinity that it sees gives NaN or infinities there.
  *   Results do not depend on the order in which workgroups finish.
- *   Errors: as for q4k_kv_append, and Q4K_ERR_ALLOC, Q4K_ERR_LAUNCH. */
+ *   Errors: as for q4k_kv_append, and Q4K_ERR_ALLOC; Q4K_ERR_LAUNCH also for more
+ *   than 2^24 row tiles. */
 int q4k_attention(const float *q, const q4k_kv_cache *cache, const q4k_sequences *sequences, float scale, float *out,
                   int T, int q_heads, hipStream_t stream);
 

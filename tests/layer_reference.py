@@ -121,8 +121,8 @@ def attention(p, q, scale, mask=None, words=0):
 
 
 def tolerance(p, S, A, longest):
-    """What out may be off, elementwise.  A score is off by the split of q (2^-22 of each
-    product, 2^-17 where the halves are bfloat16) and by the sum of D float32
+    """What out may be off, elementwise.  A score is off by the split of q (2^-21 of each
+    product at most; 2^-16 are granted over a bfloat16 cache) and by the sum of D float32
     products (sqrt(D) roundings of 2^-24 at work, times 4), relative to A; the exponent's
     argument and the hardware's exponential add |s| 2^-23 and 2^-22; numerator and
     denominator each carry it (times 2), the weights' split adds as much as q's, and

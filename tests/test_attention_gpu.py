@@ -314,3 +314,36 @@ def test_refusals():
         q4k.attention(z(1 + 3 * 256)[1:].view(3, 4, 64), cache, seqs)  # not 16-byte aligned
     with pytest.raises(ValueError, match="pages"):
         q4k.attention(q, cache, seqs._replace(pages=seqs.pages.cpu()))
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("sizes", [[(3000, 1)], [(3000, 8)], [(3000, 40)], [(200, 300), (0, 40)]])
+def test_nan_keys_of_a_whole_part(sizes, kind):
+    """Keys of NaN only over a stretch that one part of a split row may have to itself: NaN for every row."""
+    rng = rng_of(41, len(sizes), sizes[0][1], TYPES.index(kind))
+    p = Paged(rng, sizes, 2, 64, 16, kind)
+    for page in p.table[0, :12]:
+        p.k[int(page), 1] = float("nan")
+    q = rng.standard_normal((p.T, 8, 64)).astype(np.float32)
+    got = run(p, q, None).cpu().numpy()
+    first = int(p.offsets[1])
+    assert np.isnan(got[:first, 4:]).all()
+    assert np.isfinite(got[:, :4]).all() and np.isfinite(got[first:]).all()
+
+
+def test_values_of_every_size():
+    """Weights over many powers of two: a maximum that rises from tile to tile (and falls) in small and
+    large steps, in rows that are split and rows that are not."""
+    rng = rng_of(42)
+    for sizes in ([(1500, 1)], [(0, 300)], [(900, 50)]):
+        for step in (0.01, 0.05, 0.4, -0.05):
+            p = Paged(rng, sizes, 1, 64, 16, "f16")
+            for b in range(len(sizes)):
+                for j in range(int(p.lengths[b])):
+                    p.k[int(p.table[b, j // 16]), :, j % 16, 0] = step * j / 8
+            q = rng.standard_normal((p.T, 4, 64)).astype(np.float32)
+            q[..., 0] = 4 + np.arange(4)
+            cache, seqs = p.on_device()
+            got = q4k.attention(to_dev(q), cache, seqs, 0.3).cpu().numpy()
+            want, S, A = attention(p, q, 0.3)
+            assert (np.abs(got - want) <= tolerance(p, S, A, int(p.lengths.max()))).all()

@@ -35,6 +35,7 @@ def test_norm_refusals(lib):
         return lib.q4k_rms_norm(x, residual, weight, 1e-6, total, y, M, N, None)
 
     assert call(M=-1) == q4k.ERR_BAD_DIM and call(N=-1) == q4k.ERR_BAD_DIM
+    assert call(N=(1 << 30) + 1) == q4k.ERR_BAD_DIM
     for name in ("x", "weight", "y"):
         assert call(**{name: None}) == q4k.ERR_NULL, name
     for name in ("x", "residual", "weight", "total", "y"):
