@@ -1381,7 +1381,13 @@ int launch_shape(Attend &a, hipStream_t stream) {
     // Rows of a sequence on average: the smallest tiles that hold them (as far as the registers go).
     constexpr bool kBf16 = kType == Q4K_KV_BF16;
     const int64_t rows = (static_cast<int64_t>(a.p.tokens) * a.group + a.p.count - 1) / a.p.count;
-    if (rows <= 16) {
+    // Few tiles of 16 rows over a short context: each takes its keys by itself, which costs less than
+    // the wider tiles' longer steps and second launch (8, 16 and 32 tokens, four query heads a key head,
+    // 4000 keys of 128 x 16 bits: 21 -> 18, 30 -> 18, 27 -> 23 us; from 8000 keys on the keys read again
+    // cost more: 22 -> 28, 30 -> 32, 28 -> 41).  The table's width says how long a context can be.
+    const bool narrow = rows <= 128 && tiles_at_most(a, 16) * a.p.kv_heads <= kCus / 4 &&
+                        static_cast<int64_t>(a.p.max_pages) << a.p.shift <= 6000;
+    if (rows <= 16 || narrow) {
         // 128 KB of LDS are one workgroup of four waves on a CU, or two of two: with several
         // row tiles to a workgroup one's start hides behind the other's copies (48 sequences
         // of 4096 keys on average, 128 x 16 bits: 105 -> 87 us), with a few long ones there would

@@ -347,3 +347,62 @@ def test_values_of_every_size():
             got = q4k.attention(to_dev(q), cache, seqs, 0.3).cpu().numpy()
             want, S, A = attention(p, q, 0.3)
             assert (np.abs(got - want) <= tolerance(p, S, A, int(p.lengths.max()))).all()
+
+
+# (context, new tokens) of the sequences: with four query heads a key head tiles of 32, 64 and 128 rows, split along
+# the keys and not, uneven rows, and sequences that fit none of their batch's tiles.
+WIDE = {
+    "32 rows": [(700, 8)],
+    "32 rows, uneven": [(90, 1), (0, 15), (333, 8), (-3, 5), (0, 0), (1200, 7)],
+    "64 rows": [(700, 16)],
+    "64 rows, uneven": [(2, 30), (64, 1), (500, 17), (0, 3), (-2, 9)],
+    "128 rows": [(900, 32)],
+    "128 rows, uneven": [(40, 70), (300, 1), (0, 33), (0, 0), (65, 20)],
+    "many tiles": [(13 * b % 70, 8) for b in range(70)],
+    "many small": [(29 * b % 200, 1) for b in range(150)],
+}
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("D", [48, 64, 96, 128, 256])
+@pytest.mark.parametrize("name", WIDE)
+def test_every_kernel(name, D, kind):
+    """A table wide enough for a long context (which the choice of the kernel goes by), with and without a mask."""
+    rng = rng_of(43, list(WIDE).index(name), D, TYPES.index(kind))
+    sizes = WIDE[name]
+    p = Paged(rng, sizes, 2, D, 16, kind, extra_rows=1, extra_cols=400)
+    check(p, rng, 8)
+    words = 3
+    check(p, rng, 8, tree_mask(rng, sizes, words, 1), words)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("n", [8, 16, 32])
+def test_what_is_not_seen_in_every_kernel(n, kind):
+    """As test_what_is_not_seen_never_reaches_a_row, for the tiles of 32, 64 and 128 rows."""
+    import torch
+    rng = rng_of(44, n, TYPES.index(kind))
+    p = Paged(rng, [(300, n)], 2, 64, 16, kind, extra_cols=400)
+    q = rng.standard_normal((n, 8, 64)).astype(np.float32)
+    mask = tree_mask(rng, [(300, n)], 1)
+    for m in (None, mask):
+        clean = run(p, q, None, m).cpu().numpy()
+        i = n // 2
+        at = (int(p.table[0, (300 + i) // 16]), 1, (300 + i) % 16, 5)
+        old = p.v[at].clone()
+        p.v[at] = torch.tensor(float("nan")).to(p.v.dtype)
+        got = run(p, q, None, m).cpu().numpy()
+        p.v[at] = old
+        see = np.arange(n) >= i if m is None else (m[:, 0] >> i & 1) == 1
+        assert np.array_equal(got[~see], clean[~see]) and np.array_equal(got[:, :4], clean[:, :4])
+        assert np.isnan(got[see][:, 4:, 5]).all()
+        keep = np.arange(64) != 5
+        assert np.array_equal(got[see][:, :, keep], clean[see][:, :, keep])
+
+
+@pytest.mark.parametrize("page", [1, 2, 4, 8])
+def test_small_pages_in_every_kernel(page):
+    rng = rng_of(45, page)
+    for sizes in ([(500, 8)], [(90, 16)], [(300, 40)], [(70, 1), (33, 1)]):
+        for kind in ("f16", "e4m3"):
+            check(Paged(rng, sizes, 1, 128, page, kind, extra_cols=6400 // page), rng, 4)
