@@ -682,10 +682,10 @@ def _checked_rows(name, x, dims):
     shape, dev = x.shape, x.get_device()
     if len(shape) != dims or x.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32 with {dims} dimensions")
-    if max(shape) > INT_MAX:
-        raise Q4KError(ERR_BAD_DIM, f"{name} {list(shape)}")
     if dev < 0 or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device tensor")
+    if max(shape) > INT_MAX:
+        raise Q4KError(ERR_BAD_DIM, f"{name} {list(shape)}")
     return (*shape, dev)
 
 
@@ -694,12 +694,13 @@ _KV_TYPES = {}
 
 def _checked_cache(cache, kv_heads, head_dim, dev):
     """The C struct of a KVCache on GPU number dev for this many heads of this size (kv_heads None: any)."""
-    import torch
     if not _KV_TYPES:
+        import torch
         _KV_TYPES.update({torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3})
     k, v, k_scale, v_scale = cache
     shape, dtype = k.shape, k.dtype
-    if dtype not in _KV_TYPES:
+    kind = _KV_TYPES.get(dtype)
+    if kind is None:
         raise TypeError(f"the cache must be float16, bfloat16 or float8_e4m3fn, not {dtype}")
     if len(shape) != 4:
         raise ValueError("the cache must be [pages, kv_heads, page_size, head_dim]")
@@ -709,8 +710,11 @@ def _checked_cache(cache, kv_heads, head_dim, dev):
                          f"{'' if kv_heads is None else f'{kv_heads} '}heads of {head_dim}")
     if max(shape) > INT_MAX:
         raise Q4KError(ERR_BAD_DIM, f"cache {list(shape)}")
-    return _Cache(_checked_tensor("cache.k", k, dtype, shape, dev), _checked_tensor("cache.v", v, dtype, shape, dev),
-                  _KV_TYPES[dtype], pages, heads, page_size, dim, k_scale, v_scale)
+    if not (v.dtype is dtype and v.shape == shape and k.get_device() == dev and v.get_device() == dev and
+            k.is_contiguous() and v.is_contiguous()):  # (one look at both where nothing is wrong)
+        _checked_tensor("cache.k", k, dtype, shape, dev)
+        _checked_tensor("cache.v", v, dtype, shape, dev)
+    return _Cache(k.data_ptr(), v.data_ptr(), kind, pages, heads, page_size, dim, k_scale, v_scale)
 
 
 def _checked_sequences(sequences, dev):
@@ -722,9 +726,15 @@ def _checked_sequences(sequences, dev):
     B, most = pages.shape
     if B > INT_MAX or most > INT_MAX:
         raise Q4KError(ERR_BAD_DIM, f"pages {list(pages.shape)}")
-    return _Sequences(_checked_tensor("offsets", offsets, torch.int32, (B + 1,), dev),
-                      _checked_tensor("lengths", lengths, torch.int32, (B,), dev),
-                      _checked_tensor("pages", pages, torch.int32, (B, most), dev), B, most)
+    i32 = torch.int32
+    if not (offsets.dtype is i32 and lengths.dtype is i32 and pages.dtype is i32 and offsets.shape == (B + 1,) and
+            lengths.shape == (B,) and offsets.get_device() == dev and lengths.get_device() == dev and
+            pages.get_device() == dev and offsets.is_contiguous() and lengths.is_contiguous() and
+            pages.is_contiguous()):  # (one look at all three where nothing is wrong)
+        _checked_tensor("offsets", offsets, i32, (B + 1,), dev)
+        _checked_tensor("lengths", lengths, i32, (B,), dev)
+        _checked_tensor("pages", pages, i32, (B, most), dev)
+    return _Sequences(offsets.data_ptr(), lengths.data_ptr(), pages.data_ptr(), B, most)
 
 
 def kv_append(k, v, cache: KVCache, sequences: Sequences, rotation: Optional[Rotation] = None, q=None, positions=None,
@@ -753,20 +763,18 @@ def kv_append(k, v, cache: KVCache, sequences: Sequences, rotation: Optional[Rot
             q_out_ptr = _checked_tensor("q_out", q_out, torch.float32, (T, q_heads, D), dev)
     elif q_out is not None:
         raise ValueError("q_out needs a q")
-    r = _Rotation(eps=eps)
-    if q_norm is not None:
-        r.q_norm = _checked_tensor("q_norm", q_norm, torch.float32, (D,), dev)
-    if k_norm is not None:
-        r.k_norm = _checked_tensor("k_norm", k_norm, torch.float32, (D,), dev)
+    freq_ptr, rotary, pairs = None, 0, 0
     if rotation is not None:
         inv_freq, interleaved = rotation
         if len(inv_freq.shape) != 1:
             raise ValueError("inv_freq must be float32 [R / 2]")
         half = inv_freq.shape[0]
-        r.inv_freq = _checked_tensor("inv_freq", inv_freq, torch.float32, (half,), dev)
-        r.rotary, r.interleaved = min(2 * half, INT_MAX - 1), 1 if interleaved else 0
-    if positions is not None:
-        r.positions = _checked_tensor("positions", positions, torch.int32, (T,), dev)
+        freq_ptr = _checked_tensor("inv_freq", inv_freq, torch.float32, (half,), dev)
+        rotary, pairs = min(2 * half, INT_MAX - 1), 1 if interleaved else 0
+    r = _Rotation(None if q_norm is None else _checked_tensor("q_norm", q_norm, torch.float32, (D,), dev),
+                  None if k_norm is None else _checked_tensor("k_norm", k_norm, torch.float32, (D,), dev), freq_ptr,
+                  None if positions is None else _checked_tensor("positions", positions, torch.int32, (T,), dev),
+                  eps, rotary, pairs)
     rc = library().q4k_kv_append(q_ptr, k.data_ptr(), v_ptr, c, s, r, q_out_ptr, T, q_heads, _stream_for(dev, stream))
     if rc != OK:
         raise Q4KError(rc, "q4k_kv_append")
