@@ -175,6 +175,12 @@ __device__ __forceinline__ void wait_copies() {
     __builtin_amdgcn_s_waitcnt(0x0070 | (VM & 15) | (VM >> 4) << 14);
     asm volatile("" ::: "memory");
 }
+// Every LDS operation of this wave has ended (copies may be on their way).
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ void barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -436,9 +442,17 @@ struct Piece {
     __device__ Piece(const Attend &a_, int64_t w) : a(a_), kept(a_, 0, 0, 0), kept_b(0), workgroup(w) {
         size = 1;
         if (a.target) {
-            int64_t all = __shfl(kept.line_sum, 63);
-            for (int b = 64; b < a.p.count; b += 64) all = __shfl(S(a, b, 0, all).line_sum, 63);
-            size = max(uniform(quotient(uniform(all) + a.target - 1, a.target)), static_cast<int64_t>(a.least));
+            int64_t all = __shfl(kept.line_sum, 63), rows = __shfl(kept.tiles_sum, 63);
+            for (int b = 64; b < a.p.count; b += 64) {
+                const S x(a, b, rows, all);
+                all = __shfl(x.line_sum, 63);
+                rows = __shfl(x.tiles_sum, 63);
+            }
+            all = uniform(all);
+            // (16-row tiles over few keys: one key tile a workgroup as long as the parts are few, 500 keys 11.3 ->
+            // 9.8 us; with 32 parts of 4000 keys it took 15.7 us instead of 13.4)
+            const int least = kKeep && all <= 12 * uniform(rows) ? 1 : a.least;
+            size = max(uniform(quotient(all + a.target - 1, a.target)), static_cast<int64_t>(least));
         }
         at = w * size;
         stop = at + size;
@@ -863,13 +877,15 @@ struct FewShape {
     static constexpr int kRows = 16 * NB;
     static constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2;
     static constexpr int RB = DP * kSize;
-    // Four waves, or as many as have room in LDS; two workgroups on a CU where that is 64 KB.
-    static constexpr int kWaves = RB == 512 || kShort ? 2 : 4;
+    // Four waves; two workgroups on a CU where that is 64 KB of LDS.  Rows of 512 bytes leave room for
+    // one buffer a wave: the other three waves' copies are on their way while one computes.
+    static constexpr int kWaves = kShort ? 2 : 4;
+    static constexpr int kBuffers = RB == 512 ? 1 : 2;  // of a wave
     static constexpr int kBytes = 32 * RB;  // of a tile's K, and of its V
     static constexpr int kCopies = kBytes / 1024;
     static constexpr int kJoin = kWaves * kRows * (DP + 4) * 4;
     static constexpr int kMarks = 32 * DP / 8;  // a bit per value
-    static constexpr int kOwn = 4 * kBytes + kMarks;
+    static constexpr int kOwn = 2 * kBuffers * kBytes + kMarks;
     static constexpr int kEnded = kWaves * kOwn > kJoin ? kWaves * kOwn : kJoin;
     static constexpr bool kLow = NB * DP > 256;  // the queries' second parts in LDS: there are too few registers
     static constexpr int kLds = kEnded + 16 + (kLow ? kRows * DP * 2 : 0);
@@ -993,16 +1009,24 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (Fe
             for (int d = 0; d < ND; ++d) acc[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         int buf = 0;
-        for (int t = t0; t < t1; t += S::kWaves, buf ^= 1) {
+        const auto turn = [&](int t) {
+            if (S::kBuffers == 2) {
+                buf ^= 1;
+            } else if (t + S::kWaves < t1) {
+                wait_lds();  // (nothing is on its way to the buffer any more)
+                here = copy(t + S::kWaves, 0);
+            }
+        };
+        for (int t = t0; t < t1; turn(t), t += S::kWaves) {
             const uint64_t now = here;
-            if (t + S::kWaves < t1) {
+            if (S::kBuffers == 2 && t + S::kWaves < t1) {
                 here = copy(t + S::kWaves, buf ^ 1);
                 wait_copies<2 * S::kCopies>();
             } else {
                 wait_copies<0>();
             }
             const uint8_t *kt = own + buf * 2 * S::kBytes;
-            uint8_t *vt = own + (buf * 2 + 1) * S::kBytes, *marks = own + 4 * S::kBytes;
+            uint8_t *vt = own + (buf * 2 + 1) * S::kBytes, *marks = own + 2 * S::kBuffers * S::kBytes;
             const bool apart = t * 32 + 32 > common && set_apart<kType, RB, S::kBytes>(vt, 0, marks);
             uint32_t vis[NB], any = 0;
 #pragma unroll
