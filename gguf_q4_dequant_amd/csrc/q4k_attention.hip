@@ -30,8 +30,9 @@
 // its values are multiplied as zeros and the rows that see one are made NaN.
 //
 // Few row tiles are split along the keys (Piece): the workgroups that fill the
-// card take equal shares of all key tiles, and a second launch joins the parts.
-// The lengths stay on the device; every workgroup works its share out by itself.
+// card take equal shares of all key tiles, and the parts of a row are joined, by
+// the last of them to end or by a second launch.  The lengths stay on the
+// device; every workgroup works its share out by itself.
 #include <math.h>
 
 #include "q4k_cache.h"
@@ -49,7 +50,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 struct Part {  // a row tile's units
-    int unit0, chunks;
+    int unit0, units;
 };
 
 struct Attend {
@@ -872,15 +873,16 @@ __device__ __forceinline__ f32x2 shared_pair(const float *at) {
     return f32x2{__uint_as_float(static_cast<uint32_t>(pair)), __uint_as_float(static_cast<uint32_t>(pair >> 32))};
 }
 
-template <int kType, int DP, int NB, bool kShort>
+template <int kType, int DP, int NB, bool kPaired>
 struct FewShape {
     static constexpr int kRows = 16 * NB;
     static constexpr int kSize = kType == Q4K_KV_E4M3 ? 1 : 2;
     static constexpr int RB = DP * kSize;
-    // Four waves; two workgroups on a CU where that is 64 KB of LDS.  Rows of 512 bytes leave room for
-    // one buffer a wave: the other three waves' copies are on their way while one computes.
-    static constexpr int kWaves = kShort ? 2 : 4;
-    static constexpr int kBuffers = RB == 512 ? 1 : 2;  // of a wave
+    // Two workgroups on a CU where their LDS allows it.  Of 512-byte rows there is room for one buffer a
+    // wave, of 256-byte ones too where two workgroups are wanted: a wave then computes while the
+    // others' copies are on their way.
+    static constexpr int kWaves = 4;
+    static constexpr int kBuffers = RB == 512 || kPaired ? 1 : 2;  // of a wave
     static constexpr int kBytes = 32 * RB;  // of a tile's K, and of its V
     static constexpr int kCopies = kBytes / 1024;
     static constexpr int kJoin = kWaves * kRows * (DP + 4) * 4;
@@ -891,13 +893,13 @@ struct FewShape {
     static constexpr int kLds = kEnded + 16 + (kLow ? kRows * DP * 2 : 0);
     static constexpr bool kJoined = NB == 1;  // in the same launch
     static constexpr int kPerCu = NB < 4 && kLds <= 81920 ? 2 : 1;
-    static constexpr int kPerSimd = kPerCu * kWaves > 4 ? 2 : 1;  // waves
+    static constexpr int kPerSimd = kPerCu;  // waves
 };
 
-template <int kType, int DP, int NB, bool kShort>
-__global__ __launch_bounds__((FewShape<kType, DP, NB, kShort>::kWaves * 64), (FewShape<kType, DP, NB, kShort>::kPerSimd))
+template <int kType, int DP, int NB, bool kPaired>
+__global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (FewShape<kType, DP, NB, kPaired>::kPerSimd))
     void attend_few(const Attend a) {
-    typedef FewShape<kType, DP, NB, kShort> S;
+    typedef FewShape<kType, DP, NB, kPaired> S;
     typedef Math<kType> M;
     typedef typename M::v8 v8;
     constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16, kRows = S::kRows;
@@ -1287,8 +1289,8 @@ __global__ __launch_bounds__(256) void join_units(const Attend a) {
         }
     }
     // (what offsets out of order left in the plan is not followed)
-    const bool here = part.chunks > 1 && part.unit0 >= 0 && part.chunks <= a.units - part.unit0;
-    const int chunks = here ? part.chunks : 0;
+    const bool here = part.units > 1 && part.unit0 >= 0 && part.units <= a.units - part.unit0;
+    const int units = here ? part.units : 0;
     const int D = p.head_dim, quads = D / 4, streams = kThreads / quads;
     const int quad = tid % quads, stream = tid / quads;
     const auto place = [&](int c) { return (static_cast<int64_t>(part.unit0 + c) * p.kv_heads + head) * ROWS + r; };
@@ -1297,7 +1299,7 @@ __global__ __launch_bounds__(256) void join_units(const Attend a) {
         else __builtin_amdgcn_wave_barrier();
     };
     float top = -INFINITY;
-    for (int c = tid; c < chunks; c += kThreads) top = fmaxf(top, a.part_ml[2 * place(c)]);
+    for (int c = tid; c < units; c += kThreads) top = fmaxf(top, a.part_ml[2 * place(c)]);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
     if (kThreads > 64) {
@@ -1309,9 +1311,9 @@ __global__ __launch_bounds__(256) void join_units(const Attend a) {
     float *const weight = weights + mine * kThreads;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
     float total = 0.f;
-    for (int c0 = 0; c0 < chunks; c0 += kThreads) {
+    for (int c0 = 0; c0 < units; c0 += kThreads) {
         sync();
-        const int n = min(chunks - c0, kThreads);
+        const int n = min(units - c0, kThreads);
         if (tid < n) {
             const float m = a.part_ml[2 * place(c0 + tid)];
             const float f = __builtin_amdgcn_exp2f(m - zero);
@@ -1393,10 +1395,10 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
     return Q4K_OK;
 }
 
-template <int kType, int DP, int NB, bool kShort = false>
+template <int kType, int DP, int NB, bool kPaired = false>
 int launch_few(Attend &a, hipStream_t stream) {
-    typedef FewShape<kType, DP, NB, kShort> S;
-    return launch<S::kRows, 32 * S::kWaves, S::kJoined>(a, attend_few<kType, DP, NB, kShort>, S::kWaves * 64, S::kLds,
+    typedef FewShape<kType, DP, NB, kPaired> S;
+    return launch<S::kRows, 32 * S::kWaves, S::kJoined>(a, attend_few<kType, DP, NB, kPaired>, S::kWaves * 64, S::kLds,
                                                         S::kPerCu, 2, stream);
 }
 
@@ -1412,12 +1414,14 @@ int launch_shape(Attend &a, hipStream_t stream) {
     const bool narrow = rows <= 128 && tiles_at_most(a, 16) * a.p.kv_heads <= kCus / 4 &&
                         static_cast<int64_t>(a.p.max_pages) << a.p.shift <= 6000;
     if (rows <= 16 || narrow) {
-        // 128 KB of LDS are one workgroup of four waves on a CU, or two of two: with several
-        // row tiles to a workgroup one's start hides behind the other's copies (48 sequences
-        // of 4096 keys on average, 128 x 16 bits: 105 -> 87 us), with a few long ones there would
-        // be twice the parts to join (one of 131072 keys: 102 -> 119 us).
+        // 128 KB of LDS are one workgroup on a CU with two buffers a wave, or two with one: with
+        // many row tiles a workgroup's start hides behind the other's copies and eight waves
+        // compute (48 sequences of 4096 keys on average, 128 x 16 bits: 105 -> 85 us, 16 of 16000:
+        // 202 -> 187, eight tiles over 4000 keys: 24.5 -> 21.9), with a few there would be twice
+        // the parts to join (one sequence of 16000 keys: 21 -> 25 us, four tiles over 4000:
+        // 17.7 -> 21.8).
         if constexpr (FewShape<kType, DP, 1, false>::RB == 256)
-            if (2 * tiles_at_most(a, 16) * a.p.kv_heads > kCus) return launch_few<kType, DP, 1, true>(a, stream);
+            if (4 * tiles_at_most(a, 16) * a.p.kv_heads >= kCus) return launch_few<kType, DP, 1, true>(a, stream);
         return launch_few<kType, DP, 1>(a, stream);
     }
     if constexpr (DP <= (kBf16 ? 128 : 256))

@@ -406,3 +406,34 @@ def test_small_pages_in_every_kernel(page):
     for sizes in ([(500, 8)], [(90, 16)], [(300, 40)], [(70, 1), (33, 1)]):
         for kind in ("f16", "e4m3"):
             check(Paged(rng, sizes, 1, 128, page, kind, extra_cols=6400 // page), rng, 4)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("D", [80, 128, 208])
+@pytest.mark.parametrize("page", [1, 64])
+def test_many_tiles_of_few_rows(page, D, kind):
+    """Enough row tiles for two workgroups on a CU, with contexts of many key tiles a wave (whose buffers are
+    filled again and again), with and without a mask."""
+    rng = rng_of(46, page, D, TYPES.index(kind))
+    sizes = [(int(c), 1 + b % 3) for b, c in enumerate(rng.integers(0, 1500, 34))]
+    p = Paged(rng, sizes, 2, D, page, kind, extra_rows=1)
+    check(p, rng, 8)
+    check(p, rng, 8, tree_mask(rng, sizes, 1, 1), 1)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_what_is_not_seen_by_many_tiles_of_few_rows(kind):
+    import torch
+    rng = rng_of(47, TYPES.index(kind))
+    contexts = [0, 31, 300, 700] * 8
+    p = Paged(rng, [(c, 3) for c in contexts], 2, 128, 16, kind)
+    q = rng.standard_normal((96, 8, 128)).astype(np.float32)
+    clean = run(p, q, None).cpu().numpy()
+    for b, c in enumerate(contexts):
+        p.v[int(p.table[b, (c + 1) // 16]), 1, (c + 1) % 16, 77] = torch.tensor(float("nan")).to(p.v.dtype)
+    got = run(p, q, None).cpu().numpy()
+    see = np.arange(96) % 3 >= 1
+    assert np.array_equal(got[~see], clean[~see]) and np.array_equal(got[:, :4], clean[:, :4])
+    assert np.isnan(got[see][:, 4:, 77]).all()
+    keep = np.arange(128) != 77
+    assert np.array_equal(got[see][:, :, keep], clean[see][:, :, keep])
