@@ -344,7 +344,7 @@ __device__ __forceinline__ bool set_apart(uint8_t *v, int at, uint8_t *marks) {
 // time whatever the lengths are; workgroup w takes piece w.  What it has of a row
 // tile is a unit, number w + (number of the row tile): either number grows by
 // one from unit to unit, so a row tile's units follow each other.  With as many
-// row tiles or more, every workgroup takes one.
+// row tiles or more, every workgroup takes one, the most keys first.
 
 struct Unit {
     int b, first, n;  // sequence, its first row of q, its new tokens
@@ -387,17 +387,17 @@ struct Span {
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));  // (no addresses kept from one unit to the next)
         first = n = length = 0;
-        if (b + lane < p.count) {
+        if (a.target && b + lane < p.count) {
             first = offset_of(p, b + lane);
             n = max(offset_of(p, b + lane + 1) - first, 0);
             length = max(p.lengths[b + lane], 0);  // (without tokens nothing is seen)
         }
         tiles = (static_cast<int64_t>(n) * a.group + ROWS - 1) / ROWS;
         key_tiles = max((min(length, p.max_pages << p.shift) + KT - 1) / KT, 1);
-        line = a.target ? tiles * key_tiles : tiles;
+        line = tiles * key_tiles;
         tiles_sum = tiles;
         line_sum = line;
-        if (p.count == 1) {  // (one user's token: 0.3 us less)
+        if (p.count == 1 || !a.target) {  // (one user's token: 0.3 us less)
             tiles_sum = uniform(tiles);
             line_sum = uniform(line);
             return;
@@ -429,6 +429,18 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return q;
 }
 
+// A sum (or largest) over a wave's lanes, of numbers not below 0; uniform.
+template <typename Op>
+__device__ __forceinline__ int reduced(int x, Op op) {
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));  // a row of 16 lanes: from 1 below,
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));  // 2,
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));  // 4,
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));  // 8;
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));  // lane 15 to the second row, 47 to the fourth,
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));  // lane 31 to the upper half
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
 // A workgroup's piece of the line.  kKeep: the 64 sequences last looked through stay
 // in registers; without it (where the products need them) they are looked through
 // again for every unit.
@@ -438,6 +450,7 @@ struct Piece {
     const Attend &a;
     S kept;
     int kept_b;
+    static constexpr int kSets = kKeep ? 4 : 1;  // of 64 sequences
     int64_t at, stop, size, workgroup;
 
     __device__ Piece(const Attend &a_, int64_t w) : a(a_), kept(a_, 0, 0, 0), kept_b(0), workgroup(w) {
@@ -458,8 +471,97 @@ struct Piece {
         at = w * size;
         stop = at + size;
     }
+    // Every workgroup has one row tile, and the ones with the most keys go first: the one of rank at by the tokens
+    // before its end (counted in row tiles), of every 256 sequences (where there are many rows: 64).  Tile t of a
+    // sequence has level context + t, and the tiles of a level and above are quickly counted, so the rank's level is
+    // found by halving.  (In the batch's order or against it the longest may start last: seven prompts up to 1531
+    // tokens 116 -> 103 us, 96 tokens over up to 4000 keys 166 -> 147, 64 chunks of 8 behind up to 4000 164 -> 116;
+    // where all are alike it takes 1 us: 64 tokens over 500 keys 29.6 -> 30.7.)
+    __device__ __forceinline__ bool most_keys_first(Unit &u) {
+        if (at >= stop) return false;
+        const Paged &p = a.p;
+        const auto sum = [](int x, int y) { return x + y; };
+        int lane = threadIdx.x & 63, rank = static_cast<int>(at);
+        at = stop;
+        u.begin = 0;
+        u.end = INT_MAX;
+        u.number = u.row_tile = u.unit0 = 0;
+        u.units = 1;
+        if (p.count == 1) {  // (1 us less)
+            u.b = 0;
+            u.first = offset_of(p, 0);
+            u.n = max(offset_of(p, 1) - u.first, 0);
+            u.length = max(p.lengths[0], 0);
+            u.tile = static_cast<int>((static_cast<int64_t>(u.n) * a.group + ROWS - 1) / ROWS) - 1 - rank;
+            return u.tile >= 0;
+        }
+        for (int b0 = 0; b0 < p.count; b0 += 64 * kSets) {
+            int first[kSets], n[kSets], length[kSets], tiles[kSets], lowest[kSets], all = 0, end = 0, below = 0;
+            constexpr int kHighest = 1 << 29;
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) {
+                const int b = b0 + 64 * k + lane;
+                first[k] = n[k] = length[k] = 0;
+                if (b < p.count) {
+                    first[k] = offset_of(p, b);
+                    n[k] = max(offset_of(p, b + 1) - first[k], 0);
+                    length[k] = max(p.lengths[b], 0);  // (without tokens nothing is seen)
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) {
+                tiles[k] = static_cast<int>((static_cast<int64_t>(n[k]) * a.group + ROWS - 1) / ROWS);
+                const int64_t context = static_cast<int64_t>(max(length[k] - n[k], 0)) * a.group / ROWS;
+                lowest[k] = static_cast<int>(min(context, int64_t{kHighest}));
+                all += tiles[k];
+                if (tiles[k]) {
+                    end = max(end, lowest[k] + tiles[k]);
+                    below = max(below, kHighest - lowest[k]);
+                }
+            }
+            all = reduced(all, sum);
+            if (rank >= all) {
+                rank -= all;
+                continue;
+            }
+            const auto larger = [](int x, int y) { return max(x, y); };
+            int low = kHighest - reduced(below, larger), high = reduced(end, larger), above = 0;
+            while (high - low > 1) {
+                const int middle = (low + high) >> 1;
+                int more = 0;
+#pragma unroll
+                for (int k = 0; k < kSets; ++k) more += min(max(lowest[k] + tiles[k] - middle, 0), tiles[k]);
+                more = reduced(more, sum);
+                if (more > rank) {
+                    low = middle;
+                } else {
+                    high = middle;
+                    above = more;
+                }
+            }
+            int index = rank - above;  // among those of the level
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) {
+                uint64_t level = __ballot(lowest[k] <= low && low < lowest[k] + tiles[k]);
+                if (index < __popcll(level)) {
+                    for (; index > 0; --index) level &= level - 1;
+                    const int l = __builtin_ctzll(level);
+                    u.b = b0 + 64 * k + l;
+                    u.first = __builtin_amdgcn_readlane(first[k], l);
+                    u.n = __builtin_amdgcn_readlane(n[k], l);
+                    u.length = __builtin_amdgcn_readlane(length[k], l);
+                    u.tile = low - __builtin_amdgcn_readlane(lowest[k], l);
+                    return true;
+                }
+                index -= __popcll(level);
+            }
+            return false;  // (offsets out of order, more tiles than a word counts)
+        }
+        return false;
+    }
     // The piece's next unit; false behind its last.  Every lane has the same.
     __device__ bool next(Unit &u) {
+        if (!a.target) return most_keys_first(u);
         if (at >= stop) return false;
         if constexpr (!kKeep) {
             kept = S(a, 0, 0, 0);
@@ -477,16 +579,6 @@ struct Piece {
         u.n = __builtin_amdgcn_readlane(kept.n, l);
         u.length = __builtin_amdgcn_readlane(kept.length, l);
         const int64_t rest = at - uniform(__shfl(kept.line_sum - kept.line, l));
-        if (!a.target) {
-            u.tile = static_cast<int>(rest);
-            u.begin = 0;
-            u.end = INT_MAX;
-            u.number = u.row_tile = at;
-            u.unit0 = static_cast<int>(at);
-            u.units = 1;
-            at += 1;
-            return true;
-        }
         const int keys = __builtin_amdgcn_readlane(kept.key_tiles, l);
         u.tile = rest < keys ? 0 : static_cast<int>(uniform(quotient(rest, keys)));
         u.begin = static_cast<int>(rest - static_cast<int64_t>(u.tile) * keys);
@@ -594,9 +686,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
     uint8_t *const marks = lds + 4 * S::kBytes;
     int *const flag = reinterpret_cast<int *>(marks + S::kMarks);
     const int head = blockIdx.x % a.p.kv_heads;
-    // the last tiles of a prompt have the most keys: they go first
-    const int64_t w0 = blockIdx.x / a.p.kv_heads;
-    Piece<kTileRows, KT, false> piece(a, a.target ? w0 : a.units - 1 - w0);
+    Piece<kTileRows, KT, false> piece(a, blockIdx.x / a.p.kv_heads);
     for (Unit u; piece.next(u); __syncthreads()) {
         int thread = threadIdx.x;
         asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)

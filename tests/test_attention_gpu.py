@@ -437,3 +437,18 @@ def test_what_is_not_seen_by_many_tiles_of_few_rows(kind):
     assert np.isnan(got[see][:, 4:, 77]).all()
     keep = np.arange(128) != 77
     assert np.array_equal(got[see][:, :, keep], clean[see][:, :, keep])
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_as_many_tiles_as_workgroups(kind):
+    """Every workgroup takes one row tile, the most keys first: sequences of one length, of every length, without
+    new tokens and without a context, more than are looked through at once."""
+    rng = rng_of(48, TYPES.index(kind))
+    for B in (65, 300):
+        for n, longest in ((1, 400), (3, 1)):
+            sizes = [(int(c), int(rng.integers(0, n + 1))) for c in rng.integers(0, longest // 2 + 1, B)]
+            check(Paged(rng, sizes, 8, 32, 16, kind, extra_rows=1), rng, 16)
+    check(Paged(rng, [(70, 2)] * 150, 8, 16, 16, kind), rng, 8)
+    check(Paged(rng, [(0, 900), (300, 0), (0, 0), (17, 500)], 8, 16, 16, kind), rng, 32)
+    check(Paged(rng, [(int(c), 20) for c in rng.integers(0, 90, 130)], 8, 16, 16, kind), rng, 64)
+    check(Paged(rng, [(5, 1000)], 8, 16, 16, kind), rng, 32)
