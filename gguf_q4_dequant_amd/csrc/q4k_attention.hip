@@ -419,6 +419,7 @@ struct Span {
 // compiler's four divisions of 64 bits took 2 us of a workgroup's start).  The
 // double is off by one where the quotient is below 2^52, and the remainder says so.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    asm volatile("" : "+v"(b));  // (its double is not kept over the products)
     int64_t q = static_cast<int64_t>(static_cast<double>(a) * __builtin_amdgcn_rcp(static_cast<double>(b)));
     int64_t rest = a - q * b;
     while (rest < 0 || rest >= b) {
@@ -595,10 +596,10 @@ struct Piece {
     }
 };
 
-// A lane's row: its query, its place in the outputs and what it sees.
+// A lane's row: its query, its place in the outputs and what it sees (rows behind the
+// last see anything).
 struct Row {
-    bool real;
-    int64_t at;  // element of q and out
+    int64_t at;  // element of q and out; -1: no row
     int stop;    // causal: the keys below it are seen; tree: the length
     const unsigned *mask;
 };
@@ -606,10 +607,10 @@ struct Row {
 __device__ __forceinline__ Row row_of(const Attend &a, const Unit &u, int r, int head) {
     Row w;
     const int i = r / a.group, g = r - i * a.group;
-    w.real = i < u.n;
-    const int64_t t = static_cast<int64_t>(u.first) + (w.real ? i : 0);
-    w.at = (t * a.q_heads + head * a.group + (w.real ? g : 0)) * a.p.head_dim;
-    w.stop = a.mask || !w.real ? u.length : u.length - u.n + i + 1;
+    const bool real = i < u.n;
+    const int64_t t = static_cast<int64_t>(u.first) + (real ? i : 0);
+    w.at = real ? (t * a.q_heads + head * a.group + g) * a.p.head_dim : -1;
+    w.stop = a.mask || !real ? u.length : u.length - u.n + i + 1;
     w.mask = a.mask ? a.mask + t * a.words : nullptr;
     return w;
 }
@@ -632,7 +633,7 @@ __device__ __forceinline__ uint64_t seen(const Attend &a, const Row &w, int befo
     const uint64_t low = word[0] | word[1] << 32;
     const int s = static_cast<int>(from & 31);
     const uint64_t bits = from < 0 ? low << -from | ((1ull << -from) - 1) : s ? low >> s | word[2] << (64 - s) : low;
-    return w.real ? bits : below;
+    return bits;
 }
 
 // The query's power of two: |x| * 2^e of the largest is in [2^13, 2^14).
@@ -644,7 +645,7 @@ __device__ __forceinline__ int exponent_for(float largest) {
 // Eight values of the query from dimension d on.
 __device__ __forceinline__ void load_query(const Attend &a, const Row &w, int d, float *x) {
     f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
-    if (w.real && d < a.p.head_dim) {
+    if (w.at >= 0 && d < a.p.head_dim) {
         x0 = *reinterpret_cast<const f32x4 *>(a.q + w.at + d);
         x1 = *reinterpret_cast<const f32x4 *>(a.q + w.at + d + 4);
     }
@@ -674,10 +675,12 @@ struct TileShape {
     static constexpr int kMarks = KT * DP / 8;        // a bit per value
     static constexpr int kThird = kType == Q4K_KV_BF16 ? kTileRows * DP * 2 : 0;  // the queries' third parts
     static constexpr int kLds = 4 * kBytes + kMarks + 16 + kThird;
+    // Workgroups, as the registers allow (64 dimensions, two: seven prompts up to 1531 tokens 94 -> 103 us).
+    static constexpr int kPerCu = DP == 64 ? 3 : DP == 128 ? 2 : 1;
 };
 
 template <int kType, int DP>
-__global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Attend a) {
+__global__ __launch_bounds__(256, (TileShape<kType, DP>::kPerCu)) void attend_tiles(const Attend a) {
     typedef TileShape<kType, DP> S;
     typedef Math<kType> M;
     typedef typename M::v8 v8;
@@ -909,7 +912,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void attend_tiles(const Att
         int r0 = row0 + wave * 32 + col, D = a.p.head_dim;
         asm volatile("" : "+v"(r0), "+s"(D));  // worked out again rather than kept over the loops
         const Row o = row_of(a, u, r0, head);
-        if (!o.real) continue;
+        if (o.at < 0) continue;
         float *to = a.out + o.at;
         float f = sum == 0.f ? 0.f : a.p.v_scale / sum;
         if (u.units > 1) {
@@ -1519,7 +1522,8 @@ int launch_shape(Attend &a, hipStream_t stream) {
     if constexpr (DP <= (kBf16 ? 64 : 128))
         if (rows <= 64) return launch_few<kType, DP, 4>(a, stream);
     typedef TileShape<kType, DP> S;
-    return launch<kTileRows, S::KT, false>(a, attend_tiles<kType, DP>, 256, S::kLds, S::kLds > 81920 ? 1 : 2, 4, stream);
+    // (split for two a CU at most: with three, 64 row tiles a key head are split too, 59 -> 96 us)
+    return launch<kTileRows, S::KT, false>(a, attend_tiles<kType, DP>, 256, S::kLds, S::kPerCu < 2 ? 1 : 2, 4, stream);
 }
 
 template <int kType>
