@@ -914,7 +914,8 @@ __global__ __launch_bounds__(256, (TileShape<kType, DP>::kPerCu)) void attend_ti
         const Row o = row_of(a, u, r0, head);
         if (o.at < 0) continue;
         float *to = a.out + o.at;
-        float f = sum == 0.f ? 0.f : a.p.v_scale / sum;
+        // (v_scale / sum could be a subnormal number or infinite where the output is neither)
+        float f = sum == 0.f ? 0.f : 1.f / sum, v_scale = a.p.v_scale;
         if (u.units > 1) {
             if (u.number >= a.units) continue;  // (offsets out of order)
             const int64_t at = (u.number * a.p.kv_heads + head) * kTileRows + wave * 32 + col;
@@ -924,7 +925,7 @@ __global__ __launch_bounds__(256, (TileShape<kType, DP>::kPerCu)) void attend_ti
             }
             if (m == -INFINITY && sum == 0.f) continue;  // the output is not read
             to = a.part + at * D;
-            f = 1.f;
+            f = v_scale = 1.f;
         }
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -934,7 +935,7 @@ __global__ __launch_bounds__(256, (TileShape<kType, DP>::kPerCu)) void attend_ti
                 if (at < D) {
                     f32x4 y;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = f == 0.f ? 0.f : acc[d][r + i] * f;
+                    for (int i = 0; i < 4; ++i) y[i] = f == 0.f ? 0.f : acc[d][r + i] * f * v_scale;
                     *reinterpret_cast<f32x4 *>(to + at) = y;
                 }
             }
@@ -1281,9 +1282,8 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (F
                 y += *reinterpret_cast<const f32x4 *>(from + d) * f;
             }
             if (u.units == 1) {
-                const float f = a.p.v_scale / total;
                 if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
-                else y *= f;
+                else y = y * (1.f / total) * a.p.v_scale;
                 *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
             } else if (shared) {
                 const int64_t at = (u.number * a.p.kv_heads + head) * kRows + r;
@@ -1342,9 +1342,8 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (F
                     }
                 }
             }
-            const float f = a.p.v_scale / total;
             if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
-            else y *= f;
+            else y = y * (1.f / total) * a.p.v_scale;
             *reinterpret_cast<f32x4 *>(a.out + at_of(r) + d) = y;
         }
     }
@@ -1436,9 +1435,8 @@ __global__ __launch_bounds__(256) void join_units(const Attend a) {
     }
     if (!here || tid >= quads) return;
     for (int k = 1; k < streams; ++k) y += sums[mine * kThreads + k * quads + tid];
-    const float f = p.v_scale / total;
     if (total == 0.f) y = f32x4{0.f, 0.f, 0.f, 0.f};
-    else y *= f;
+    else y = y * (1.f / total) * p.v_scale;
     *reinterpret_cast<f32x4 *>(a.out + id * D + tid * 4) = y;
 }
 
