@@ -75,8 +75,7 @@ struct Attend {
 __device__ const __align__(16) uint8_t kZeros[16] = {};
 
 constexpr int kCus = 256;
-constexpr float kBias = 13.f;  // weights are 2^(s - max + 13): binary16's subnormal numbers begin 2^-27 below the largest
-constexpr float kSlack = 2.75f;  // a row's maximum may be this much above the one in use: weights stay below 2^15.75
+constexpr float kSlack = 2.75f;  // a row's maximum may be this much above the one in use
 constexpr float kLog2e = 1.4426950408889634f;
 
 // x less the lower or upper half of h, exactly: the instruction reads binary16 halves as
@@ -93,10 +92,16 @@ __device__ __forceinline__ float less_high(float x, half2v h) {
 }
 
 // Float32 values in parts of 16 bits: two of binary16 (22 bits), three of bfloat16 (24).
+// Weights are 2^(s - max + kBias).  Binary16: 13, its subnormal numbers begin 2^-27 below the
+// largest weight, and with kSlack weights stay below 2^15.75.  Bfloat16 has float32's range and
+// values up to 2^128: with -13 the sum of 2^(13 - kSlack) = 1217 weights is at most 1, so that
+// sums of weights times values stay finite (the exponential's argument then rounds a little
+// more coarsely: errors of 32 tokens behind 4000 6.2e-7 -> 7.4e-7 of the result).
 template <int kType>
 struct Math {  // binary16 (e4m3 widened to it)
     typedef half8v v8;
     static constexpr int kParts = 2;
+    static constexpr float kBias = 13.f;
     static constexpr bool kScaled = true;
     __device__ static f32x16 mfma32(v8 a, v8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
     __device__ static f32x4 mfma16(v8 a, v8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
@@ -116,6 +121,7 @@ template <>
 struct Math<Q4K_KV_BF16> {
     typedef bf8v v8;
     static constexpr int kParts = 3;
+    static constexpr float kBias = -13.f;
     static constexpr bool kScaled = false;
     __device__ static f32x16 mfma32(v8 a, v8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
     __device__ static f32x4 mfma16(v8 a, v8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -856,7 +862,7 @@ __global__ __launch_bounds__(256, (TileShape<kType, DP>::kPerCu)) void attend_ti
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[d][r] *= fade;
             }
-            const float shift = kBias - (m == -INFINITY ? 0.f : m);
+            const float shift = M::kBias - (m == -INFINITY ? 0.f : m);
             float part = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
@@ -1185,7 +1191,7 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (F
                 const float zero = m1 == -INFINITY ? 0.f : m1;
                 fade[n] = __builtin_amdgcn_exp2f(m[n] - zero);
                 m[n] = m1;
-                const float shift = kBias - zero;
+                const float shift = M::kBias - zero;
                 float x[8], part = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

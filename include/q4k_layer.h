@@ -143,7 +143,9 @@ int q4k_kv_append(const float *q, const float *k, const float *v, const q4k_kv_c
  *   largest is dropped; products, maxima, sums and outputs are float32.
  *   What a token does not see never reaches its row, NaN and infinities
  *   included (keys and values behind a sequence's end may hold anything).  A
- *   NaN or infinity that it sees gives NaN or infinities there.
+ *   NaN or infinity that it sees gives NaN or infinities there.  So may, over a
+ *   bfloat16 cache, finite values above 2^138 / (keys that the row sees): 2^121
+ *   with 131072 keys; up to 1024 keys every finite value is kept.
  *   Results do not depend on the order in which workgroups finish.
  *   Errors: as for q4k_kv_append, and Q4K_ERR_ALLOC; Q4K_ERR_LAUNCH also for more
  *   than 2^24 row tiles. */

@@ -22,6 +22,24 @@ def run(p, q, scale):
 
 
 @pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("name", SIZES)
+def test_values_near_the_types_largest(name, kind):
+    """Values of the type's largest size, of one sign in half of the dimensions: the weighted sums in front of
+    the division are as large as they get."""
+    import torch
+    rng = rng_of(80, list(SIZES).index(name), TYPES.index(kind))
+    p = Paged(rng, SIZES[name], 2, 64, 16, kind, extra_cols=400)
+    largest = torch.finfo(p.v.dtype).max
+    sign = torch.from_numpy(np.sign(rng.standard_normal(p.v.shape)))
+    sign[..., ::2] = 1
+    p.v = torch.where(p.v.double().isfinite(), sign * largest, p.v.double()).to(p.v.dtype)
+    q = rng.standard_normal((p.T, 8, 64)).astype(np.float32)
+    got, want, tol = run(p, q, 0.125)
+    assert np.isfinite(got).all()
+    assert (np.abs(got.astype(np.float64) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("v_scale", [2.0 ** -120, 2.0 ** 120])
 @pytest.mark.parametrize("name", SIZES)
 def test_scales_near_float32s_ends(name, v_scale, kind):
