@@ -12,6 +12,7 @@
 #include <math.h>
 
 #include "q4k_cache.h"
+#include "q4k_factor.h"
 
 namespace q4k {
 
@@ -160,16 +161,16 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const Append a) {
         }
         const float *norm = what == 0 ? a.q_norm : what == 1 ? a.k_norm : nullptr;
         if (norm) {
-            float sum = 0.f;
+            double sum = 0.;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+            for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
             for (int o = spread / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-            const float f = 1.f / sqrtf(sum / static_cast<float>(D) + a.eps);
+            const Factor f(sum / D, a.eps);
             if (here) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[i] *= f * norm[d0 + i];
-                    x[4 + i] *= f * norm[d1 + i];
+                    x[i] = f.times(x[i]) * norm[d0 + i];
+                    x[4 + i] = f.times(x[4 + i]) * norm[d1 + i];
                 }
             }
         }

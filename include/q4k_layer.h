@@ -113,6 +113,7 @@ int q4k_rms_norm(const float *x, const float *residual, const float *weight, flo
  * and rounded; q_out is q normed (q_norm) and rotated.
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  * Angles are reduced in double (a position of 2^31 - 1 loses nothing), the
+ * norms' sums of squares are held in double (heads of every float32 size), the
  * rest is float32 with one rounding to the cache's type: to the nearest, ties
  * to even; e4m3 saturates at +-448 (infinities too), NaN stays NaN.
  *   q: DEVICE float32 [T, q_heads, head_dim] or NULL (then q_out is NULL
