@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "../../include/q4k_layer.h"
+#include "q4k_factor.h"
 #include "q4k_internal.h"
 
 namespace q4k {
@@ -78,11 +79,13 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const float *x, cons
 #pragma unroll
         for (int w = 0; w < kThreads / 64; ++w) sum += sums[w];
     }
-    const float f = static_cast<float>(1. / sqrt(sum / N + static_cast<double>(eps)));
+    const Factor f(sum / N, eps);
     const auto finish = [&](int i, float4u v) {
         if (tr) store4(tr, i, N, v);
         const float4u w = load4(weight, i, N);
-        store4(yr, i, N, v * f * w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = f.times(v[k]);
+        store4(yr, i, N, v * w);
     };
 #pragma unroll
     for (int j = 0; j < kHold; ++j)

@@ -11,6 +11,20 @@ pytestmark = pytest.mark.gpu
 SIZES = [2.0 ** -140, 1e-38, 1e-30, 1e-20, 1e-10, 1.0, 1e10, 1e20, 1e30, 1e37]
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("N", [5, 300, 5000])
+def test_norm_of_rows_of_every_size(N, eps):
+    """The factor is beyond float32 for rows below 2^-128, and loses bits for rows above 2^126."""
+    rng = rng_of(90, N, int(eps > 0))
+    x = (rng.standard_normal((len(SIZES), N)) * np.array(SIZES)[:, None]).astype(np.float32)
+    w = (0.5 + rng.random(N)).astype(np.float32)
+    t = x.astype(np.float64)
+    want = t / np.sqrt((t * t).mean(1, keepdims=True) + eps) * w
+    got = q4k.rms_norm(to_dev(x), to_dev(w), eps).cpu().numpy()
+    # the factor and two products rounded, each by 2^-24, or by half of the least subnormal number (times a weight of up to 1.5)
+    assert (np.abs(got - want) <= 4 * 2.0 ** -24 * np.abs(want) + 2.0 ** -148).all()
+
+
 @pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "interleaved"])
 @pytest.mark.parametrize("D", [16, 80, 128, 256])
 @pytest.mark.parametrize("eps", [0.0, 1e-6])
