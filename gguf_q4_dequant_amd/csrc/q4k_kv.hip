@@ -75,15 +75,18 @@ struct Append {
     int parts;  // waves that share a token's heads
 };
 
-// cos and sin of position * f.  The product is exact to 53 bits, and turns are
-// taken from it with 1 / (2 pi) in two parts, so that what is left of it, in
-// [-1/2, 1/2] turns, is good to 2^-52 of the product's size in turns (at most
-// 1e-7 of a turn for the largest position and f = 1).
+// cos and sin of position * f.  The product has up to 55 bits and is taken in two
+// parts, exactly; turns are taken from it with 1 / (2 pi) in two parts, so that what
+// is left of it, in [-1/2, 1/2] turns, is good to 2^-100 of the product's size in
+// turns before it is rounded to float32.  (No contraction: hi - rint(hi) would become
+// a fused product that has hi's rounding in it, which lo holds too.)
 __device__ __forceinline__ void turned(int position, float f, float &c, float &s) {
-    constexpr double kHi = 0.15915494309189535, kLo = -9.839338333591243e-18;  // 1 / (2 pi)
+#pragma clang fp contract(off)
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
     const double a = static_cast<double>(position) * static_cast<double>(f);
     const double hi = a * kHi;
-    const double lo = fma(a, kLo, fma(a, kHi, -hi));
+    const double rest = fma(static_cast<double>(position), static_cast<double>(f), -a);
+    const double lo = fma(rest, kHi, fma(a, kLo, fma(a, kHi, -hi)));
     const float r = static_cast<float>((hi - rint(hi)) + lo);
     sincospif(2.f * r, &s, &c);
 }
