@@ -33,7 +33,9 @@ int check_paged(const q4k_kv_cache *cache, const q4k_sequences *sequences, int T
     if (static_cast<int64_t>(s.max_pages) * c.page_size > (1 << 30)) return Q4K_ERR_BAD_DIM;
     if (static_cast<int64_t>(T) * c.kv_heads > (1 << 30) || static_cast<int64_t>(T) * q_heads > (1 << 30)) return Q4K_ERR_BAD_DIM;
     if (q_heads % c.kv_heads != 0) return Q4K_ERR_BAD_DIM;
-    if (!(c.k_scale > 0.f) || !(c.v_scale > 0.f) || isinf(c.k_scale) || isinf(c.v_scale)) return Q4K_ERR_BAD_DIM;
+    // (the append multiplies by the reciprocals)
+    for (const float scale : {c.k_scale, c.v_scale})
+        if (!(scale > 0.f) || isinf(scale) || isinf(1.f / scale)) return Q4K_ERR_BAD_DIM;
     if (T == 0 || s.count == 0) return Q4K_OK;
     if (((!c.k || !c.v) && c.pages > 0) || !s.offsets || !s.lengths || (!s.pages && s.max_pages > 0)) return Q4K_ERR_NULL;
     if (misaligned16(c.k) || misaligned16(c.v) || misaligned4(s.offsets) || misaligned4(s.lengths) || misaligned4(s.pages))

@@ -71,7 +71,7 @@ typedef struct q4k_kv_cache {
     int kv_heads;  /* 1 .. 1024 */
     int page_size; /* a power of two, 1 .. 65536 */
     int head_dim;  /* a multiple of 16, 16 .. 256 */
-    float k_scale; /* positive and finite; 1 keeps the values as they are */
+    float k_scale; /* positive and finite, and so is 1 / k_scale (above 2^-128); 1 keeps the values as they are */
     float v_scale;
 } q4k_kv_cache;
 
@@ -123,7 +123,8 @@ int q4k_rms_norm(const float *x, const float *residual, const float *weight, flo
  *   A token without a place in the cache still has its q_out.
  *   Errors: a negative or unsupported size (the structs', T * q_heads or
  *   T * kv_heads above 2^30, q_heads not a positive multiple of kv_heads
- *   where q is given), a scale that is not positive and finite:
+ *   where q is given), a scale that is not positive and finite or whose
+ *   reciprocal is not:
  *   Q4K_ERR_BAD_DIM; a NULL array or struct (the optional ones excepted):
  *   Q4K_ERR_NULL; Q4K_ERR_ALIGN; more than 2^26 tokens: Q4K_ERR_LAUNCH. */
 int q4k_kv_append(const float *q, const float *k, const float *v, const q4k_kv_cache *cache,
