@@ -73,7 +73,7 @@ struct Append {
     float eps;
     float k_factor, v_factor;  // 1 / scale
     int rotary;
-    int q_heads;
+    int q_heads;  // 0: no queries
     int parts;  // waves that share a token's heads
 };
 
@@ -146,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const Append a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) turned(position, a.inv_freq[4 * e + i], c[i], s[i]);
     }
-    const int q_heads = a.q ? a.q_heads : 0, heads = q_heads + 2 * p.kv_heads;
+    const int q_heads = a.q_heads, heads = q_heads + 2 * p.kv_heads;
     for (int g = part; g * together < heads; g += a.parts) {
         const int head = g * together + lane / spread;
         if (head >= heads) continue;
@@ -225,6 +225,7 @@ extern "C" int q4k_kv_append(const float *q, const float *k, const float *v, con
     using namespace q4k;
     Append a = {};
     if (q && q_heads < 1) return Q4K_ERR_BAD_DIM;
+    if (!q) q_heads = 0;  // (not looked at)
     int rc = check_paged(cache, sequences, T, q_heads, &a.p);
     if (rc != Q4K_OK) return rc;
     if (rotation) {
@@ -261,7 +262,7 @@ extern "C" int q4k_kv_append(const float *q, const float *k, const float *v, con
     // tokens; 8192 in all keep the memory busy (5200 tokens of 32 + 16 heads of 128 values:
     // 63 us with one wave a token, 57 with two), more only take the angles more often.
     const int spread = lanes_of(cache->head_dim);
-    const int passes = ((q ? q_heads : 0) + 2 * cache->kv_heads + 64 / spread - 1) / (64 / spread);
+    const int passes = (q_heads + 2 * cache->kv_heads + 64 / spread - 1) / (64 / spread);
     const int64_t parts = (8192 + static_cast<int64_t>(T) - 1) / T;
     a.parts = static_cast<int>(parts < passes ? parts : passes);
     if (static_cast<int64_t>(T) * a.parts * 64 + kThreads > UINT32_MAX) return Q4K_ERR_LAUNCH;

@@ -25,3 +25,14 @@ def test_scales_whose_reciprocal_is_infinite(lib, what, name):
         assert call(c=cache(**{name: scale})) == q4k.ERR_BAD_DIM, scale
     for scale in (np.nextafter(np.float32(2.0 ** -128), np.float32(1)), 2.0 ** -127, 2.0 ** -126, float(np.finfo(np.float32).max)):
         assert call(T=0, c=cache(**{name: float(scale)})) == q4k.OK, scale
+
+
+def test_heads_of_queries_that_are_not_given(lib):
+    """q_heads is looked at where q is given, and only there."""
+    call = make(lib, "append")
+    for heads in (0, 1, 3, 5, -1, 1 << 29):
+        assert call(q=None, q_out=None, k=None, T=4, q_heads=heads) == q4k.ERR_NULL, heads  # (of k)
+        assert call(q=None, q_out=None, T=0, q_heads=heads) == q4k.OK, heads
+    for heads in (0, 1, 3, 5, -1, 1 << 29):
+        assert call(k=None, T=4, q_heads=heads) == q4k.ERR_BAD_DIM, heads
+    assert call(k=None, T=4, q_heads=4) == q4k.ERR_NULL
