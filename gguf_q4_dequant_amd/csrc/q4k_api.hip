@@ -141,31 +141,63 @@ hipError_t workspace(hipStream_t stream, size_t bytes, float **scratch_out, int 
 }
 
 namespace {
-constexpr int kCounterSlot = -1;  // beside the workspace's slots
+// Of a (device, stream): four sets of kCounters words, two for eager calls and two for
+// captured ones.
+struct CounterSets {
+    uint32_t *words = nullptr;
+    unsigned turn[2] = {0, 0};
+    unsigned long long capture = 0;  // the last capture's number
+    bool captured = false;           // there has been one
+};
+std::map<std::pair<int, uintptr_t>, CounterSets> g_counters;  // under g_ws_mutex
+
 __global__ __launch_bounds__(256) void clear_words(uint32_t *words) { words[blockIdx.x * 256 + threadIdx.x] = 0; }
+hipError_t clear_sets(uint32_t *words, int sets, hipStream_t stream) {
+    static_assert(kCounters % 256 == 0, "whole workgroups");
+    hipLaunchKernelGGL(clear_words, dim3(sets * (kCounters / 256)), dim3(256), 0, stream, words);
+    return hipGetLastError();
+}
 }  // namespace
 
-hipError_t counters(hipStream_t stream, uint32_t **words) {
-    static_assert(kCounters % 256 == 0, "whole workgroups");
-    *words = nullptr;
+// Calls take two sets in turn and clear the one that the next call has, so that a call that
+// was disturbed spoils no later one.  Eager calls run one after another; a graph's calls do
+// too, but graphs that were captured on one stream may be replayed anywhere and at once, so
+// that theirs are other sets, and the first call of a capture clears its own with a launch in
+// front (1.5 us a replay).
+hipError_t counters(hipStream_t stream, uint32_t **words, uint32_t **next) {
+    *words = *next = nullptr;
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess) return err;
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    unsigned long long capture = 0;
+    err = hipStreamGetCaptureInfo(stream, &status, &capture);
+    if (err != hipSuccess) return err;
+    const bool captured = status != hipStreamCaptureStatusNone;
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Buffer &b = g_ws[std::make_pair(std::make_pair(dev, reinterpret_cast<uintptr_t>(stream)), kCounterSlot)];
-    if (!b.ptr) {
-        Buffer fresh;
-        err = grow(fresh, kCounters * sizeof(uint32_t));
+    CounterSets &c = g_counters[std::make_pair(dev, reinterpret_cast<uintptr_t>(stream))];
+    if (!c.words) {
+        // (what zeroes them would only be recorded)
+        if (captured) return hipErrorStreamCaptureUnsupported;
+        void *p = nullptr;
+        err = hipMalloc(&p, 4 * kCounters * sizeof(uint32_t));
         if (err != hipSuccess) return err;
-        hipLaunchKernelGGL(clear_words, dim3(kCounters / 256), dim3(256), 0, stream, static_cast<uint32_t *>(fresh.ptr));
-        err = hipGetLastError();
+        err = clear_sets(static_cast<uint32_t *>(p), 4, stream);
         if (err != hipSuccess) {
-            (void)hipFree(fresh.ptr);
+            (void)hipFree(p);
             return err;
         }
-        b = fresh;
+        c.words = static_cast<uint32_t *>(p);
     }
-    *words = static_cast<uint32_t *>(b.ptr);
+    uint32_t *const pair = c.words + (captured ? 2 * kCounters : 0);
+    const unsigned turn = c.turn[captured]++ & 1;
+    *words = pair + turn * kCounters;
+    *next = pair + (turn ^ 1) * kCounters;
+    if (captured && !(c.captured && c.capture == capture)) {
+        c.captured = true;
+        c.capture = capture;
+        return clear_sets(*words, 1, stream);
+    }
     return hipSuccess;
 }
 

@@ -62,6 +62,7 @@ struct Attend {
     float *part_ml;        // ... and their maxima and sums, [units * kv_heads][rows][2]
     Part *plan;            // split, many rows: [slots], for the launch that joins them
     uint32_t *counters;    // split, few rows: the units of a row tile that have ended
+    uint32_t *next;        // split, few rows: counters to be cleared for the next call
     int64_t slots;
     int words;
     int q_heads;
@@ -75,6 +76,7 @@ struct Attend {
 __device__ const __align__(16) uint8_t kZeros[16] = {};
 
 constexpr int kCus = 256;
+static_assert(kCounters >= 2 * kCus, "a counter for every row tile that is joined in its launch");
 constexpr float kSlack = 2.75f;  // a row's maximum may be this much above the one in use
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -1005,6 +1007,9 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (F
     constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16, kRows = S::kRows;
     extern __shared__ __align__(16) uint8_t lds[];
     int *const ended = reinterpret_cast<int *>(lds + S::kEnded);
+    if (S::kJoined && a.target && blockIdx.x == 0)
+        for (int i = threadIdx.x; i < kCounters; i += S::kWaves * 64)
+            __hip_atomic_store(a.next + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int head = blockIdx.x % a.p.kv_heads;
     Piece<kRows, KT, true> piece(a, blockIdx.x / a.p.kv_heads);
     for (Unit u; piece.next(u); __syncthreads()) {
@@ -1474,7 +1479,8 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
         a.part = ws;
         a.part_ml = ws + rows * a.p.head_dim;
         a.plan = reinterpret_cast<Part *>(a.part_ml + 2 * rows);
-        if (kJoined && counters(stream, &a.counters) != hipSuccess) return Q4K_ERR_ALLOC;
+        // (row tiles of all key heads: below target * heads less heads, so below kCus * per_cu)
+        if (kJoined && counters(stream, &a.counters, &a.next) != hipSuccess) return Q4K_ERR_ALLOC;
     }
     if (lds > 65536 && allow_dynamic_lds(reinterpret_cast<const void *>(kernel), lds) != hipSuccess) return Q4K_ERR_LAUNCH;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((target ? target : tiles) * heads)), dim3(threads), lds, stream, a);

@@ -132,10 +132,10 @@ hipError_t launch_partial_sums(const Batch &b, hipStream_t stream);
 hipError_t workspace(hipStream_t stream, size_t bytes, float **scratch, int slot = 0);
 
 // kCounters library-owned words per (device, stream), zero when a kernel that uses
-// them begins: made so when they are allocated, and every kernel that counts in
-// them leaves them zero.
-constexpr int kCounters = 4096;
-hipError_t counters(hipStream_t stream, uint32_t **words);
+// them begins.  The kernel leaves them zero, and clears those at *next, which the
+// stream's next call has.
+constexpr int kCounters = 512;
+hipError_t counters(hipStream_t stream, uint32_t **words, uint32_t **next);
 
 // Raise a kernel's dynamic-LDS limit to `bytes` on the current device, once
 // per (device, kernel); thread-safe.  Returns the first call's result.
