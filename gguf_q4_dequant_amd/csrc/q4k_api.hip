@@ -61,6 +61,15 @@ struct Buffer {
     size_t bytes = 0;
 };
 std::mutex g_ws_mutex;
+
+// What tells streams apart: the handle, and for hipStreamPerThread, one handle for a stream
+// of every thread, a number of the thread's own (odd, as no other handle is).
+uintptr_t stream_key(hipStream_t stream) {
+    if (stream != hipStreamPerThread) return reinterpret_cast<uintptr_t>(stream);
+    static std::atomic<uintptr_t> threads{0};
+    thread_local const uintptr_t key = 2 * threads++ + 1;
+    return key;
+}
 std::map<std::pair<std::pair<int, uintptr_t>, int>, Buffer> g_ws;
 // Buffers replaced by larger ones.  They are never freed: a HIP graph
 // captured while one was current keeps its address, and its replays must
@@ -133,7 +142,7 @@ hipError_t workspace(hipStream_t stream, size_t bytes, float **scratch_out, int 
         return hipSuccess;
     }
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Buffer &b = g_ws[std::make_pair(std::make_pair(dev, reinterpret_cast<uintptr_t>(stream)), slot)];
+    Buffer &b = g_ws[std::make_pair(std::make_pair(dev, stream_key(stream)), slot)];
     err = grow(b, bytes);
     if (err != hipSuccess) return err;
     *scratch_out = static_cast<float *>(b.ptr);
@@ -175,7 +184,7 @@ hipError_t counters(hipStream_t stream, uint32_t **words, uint32_t **next) {
     if (err != hipSuccess) return err;
     const bool captured = status != hipStreamCaptureStatusNone;
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    CounterSets &c = g_counters[std::make_pair(dev, reinterpret_cast<uintptr_t>(stream))];
+    CounterSets &c = g_counters[std::make_pair(dev, stream_key(stream))];
     if (!c.words) {
         // (what zeroes them would only be recorded)
         if (captured) return hipErrorStreamCaptureUnsupported;

@@ -31,7 +31,8 @@
  *     dimension, -3 failure while running the forward), extended with -4..-6.
  *   - Calls are thread-safe (the library's tables are guarded per device);
  *     calls on different streams may run concurrently.
- *   - Workspace: the library keeps device scratch memory per (device, stream)
+ *   - Workspace: the library keeps device scratch memory per (device, stream;
+ *     of hipStreamPerThread per thread)
  *     for split-K partial sums, the binary16 copy of x (prefill) and the
  *     staged activations of 5 <= M <= 16 calls.  It grows on demand with
  *     hipMalloc (no synchronization), so a call whose shape needs more than
