@@ -39,3 +39,14 @@ def check_close(y, y_ref, s, tol, what=""):
         raise AssertionError(f"{what}: {int((~ok).sum())} of {ok.size} outputs beyond {tol}*S; first {detail}")
     rel = err / np.where(s > 0, s, 1.0)
     return float(rel.max()) if rel.size else 0.0
+
+
+def fresh_stream():
+    """A stream that no call has used (torch hands out the same 32 in turn)."""
+    import ctypes
+
+    import torch
+    torch.cuda.init()
+    handle = ctypes.c_void_p()
+    assert ctypes.CDLL("libamdhip64.so").hipStreamCreate(ctypes.byref(handle)) == 0
+    return torch.cuda.ExternalStream(handle.value)

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import gguf_q4_dequant_amd as q4k
-from tests.gpu_helpers import to_dev
+from tests.gpu_helpers import fresh_stream, to_dev
 from tests.layer_reference import Paged, rng_of
 
 pytestmark = pytest.mark.gpu
@@ -31,7 +31,7 @@ def test_a_capture_needs_an_eager_call_first():
     import torch
     call = batch(0, [(900, 1), (40, 1)])
     want = q4k.attention(*call)
-    side = torch.cuda.Stream()
+    side = fresh_stream()
     torch.cuda.synchronize()
     x = torch.ones(8, device="cuda")
     g = torch.cuda.CUDAGraph()
