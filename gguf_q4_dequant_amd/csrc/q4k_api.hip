@@ -26,11 +26,20 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_ok[kMaxDevices];  // 0 unknown, 1 ok, -1 bad
 
+// err, which the caller reports: the runtime keeps it too, and the next call's launch
+// would be taken for the one that failed.
+hipError_t reported(hipError_t err) {
+    (void)hipGetLastError();
+    return err;
+}
+
 }  // namespace
 
 int check_device() {
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return Q4K_ERR_DEVICE;
+    const hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) (void)reported(err);
+    if (err != hipSuccess || dev < 0 || dev >= kMaxDevices) return Q4K_ERR_DEVICE;
     int st = g_device_ok[dev].load(std::memory_order_acquire);
     if (st == 0) {
         hipDeviceProp_t prop;
@@ -85,7 +94,7 @@ hipError_t grow(Buffer &b, size_t bytes) {
     want = (want + 0xFFFF) & ~static_cast<size_t>(0xFFFF);
     void *p = nullptr;
     const hipError_t err = hipMalloc(&p, want);
-    if (err != hipSuccess) return err;
+    if (err != hipSuccess) return reported(err);
     if (b.ptr) g_retired.push_back(b.ptr);
     b.ptr = p;
     b.bytes = want;
@@ -111,7 +120,7 @@ hipError_t scratch_address(int dev, void **ptr) {
     if (!g_scratch_ptr[dev]) {
         void *p = nullptr;
         const hipError_t err = hipGetSymbolAddress(&p, HIP_SYMBOL(scratch));
-        if (err != hipSuccess) return err;
+        if (err != hipSuccess) return reported(err);
         if (!p) return hipErrorInvalidSymbol;
         g_scratch_ptr[dev] = p;
     }
@@ -130,7 +139,7 @@ hipError_t workspace(hipStream_t stream, size_t bytes, float **scratch_out, int 
     if (bytes == 0) return hipSuccess;
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
-    if (err != hipSuccess) return err;
+    if (err != hipSuccess) return reported(err);
     if (t_noalloc) {
         // slot 0 only: the allocation-free entry runs the plain products
         if (slot != 0 || dev < 0 || dev >= kMaxDevices) return hipErrorInvalidValue;
@@ -177,11 +186,11 @@ hipError_t counters(hipStream_t stream, uint32_t **words, uint32_t **next) {
     *words = *next = nullptr;
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
-    if (err != hipSuccess) return err;
+    if (err != hipSuccess) return reported(err);
     hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
     unsigned long long capture = 0;
     err = hipStreamGetCaptureInfo(stream, &status, &capture);
-    if (err != hipSuccess) return err;
+    if (err != hipSuccess) return reported(err);
     const bool captured = status != hipStreamCaptureStatusNone;
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     CounterSets &c = g_counters[std::make_pair(dev, stream_key(stream))];
@@ -190,7 +199,7 @@ hipError_t counters(hipStream_t stream, uint32_t **words, uint32_t **next) {
         if (captured) return hipErrorStreamCaptureUnsupported;
         void *p = nullptr;
         err = hipMalloc(&p, 4 * kCounters * sizeof(uint32_t));
-        if (err != hipSuccess) return err;
+        if (err != hipSuccess) return reported(err);
         err = clear_sets(static_cast<uint32_t *>(p), 4, stream);
         if (err != hipSuccess) {
             (void)hipFree(p);
@@ -213,12 +222,13 @@ hipError_t counters(hipStream_t stream, uint32_t **words, uint32_t **next) {
 hipError_t allow_dynamic_lds(const void *kernel, int bytes) {
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
-    if (err != hipSuccess) return err;
+    if (err != hipSuccess) return reported(err);
     std::lock_guard<std::mutex> lock(g_attr_mutex);
     const auto key = std::make_pair(dev, kernel);
     const auto it = g_attr.find(key);
     if (it != g_attr.end()) return it->second;
     err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != hipSuccess) (void)reported(err);
     g_attr[key] = err;
     return err;
 }
