@@ -190,6 +190,13 @@ __device__ __forceinline__ void wait_lds() {
     __builtin_amdgcn_s_waitcnt(0xC07F);
     asm volatile("" ::: "memory");
 }
+// What lanes of this wave have put into LDS is there for its other lanes (which execute
+// in order; the compiler may otherwise move accesses that it finds to be apart).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 __device__ __forceinline__ void barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -340,6 +347,7 @@ __device__ __forceinline__ bool set_apart(uint8_t *v, int at, uint8_t *marks) {
         if (found) *reinterpret_cast<u32x4 *>(v + i) = w;
         any |= found;
     }
+    wave_sync();
     return __ballot(any != 0) != 0;
 }
 
@@ -1399,7 +1407,7 @@ __global__ __launch_bounds__(256) void join_units(const Attend a) {
     const auto place = [&](int c) { return (static_cast<int64_t>(part.unit0 + c) * p.kv_heads + head) * ROWS + r; };
     const auto sync = [&] {
         if (kThreads > 64) __syncthreads();
-        else __builtin_amdgcn_wave_barrier();
+        else wave_sync();
     };
     float top = -INFINITY;
     for (int c = tid; c < units; c += kThreads) top = fmaxf(top, a.part_ml[2 * place(c)]);
