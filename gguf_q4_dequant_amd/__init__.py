@@ -330,6 +330,19 @@ def _checked_tensor(name, t, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _check_apart(name, t, others, may_be=()):
+    """t, an output that the caller gave, shares no memory with the others (named tensors, None for those
+    that are not there); those in may_be it may be itself, but not overlap otherwise."""
+    at = t.data_ptr()
+    end = at + t.numel() * t.element_size()
+    for other, o in others.items():
+        if o is None:
+            continue
+        start = o.data_ptr()
+        if start < end and at < start + o.numel() * o.element_size() and not (other in may_be and start == at):
+            raise ValueError(f"{name} must not overlap {other}")
+
+
 def _stream_for(dev, stream) -> int:
     """The handle of the given stream, or of the current one; the tensors (on GPU
     number dev) have to be on the current device, whose context the library
@@ -619,7 +632,7 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, total=None, out=None, 
     """The root-mean-square norm y = t * rsqrt(mean(t^2) + eps) * weight of the rows
     of t = x + residual (q4k_rms_norm); x and residual float32 [M, N], weight
     float32 [N].  Returns y without a residual, and (y, t) with one; ``total``
-    (for t) and ``out`` (for y) may be x or residual."""
+    (for t) and ``out`` (for y) may be x or residual, each another (any other overlap is refused)."""
     import torch
     M, N, dev = _checked_rows("x", x, 2)
     shape = (M, N)
@@ -629,13 +642,16 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, total=None, out=None, 
         out = torch.empty_like(x) if stream is None else _new(x, shape, torch.float32, stream)
     else:
         _checked_tensor("out", out, torch.float32, shape, dev)
+        _check_apart("out", out, {"x": x, "residual": residual, "weight": weight}, ("x", "residual"))
     if total is None:
         if residual is not None:
             total = torch.empty_like(x) if stream is None else _new(x, shape, torch.float32, stream)
     else:
         _checked_tensor("total", total, torch.float32, shape, dev)
-        if total is out and M and N:
+        _check_apart("total", total, {"x": x, "residual": residual, "weight": weight}, ("x", "residual"))
+        if total.data_ptr() == out.data_ptr() and M and N:
             raise ValueError("total and out must be two tensors")
+        _check_apart("total", total, {"out": out})
     rc = library().q4k_rms_norm(x.data_ptr(), residual_ptr, weight_ptr, float(eps),
                                 None if total is None else total.data_ptr(), out.data_ptr(), M, N,
                                 _stream_for(dev, stream))
@@ -743,7 +759,8 @@ def kv_append(k, v, cache: KVCache, sequences: Sequences, rotation: Optional[Rot
     their places in the cache (q4k_kv_append): k under the norm ``k_norm`` (float32
     [head_dim], each head by itself) and the rotation, both rounded to the cache's
     type.  With ``q`` float32 [T, q_heads, head_dim] returns it under ``q_norm`` and
-    the rotation, in a new tensor or in ``q_out`` (which may be q).  positions int32
+    the rotation, in a new tensor or in ``q_out`` (which may be q, and overlaps
+    nothing else).  positions int32
     [T]: other positions than the tokens' indexes in their sequences (of drafted
     tokens that form a tree: their depths)."""
     import torch
@@ -761,6 +778,7 @@ def kv_append(k, v, cache: KVCache, sequences: Sequences, rotation: Optional[Rot
             q_out_ptr = q_out.data_ptr()
         else:
             q_out_ptr = _checked_tensor("q_out", q_out, torch.float32, (T, q_heads, D), dev)
+            _check_apart("q_out", q_out, {"q": q, "k": k, "v": v, "cache.k": cache[0], "cache.v": cache[1]}, ("q",))
     elif q_out is not None:
         raise ValueError("q_out needs a q")
     freq_ptr, rotary, pairs = None, 0, 0
@@ -790,6 +808,7 @@ def _attend(q, cache, sequences, mask, scale, out, stream):
         out_ptr = out.data_ptr()
     else:
         out_ptr = _checked_tensor("out", out, torch.float32, (T, q_heads, D), dev)
+        _check_apart("out", out, {"q": q, "cache.k": cache[0], "cache.v": cache[1], "mask": mask})
     scale = D ** -0.5 if scale is None else float(scale)
     if mask is None:
         rc = library().q4k_attention(q.data_ptr(), c, s, scale, out_ptr, T, q_heads, _stream_for(dev, stream))
@@ -812,7 +831,7 @@ def attention(q, cache: KVCache, sequences: Sequences, scale: Optional[float] = 
     (q4k_attention): q float32 [T, q_heads, head_dim], as kv_append gives it, query
     head h on key head h // (q_heads // kv_heads); whole prompts, chunks behind a
     context and single tokens, packed as ``sequences`` says.  ``scale`` is
-    head_dim ** -0.5 where none is given.  A token that sees nothing has a row of
+    head_dim ** -0.5 where none is given; ``out`` must not overlap q or the cache.  A token that sees nothing has a row of
     zeros; rows behind the last sequence are left as they were (in an ``out`` made
     here they hold nothing meaningful)."""
     return _attend(q, cache, sequences, None, scale, out, stream)

@@ -118,7 +118,7 @@ int q4k_rms_norm(const float *x, const float *residual, const float *weight, flo
  * rest is float32 with one rounding to the cache's type: to the nearest, ties
  * to even; e4m3 saturates at +-448 (infinities too), NaN stays NaN.
  *   q: DEVICE float32 [T, q_heads, head_dim] or NULL (then q_out is NULL
- *   too); q_out may be q itself.  k, v: DEVICE float32 [T, kv_heads,
+ *   too); q_out may be q itself (any other overlap is not allowed).  k, v: DEVICE float32 [T, kv_heads,
  *   head_dim].  16-byte aligned, the int arrays and weights 4-byte.
  *   rotation may be NULL: q_out is a copy of q, k is stored as it is.
  *   A token without a place in the cache still has its q_out.
