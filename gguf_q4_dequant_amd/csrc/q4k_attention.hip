@@ -458,6 +458,9 @@ __device__ __forceinline__ int reduced(int x, Op op) {
     return __builtin_amdgcn_readlane(x, 63);
 }
 
+// Sequences whose row tiles are ranked together.
+constexpr int sequences_at_once(int rows) { return rows < 128 ? 256 : 64; }
+
 // A workgroup's piece of the line.  kKeep: the 64 sequences last looked through stay
 // in registers; without it (where the products need them) they are looked through
 // again for every unit.
@@ -467,7 +470,7 @@ struct Piece {
     const Attend &a;
     S kept;
     int kept_b;
-    static constexpr int kSets = kKeep ? 4 : 1;  // of 64 sequences
+    static constexpr int kAtOnce = sequences_at_once(ROWS), kSets = kAtOnce / 64;
     int64_t at, stop, size, workgroup;
 
     __device__ Piece(const Attend &a_, int64_t w) : a(a_), kept(a_, 0, 0, 0), kept_b(0), workgroup(w) {
@@ -487,6 +490,16 @@ struct Piece {
         }
         at = w * size;
         stop = at + size;
+        // Of more sequences than are ranked together, those that a workgroup's rank falls to begin at the
+        // slot of their first tile (some slots have no tile).  (Going through the sets instead took 3000 us
+        // for one token of each of 8192 sequences over 16 keys, with this 1070; of 65535, 139700 and 8800.)
+        if (!a.target && a.p.count > kAtOnce) {
+            const auto start = [&](int s) { return slot_of<ROWS>(a, s * kAtOnce, offset_of(a.p, s * kAtOnce), 0); };
+            const int s = last_started((a.p.count + kAtOnce - 1) / kAtOnce, w, start);
+            kept_b = s * kAtOnce;
+            at = w - uniform(start(s));
+            stop = max(at, int64_t{0}) + 1;
+        }
     }
     // Every workgroup has one row tile, and the ones with the most keys go first: the one of rank at by the tokens
     // before its end (counted in row tiles), of every 256 sequences (where there are many rows: 64).  Tile t of a
@@ -512,69 +525,63 @@ struct Piece {
             u.tile = static_cast<int>((static_cast<int64_t>(u.n) * a.group + ROWS - 1) / ROWS) - 1 - rank;
             return u.tile >= 0;
         }
-        for (int b0 = 0; b0 < p.count; b0 += 64 * kSets) {
-            int first[kSets], n[kSets], length[kSets], tiles[kSets], lowest[kSets], all = 0, end = 0, below = 0;
-            constexpr int kHighest = 1 << 29;
+        int first[kSets], n[kSets], length[kSets], tiles[kSets], lowest[kSets], all = 0, end = 0, below = 0;
+        constexpr int kHighest = 1 << 29;
 #pragma unroll
-            for (int k = 0; k < kSets; ++k) {
-                const int b = b0 + 64 * k + lane;
-                first[k] = n[k] = length[k] = 0;
-                if (b < p.count) {
-                    first[k] = offset_of(p, b);
-                    n[k] = max(offset_of(p, b + 1) - first[k], 0);
-                    length[k] = max(p.lengths[b], 0);  // (without tokens nothing is seen)
-                }
+        for (int k = 0; k < kSets; ++k) {
+            const int b = kept_b + 64 * k + lane;
+            first[k] = n[k] = length[k] = 0;
+            if (b < p.count) {
+                first[k] = offset_of(p, b);
+                n[k] = max(offset_of(p, b + 1) - first[k], 0);
+                length[k] = max(p.lengths[b], 0);  // (without tokens nothing is seen)
             }
-#pragma unroll
-            for (int k = 0; k < kSets; ++k) {
-                tiles[k] = static_cast<int>((static_cast<int64_t>(n[k]) * a.group + ROWS - 1) / ROWS);
-                const int64_t context = static_cast<int64_t>(max(length[k] - n[k], 0)) * a.group / ROWS;
-                lowest[k] = static_cast<int>(min(context, int64_t{kHighest}));
-                all += tiles[k];
-                if (tiles[k]) {
-                    end = max(end, lowest[k] + tiles[k]);
-                    below = max(below, kHighest - lowest[k]);
-                }
-            }
-            all = reduced(all, sum);
-            if (rank >= all) {
-                rank -= all;
-                continue;
-            }
-            const auto larger = [](int x, int y) { return max(x, y); };
-            int low = kHighest - reduced(below, larger), high = reduced(end, larger), above = 0;
-            while (high - low > 1) {
-                const int middle = (low + high) >> 1;
-                int more = 0;
-#pragma unroll
-                for (int k = 0; k < kSets; ++k) more += min(max(lowest[k] + tiles[k] - middle, 0), tiles[k]);
-                more = reduced(more, sum);
-                if (more > rank) {
-                    low = middle;
-                } else {
-                    high = middle;
-                    above = more;
-                }
-            }
-            int index = rank - above;  // among those of the level
-#pragma unroll
-            for (int k = 0; k < kSets; ++k) {
-                uint64_t level = __ballot(lowest[k] <= low && low < lowest[k] + tiles[k]);
-                if (index < __popcll(level)) {
-                    for (; index > 0; --index) level &= level - 1;
-                    const int l = __builtin_ctzll(level);
-                    u.b = b0 + 64 * k + l;
-                    u.first = __builtin_amdgcn_readlane(first[k], l);
-                    u.n = __builtin_amdgcn_readlane(n[k], l);
-                    u.length = __builtin_amdgcn_readlane(length[k], l);
-                    u.tile = low - __builtin_amdgcn_readlane(lowest[k], l);
-                    return true;
-                }
-                index -= __popcll(level);
-            }
-            return false;  // (offsets out of order, more tiles than a word counts)
         }
-        return false;
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+            tiles[k] = static_cast<int>((static_cast<int64_t>(n[k]) * a.group + ROWS - 1) / ROWS);
+            const int64_t context = static_cast<int64_t>(max(length[k] - n[k], 0)) * a.group / ROWS;
+            lowest[k] = static_cast<int>(min(context, int64_t{kHighest}));
+            all += tiles[k];
+            if (tiles[k]) {
+                end = max(end, lowest[k] + tiles[k]);
+                below = max(below, kHighest - lowest[k]);
+            }
+        }
+        all = reduced(all, sum);
+        if (rank < 0 || rank >= all) return false;
+        const auto larger = [](int x, int y) { return max(x, y); };
+        int low = kHighest - reduced(below, larger), high = reduced(end, larger), above = 0;
+        while (high - low > 1) {
+            const int middle = (low + high) >> 1;
+            int more = 0;
+#pragma unroll
+            for (int k = 0; k < kSets; ++k) more += min(max(lowest[k] + tiles[k] - middle, 0), tiles[k]);
+            more = reduced(more, sum);
+            if (more > rank) {
+                low = middle;
+            } else {
+                high = middle;
+                above = more;
+            }
+        }
+        int index = rank - above;  // among those of the level
+#pragma unroll
+        for (int k = 0; k < kSets; ++k) {
+            uint64_t level = __ballot(lowest[k] <= low && low < lowest[k] + tiles[k]);
+            if (index < __popcll(level)) {
+                for (; index > 0; --index) level &= level - 1;
+                const int l = __builtin_ctzll(level);
+                u.b = kept_b + 64 * k + l;
+                u.first = __builtin_amdgcn_readlane(first[k], l);
+                u.n = __builtin_amdgcn_readlane(n[k], l);
+                u.length = __builtin_amdgcn_readlane(length[k], l);
+                u.tile = low - __builtin_amdgcn_readlane(lowest[k], l);
+                return true;
+            }
+            index -= __popcll(level);
+        }
+        return false;  // (offsets out of order, more tiles than a word counts)
     }
     // The piece's next unit; false behind its last.  Every lane has the same.
     __device__ bool next(Unit &u) {
@@ -1475,13 +1482,14 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
     if (tiles >= target || (static_cast<int64_t>(a.p.max_pages) << a.p.shift) <= static_cast<int64_t>(least) * KT) target = 0;
     a.target = static_cast<int>(target);
     a.least = least;
+    a.slots = static_cast<int64_t>(a.p.tokens) * a.group / ROWS + a.p.count;
     const int64_t units = tiles + target;
-    if (units * heads * threads > UINT32_MAX) return Q4K_ERR_LAUNCH;
+    const int64_t workgroups = target ? target : a.p.count > sequences_at_once(ROWS) ? a.slots : tiles;
+    if (max(units, workgroups) * heads * threads > UINT32_MAX) return Q4K_ERR_LAUNCH;
     a.units = static_cast<int>(units);
     if (target) {
         const size_t rows = static_cast<size_t>(units) * heads * ROWS;
         float *ws = nullptr;
-        a.slots = static_cast<int64_t>(a.p.tokens) * a.group / ROWS + a.p.count;
         const size_t bytes = rows * (a.p.head_dim + 2) * sizeof(float) + a.slots * sizeof(Part);
         if (workspace(stream, bytes, &ws, 0) != hipSuccess) return Q4K_ERR_ALLOC;
         a.part = ws;
@@ -1491,7 +1499,7 @@ int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least
         if (kJoined && counters(stream, &a.counters, &a.next) != hipSuccess) return Q4K_ERR_ALLOC;
     }
     if (lds > 65536 && allow_dynamic_lds(reinterpret_cast<const void *>(kernel), lds) != hipSuccess) return Q4K_ERR_LAUNCH;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((target ? target : tiles) * heads)), dim3(threads), lds, stream, a);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(workgroups * heads)), dim3(threads), lds, stream, a);
     if (hipGetLastError() != hipSuccess) return Q4K_ERR_LAUNCH;
     if constexpr (!kJoined) {
         if (target) {
