@@ -68,8 +68,9 @@ struct Attend {
     int q_heads;
     int group;   // query heads of a key head
     int target;  // split: workgroups of a key head; 0: one for every row tile
+    int spread;  // not split: workgroups of a key head if the lengths are so uneven that it is after all; 0: it never is
     int least;   // split: key tiles of a workgroup at least
-    int units;   // of a key head, at most (without a split: row tiles)
+    int units;   // split: of a key head, at most
     float scale;
 };
 
@@ -358,9 +359,12 @@ __device__ __forceinline__ bool set_apart(uint8_t *v, int at, uint8_t *marks) {
 // there are fewer row tiles than workgroups that the card holds (a.target), the
 // line is cut into that many equal pieces, so that all of them end at the same
 // time whatever the lengths are; workgroup w takes piece w.  What it has of a row
-// tile is a unit, number w + (number of the row tile): either number grows by
-// one from unit to unit, so a row tile's units follow each other.  With as many
-// row tiles or more, every workgroup takes one, the most keys first.
+// tile is a unit.  At most one row tile begins in a workgroup and goes on in the
+// next: what workgroup w has of the one that begins in w0 has number w0 + w, so a
+// row tile's units follow each other, and the next such row tile (which begins in
+// the last one's workgroup or later) has higher numbers.  With as many row tiles
+// or more, every workgroup takes one, the most keys first; but where the longest
+// would take far longer than its share (a.spread), the line is cut all the same.
 
 struct Unit {
     int b, first, n;  // sequence, its first row of q, its new tokens
@@ -369,7 +373,7 @@ struct Unit {
     int begin, end;   // key tiles
     int64_t number;
     int unit0, units;  // the row tile's
-    int64_t row_tile;  // its number
+    int64_t w0;        // the workgroup that it begins in
 };
 
 // Where the plan of a sequence's row tile is kept (below tokens * group / ROWS + count).
@@ -398,12 +402,12 @@ template <int ROWS, int KT>
 struct Span {
     int first, n, length, key_tiles;
     int64_t tiles, line, tiles_sum, line_sum;
-    __device__ Span(const Attend &a, int b, int64_t tiles_before, int64_t line_before) {
+    __device__ Span(const Attend &a, bool line_wanted, int b, int64_t tiles_before, int64_t line_before) {
         const Paged &p = a.p;
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));  // (no addresses kept from one unit to the next)
         first = n = length = 0;
-        if (a.target && b + lane < p.count) {
+        if (line_wanted && b + lane < p.count) {
             first = offset_of(p, b + lane);
             n = max(offset_of(p, b + lane + 1) - first, 0);
             length = max(p.lengths[b + lane], 0);  // (without tokens nothing is seen)
@@ -413,7 +417,7 @@ struct Span {
         line = tiles * key_tiles;
         tiles_sum = tiles;
         line_sum = line;
-        if (p.count == 1 || !a.target) {  // (one user's token: 0.3 us less)
+        if (p.count == 1 || !line_wanted) {  // (one user's token: 0.3 us less)
             tiles_sum = uniform(tiles);
             line_sum = uniform(line);
             return;
@@ -446,6 +450,10 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return q;
 }
 
+__device__ __forceinline__ float uniform_of(float x) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // A sum (or largest) over a wave's lanes, of numbers not below 0; uniform.
 template <typename Op>
 __device__ __forceinline__ int reduced(int x, Op op) {
@@ -458,48 +466,67 @@ __device__ __forceinline__ int reduced(int x, Op op) {
     return __builtin_amdgcn_readlane(x, 63);
 }
 
+// As many row tiles as workgroups: their line is cut all the same where the longest context has so many key tiles,
+// and so many times a workgroup's share.  A workgroup by itself walks over 128 keys of 128 x 16 bits in 1.84 us, 512
+// at once in 6.5, so that the longest row tile lasts beyond the others from 3.5 times the share on.  (One token of
+// each of 64 sequences, one of them over 131072 keys and 63 over 300: 1870 us uncut and 127 cut; over 16000 keys and
+// 2000, 289 and 110; comparing the lengths costs 1% of a batch of 200 over 1000 keys.)
+constexpr int kUnevenTiles = 32;
+constexpr float kUneven = 4.f;
+
 // Sequences whose row tiles are ranked together.
 constexpr int sequences_at_once(int rows) { return rows < 128 ? 256 : 64; }
 
 // A workgroup's piece of the line.  kKeep: the 64 sequences last looked through stay
 // in registers; without it (where the products need them) they are looked through
-// again for every unit.
-template <int ROWS, int KT, bool kKeep>
+// again for every unit.  kCut: as many row tiles as workgroups may be cut (parts are joined without a launch).
+template <int ROWS, int KT, bool kKeep, bool kCut>
 struct Piece {
     typedef Span<ROWS, KT> S;
     const Attend &a;
     S kept;
     int kept_b;
+    int cut_target;
+    // Workgroups of a key head that share the line; 0: each has a row tile.
+    __device__ __forceinline__ int target() const { return kCut ? cut_target : a.target; }
     static constexpr int kAtOnce = sequences_at_once(ROWS), kSets = kAtOnce / 64;
     int64_t at, stop, size, workgroup;
 
-    __device__ Piece(const Attend &a_, int64_t w) : a(a_), kept(a_, 0, 0, 0), kept_b(0), workgroup(w) {
-        size = 1;
-        if (a.target) {
-            int64_t all = __shfl(kept.line_sum, 63), rows = __shfl(kept.tiles_sum, 63);
-            for (int b = 64; b < a.p.count; b += 64) {
-                const S x(a, b, rows, all);
-                all = __shfl(x.line_sum, 63);
-                rows = __shfl(x.tiles_sum, 63);
-            }
-            all = uniform(all);
-            // (16-row tiles over few keys: one key tile a workgroup as long as the parts are few, 500 keys 11.3 ->
-            // 9.8 us; with 32 parts of 4000 keys it took 15.7 us instead of 13.4)
-            const int least = kKeep && all <= 12 * uniform(rows) ? 1 : a.least;
-            size = max(uniform(quotient(all + a.target - 1, a.target)), static_cast<int64_t>(least));
+    __device__ Piece(const Attend &a_, int64_t w)
+        : a(a_), kept(a_, a_.target != 0, 0, 0, 0), kept_b(0), size(1), workgroup(w) {
+        if constexpr (kCut) cut_target = a.target;
+        if (target()) {
+            share_line();
+        } else {
+            at = w;
+            stop = at + 1;
         }
-        at = w * size;
-        stop = at + size;
         // Of more sequences than are ranked together, those that a workgroup's rank falls to begin at the
         // slot of their first tile (some slots have no tile).  (Going through the sets instead took 3000 us
         // for one token of each of 8192 sequences over 16 keys, with this 1070; of 65535, 139700 and 8800.)
-        if (!a.target && a.p.count > kAtOnce) {
+        if (!target() && a.p.count > kAtOnce) {
             const auto start = [&](int s) { return slot_of<ROWS>(a, s * kAtOnce, offset_of(a.p, s * kAtOnce), 0); };
             const int s = last_started((a.p.count + kAtOnce - 1) / kAtOnce, w, start);
             kept_b = s * kAtOnce;
             at = w - uniform(start(s));
             stop = max(at, int64_t{0}) + 1;
         }
+    }
+    // The line's total, and the workgroup's piece of it.
+    __device__ __forceinline__ void share_line() {
+        int64_t all = __shfl(kept.line_sum, 63), rows = __shfl(kept.tiles_sum, 63);
+        for (int b = 64; b < a.p.count; b += 64) {
+            const S x(a, true, b, rows, all);
+            all = __shfl(x.line_sum, 63);
+            rows = __shfl(x.tiles_sum, 63);
+        }
+        all = uniform(all);
+        // (16-row tiles over few keys: one key tile a workgroup as long as the parts are few, 500 keys 11.3 ->
+        // 9.8 us; with 32 parts of 4000 keys it took 15.7 us instead of 13.4)
+        const int least = kKeep && all <= 12 * uniform(rows) ? 1 : a.least;
+        size = max(uniform(quotient(all + target() - 1, target())), static_cast<int64_t>(least));
+        at = workgroup * size;
+        stop = !kCut || workgroup < target() ? at + size : at;
     }
     // Every workgroup has one row tile, and the ones with the most keys go first: the one of rank at by the tokens
     // before its end (counted in row tiles), of every 256 sequences (where there are many rows: 64).  Tile t of a
@@ -515,7 +542,7 @@ struct Piece {
         at = stop;
         u.begin = 0;
         u.end = INT_MAX;
-        u.number = u.row_tile = u.unit0 = 0;
+        u.number = u.w0 = u.unit0 = 0;
         u.units = 1;
         if (p.count == 1) {  // (1 us less)
             u.b = 0;
@@ -548,9 +575,30 @@ struct Piece {
                 below = max(below, kHighest - lowest[k]);
             }
         }
+        const auto larger = [](int x, int y) { return max(x, y); };
+        if constexpr (kCut) {
+            if (a.spread) {  // (all sequences are in these sets)
+                float line = 0.f;
+                int longest = 0;
+#pragma unroll
+                for (int k = 0; k < kSets; ++k) {
+                    const int key_tiles = max((min(length[k], p.max_pages << p.shift) + KT - 1) / KT, 1);
+                    line += static_cast<float>(tiles[k]) * static_cast<float>(key_tiles);
+                    longest = max(longest, tiles[k] ? key_tiles : 0);
+                }
+#pragma unroll
+                for (int o = 32; o > 0; o >>= 1) line += __shfl_xor(line, o);
+                longest = reduced(longest, larger);
+                if (longest >= kUnevenTiles && static_cast<float>(longest) * static_cast<float>(a.spread) > kUneven * uniform_of(line)) {
+                    cut_target = a.spread;
+                    kept = S(a, true, 0, 0, 0);
+                    share_line();
+                    return false;
+                }
+            }
+        }
         all = reduced(all, sum);
         if (rank < 0 || rank >= all) return false;
-        const auto larger = [](int x, int y) { return max(x, y); };
         int low = kHighest - reduced(below, larger), high = reduced(end, larger), above = 0;
         while (high - low > 1) {
             const int middle = (low + high) >> 1;
@@ -585,17 +633,20 @@ struct Piece {
     }
     // The piece's next unit; false behind its last.  Every lane has the same.
     __device__ bool next(Unit &u) {
-        if (!a.target) return most_keys_first(u);
+        if (!target()) {
+            const bool taken = most_keys_first(u);
+            if (!target()) return taken;
+        }
         if (at >= stop) return false;
         if constexpr (!kKeep) {
-            kept = S(a, 0, 0, 0);
+            kept = S(a, true, 0, 0, 0);
             kept_b = 0;
         }
         uint64_t behind;
         while ((behind = __ballot(kept.line_sum > at)) == 0) {
             kept_b += 64;
             if (kept_b >= a.p.count) return false;
-            kept = S(a, kept_b, __shfl(kept.tiles_sum, 63), __shfl(kept.line_sum, 63));
+            kept = S(a, true, kept_b, __shfl(kept.tiles_sum, 63), __shfl(kept.line_sum, 63));
         }
         const int l = __builtin_ctzll(behind);
         u.b = kept_b + l;
@@ -608,12 +659,11 @@ struct Piece {
         u.begin = static_cast<int>(rest - static_cast<int64_t>(u.tile) * keys);
         u.end = static_cast<int>(min(static_cast<int64_t>(keys), u.begin + (stop - at)));
         const int64_t begin = at - u.begin;  // the row tile's place on the line
-        u.row_tile = uniform(__shfl(kept.tiles_sum - kept.tiles, l)) + u.tile;
-        u.number = workgroup + u.row_tile;
-        const int64_t w0 = u.begin == 0 ? workgroup : uniform(quotient(begin, size));
+        u.w0 = u.begin == 0 ? workgroup : uniform(quotient(begin, size));
         const int64_t w1 = begin + keys <= stop ? workgroup : uniform(quotient(begin + keys - 1, size));
-        u.unit0 = static_cast<int>(min(w0 + u.row_tile, static_cast<int64_t>(a.units)));
-        u.units = static_cast<int>(w1 - w0) + 1;
+        u.number = u.w0 + workgroup;
+        u.unit0 = static_cast<int>(min(2 * u.w0, static_cast<int64_t>(a.units)));
+        u.units = static_cast<int>(w1 - u.w0) + 1;
         at += u.end - u.begin;
         return true;
     }
@@ -712,7 +762,7 @@ __global__ __launch_bounds__(256, (TileShape<kType, DP>::kPerCu)) void attend_ti
     uint8_t *const marks = lds + 4 * S::kBytes;
     int *const flag = reinterpret_cast<int *>(marks + S::kMarks);
     const int head = blockIdx.x % a.p.kv_heads;
-    Piece<kTileRows, KT, false> piece(a, blockIdx.x / a.p.kv_heads);
+    Piece<kTileRows, KT, false, false> piece(a, blockIdx.x / a.p.kv_heads);
     for (Unit u; piece.next(u); __syncthreads()) {
         int thread = threadIdx.x;
         asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
@@ -1022,11 +1072,11 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (F
     constexpr int RB = S::RB, KT = 32 * S::kWaves, NS = DP / 32, ND = DP / 16, kRows = S::kRows;
     extern __shared__ __align__(16) uint8_t lds[];
     int *const ended = reinterpret_cast<int *>(lds + S::kEnded);
-    if (S::kJoined && a.target && blockIdx.x == 0)
+    if (S::kJoined && a.next && blockIdx.x == 0)
         for (int i = threadIdx.x; i < kCounters; i += S::kWaves * 64)
             __hip_atomic_store(a.next + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int head = blockIdx.x % a.p.kv_heads;
-    Piece<kRows, KT, true> piece(a, blockIdx.x / a.p.kv_heads);
+    Piece<kRows, KT, true, S::kJoined> piece(a, blockIdx.x / a.p.kv_heads);
     for (Unit u; piece.next(u); __syncthreads()) {
         int thread = threadIdx.x;
         asm volatile("" : "+v"(thread));  // (what follows from it is worked out for every unit, not kept over them)
@@ -1286,7 +1336,7 @@ __global__ __launch_bounds__((FewShape<kType, DP, NB, kPaired>::kWaves * 64), (F
         __syncthreads();
         const int quads = a.p.head_dim / 4;
         // (offsets out of order can give more units or row tiles than there is room for)
-        const int64_t counter = u.row_tile * a.p.kv_heads + head;
+        const int64_t counter = u.w0 * a.p.kv_heads + head;
         const bool shared = u.units > 1 && u.unit0 + u.units <= a.units && (!S::kJoined || counter < kCounters);
         const int at_once = S::kWaves * 64 / quads;  // rows
         const auto at_of = [&](int r) { return *reinterpret_cast<const int64_t *>(po + r * kStride + DP + 2); };
@@ -1477,25 +1527,30 @@ int64_t tiles_at_most(const Attend &a, int rows) {
 template <int ROWS, int KT, bool kJoined, class Kernel>
 int launch(Attend &a, Kernel kernel, int threads, int lds, int per_cu, int least, hipStream_t stream) {
     const int64_t tiles = tiles_at_most(a, ROWS), heads = a.p.kv_heads;
+    const int64_t capacity = static_cast<int64_t>(a.p.max_pages) << a.p.shift;
     int64_t target = (static_cast<int64_t>(kCus) * per_cu + heads - 1) / heads;
+    const int64_t held = target;
     // (as many row tiles, or not two workgroups' worth of keys in the longest sequence that can be)
-    if (tiles >= target || (static_cast<int64_t>(a.p.max_pages) << a.p.shift) <= static_cast<int64_t>(least) * KT) target = 0;
+    if (tiles >= target || capacity <= static_cast<int64_t>(least) * KT) target = 0;
+    // (lengths may be uneven: several sequences, as many as a workgroup ranks, and a table wide enough)
+    const bool cut = kJoined && !target && held > 1 && a.p.count > 1 && a.p.count <= sequences_at_once(ROWS) &&
+                     capacity >= kUnevenTiles * KT;
     a.target = static_cast<int>(target);
+    a.spread = cut ? static_cast<int>(held) : 0;
     a.least = least;
     a.slots = static_cast<int64_t>(a.p.tokens) * a.group / ROWS + a.p.count;
-    const int64_t units = tiles + target;
+    a.units = static_cast<int>(2 * held);
     const int64_t workgroups = target ? target : a.p.count > sequences_at_once(ROWS) ? a.slots : tiles;
-    if (max(units, workgroups) * heads * threads > UINT32_MAX) return Q4K_ERR_LAUNCH;
-    a.units = static_cast<int>(units);
-    if (target) {
-        const size_t rows = static_cast<size_t>(units) * heads * ROWS;
+    if (workgroups * heads * threads > UINT32_MAX) return Q4K_ERR_LAUNCH;
+    if (target || cut) {
+        const size_t rows = static_cast<size_t>(a.units) * heads * ROWS;
         float *ws = nullptr;
-        const size_t bytes = rows * (a.p.head_dim + 2) * sizeof(float) + a.slots * sizeof(Part);
+        const size_t bytes = rows * (a.p.head_dim + 2) * sizeof(float) + (target ? a.slots * sizeof(Part) : 0);
         if (workspace(stream, bytes, &ws, 0) != hipSuccess) return Q4K_ERR_ALLOC;
         a.part = ws;
         a.part_ml = ws + rows * a.p.head_dim;
         a.plan = reinterpret_cast<Part *>(a.part_ml + 2 * rows);
-        // (row tiles of all key heads: below target * heads less heads, so below kCus * per_cu)
+        // (row tiles that are cut, of all key heads: one for each workgroup but the last of a head, below kCus * per_cu)
         if (kJoined && counters(stream, &a.counters, &a.next) != hipSuccess) return Q4K_ERR_ALLOC;
     }
     if (lds > 65536 && allow_dynamic_lds(reinterpret_cast<const void *>(kernel), lds) != hipSuccess) return Q4K_ERR_LAUNCH;

@@ -36,10 +36,11 @@
  * count == 0 (M or N zero) is a successful no-op.  The arrays are not to be
  * changed while a call that reads them runs.
  *
- * Workspace.  Attention over few row tiles (256 workgroups on the card or
- * less: single tokens, short chunks, trees) is split along the keys and keeps
- * its parts there, for each part 4 * (head_dim + 2) bytes a row of its tile (16
- * to 128 rows), at most 3 * 512 parts, and 8 KB of counters that every call
+ * Workspace.  Attention over few row tiles (fewer than 512 over all key heads,
+ * 256 for the kernels that have a CU to themselves: single tokens of a batch,
+ * chunks, trees, short prompts), or over contexts of very different lengths, is
+ * split along the keys and keeps its parts there, for each part
+ * 4 * (head_dim + 2) bytes a row of its tile (16 to 128 rows), at most 4 * 512 parts, and 8 KB of counters that every call
  * leaves at zero.  So make one eager call of each shape before a graph
  * capture (an attention call that counts, captured on a stream that has no
  * counters yet, is Q4K_ERR_ALLOC); and host threads that share a stream take

@@ -5,7 +5,7 @@ import pytest
 
 import gguf_q4_dequant_amd as q4k
 from tests.gpu_helpers import to_dev
-from tests.layer_reference import Paged, attention, rng_of, tolerance
+from tests.layer_reference import TYPES, Paged, attention, rng_of, tolerance, tree_mask
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,59 @@ def test_many_sequences():
     for b in range(B):
         j = int(p.lengths[b]) - 1
         assert np.array_equal(stored[p.table[b, j // 8], 0, j % 8], k[b, 0].astype(np.float16).astype(np.float32))
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("B,longs", [(65, (5000,)), (200, (4200, 6100, 90)), (256, (7000, 7000)), (257, (6000,)), (1000, (6000,))])
+def test_uneven_batches(B, longs, kind):
+    """A row tile a workgroup, or the line cut where the longest context is far above the others' (up to 256
+    sequences); sequences without new tokens and without a context; causal and with a mask."""
+    rng = rng_of(142, B, TYPES.index(kind))
+    sizes = [(int(c), int(n)) for c, n in zip(rng.integers(0, 30, B), rng.integers(0, 3, B))]
+    for c in longs:
+        sizes[int(rng.integers(B))] = (c, 2)
+    p = Paged(rng, sizes, 8, 16, 16, kind, extra_rows=1)
+    q = rng.standard_normal((p.T, 16, 16)).astype(np.float32)
+    cache, seqs = p.on_device()
+    out = to_dev(np.full(q.shape, 7.25, np.float32))
+    mask = tree_mask(rng, sizes, 1, 1)
+    for m in (None, mask):
+        if m is None:
+            q4k.attention(to_dev(q), cache, seqs, out=out)
+        else:
+            q4k.attention_tree(to_dev(q), cache, seqs, to_dev(m.view(np.int32)), out=out)
+        got = out.cpu().numpy()
+        assert (got[-1] == 7.25).all()
+        with np.errstate(invalid="ignore"):
+            want, S, A = attention(p, q, 0.25, m, 1)
+        off, tol = np.abs(got - want)[:-1], tolerance(p, S, A, max(longs))[:-1]
+        assert (off <= tol).all(), float((off / tol).max())
+
+
+def test_uneven_batches_in_a_graph():
+    """Whether the line is cut is found on the device: lengths that change between replays."""
+    import torch
+    rng = rng_of(143)
+    p = Paged(rng, [(6000, 1)] + [(int(c), 1) for c in rng.integers(0, 60, 79)], 8, 64, 16, "f16")
+    cache, seqs = p.on_device()
+    q = to_dev(rng.standard_normal((80, 16, 64)).astype(np.float32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q4k.attention(q, cache, seqs)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs = [q4k.attention(q, cache, seqs) for _ in range(2)]
+    torch.cuda.synchronize()
+    for first in (6001, 40, 3000, 6001, 0, 4500):
+        seqs.lengths[0] = first
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        want = q4k.attention(q, cache, seqs)
+        assert all(torch.equal(o, want) for o in outs), first
+        p.lengths[0] = first
+        with np.errstate(invalid="ignore"):
+            exact, S, A = attention(p, q.cpu().numpy(), 0.125)
+        assert (np.abs(want.cpu().numpy() - exact) <= tolerance(p, S, A, 6001)).all(), first
