@@ -437,7 +437,9 @@ struct Span {
 
 // a / b of uniform numbers, a not negative, b positive, by way of a double (the
 // compiler's four divisions of 64 bits took 2 us of a workgroup's start).  The
-// double is off by one where the quotient is below 2^52, and the remainder says so.
+// hardware's reciprocal is far coarser than a double, so that the first quotient may be
+// off by more than one where it is large; the loop makes it exact, by a true division
+// of what remains.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     asm volatile("" : "+v"(b));  // (its double is not kept over the products)
     int64_t q = static_cast<int64_t>(static_cast<double>(a) * __builtin_amdgcn_rcp(static_cast<double>(b)));
@@ -1578,13 +1580,18 @@ int launch_few(Attend &a, hipStream_t stream) {
 
 template <int kType, int DP>
 int launch_shape(Attend &a, hipStream_t stream) {
-    // Rows of a sequence on average: the smallest tiles that hold them (as far as the registers go).
+    // Rows of a sequence on average: the smallest tiles that hold them (as far as the registers go).  (The lengths
+    // are on the device, so a batch of unlike sequences takes what its average asks for: 31 tokens and a chunk of 256,
+    // all behind 2000 keys, 32/8 heads of 128 x 16 bits, 142 us where the two alone take 45 and 43; with a chunk of 64
+    // 51 against 45 and 30; seven tokens and a chunk of 512 74 against 17 and 62.)
     constexpr bool kBf16 = kType == Q4K_KV_BF16;
     const int64_t rows = (static_cast<int64_t>(a.p.tokens) * a.group + a.p.count - 1) / a.p.count;
     // Few tiles of 16 rows over a short context: each takes its keys by itself, which costs less than
     // the wider tiles' longer steps and second launch (8, 16 and 32 tokens, four query heads a key head,
-    // 4000 keys of 128 x 16 bits: 21 -> 18, 30 -> 18, 27 -> 23 us; from 8000 keys on the keys read again
-    // cost more: 22 -> 28, 30 -> 32, 28 -> 41).  The table's width says how long a context can be.
+    // 4000 keys of 128 x 16 bits: 21 -> 18, 29 -> 18, 27 -> 20 us; from 8000 keys on the keys read again
+    // cost more: 22 -> 28, 30 -> 32, 28 -> 41).  The table's width says how long a context can be.  With more rows
+    // the gain gets small over 4000 keys (33, 48 and 64 tokens 27 -> 26, 28 -> 29, 30 -> 26 us, two chunks of 32
+    // 37 -> 37) and stays over 1000 (28 -> 18, 30 -> 20, 33 -> 18): the limit is on the safe side.
     const bool narrow = rows <= 128 && tiles_at_most(a, 16) * a.p.kv_heads <= kCus / 4 &&
                         static_cast<int64_t>(a.p.max_pages) << a.p.shift <= 6000;
     if (rows <= 16 || narrow) {

@@ -1,9 +1,10 @@
 // Residual addition and root-mean-square norm (include/q4k_layer.h).
 //
-// One workgroup per row: every value is read once and kept in registers (rows
-// up to kThreads * kHold * 4 values), the sum of squares is taken in double,
-// and the row is written once.  Longer rows are read a second time.  Memory bounds
-// it: 4096 rows of 5120 (336 MB) 67.5 us, 5.0 TB/s; one row of 2048 2.9 us, a launch's own time.
+// One workgroup per row: its first kThreads * kHold * 4 = 4096 values are read once
+// and kept in registers, the sum of squares is taken in double, and the row is
+// written once.  What a longer row has behind them is read a second time (of 5120
+// values the last 1024, from the L2).  Memory bounds it: 4096 rows of 5120 (336 MB)
+// 67.5 us, 5.0 TB/s; one row of 2048 2.9 us, a launch's own time.
 #include <math.h>
 
 #include "../../include/q4k_layer.h"

@@ -40,12 +40,13 @@
  * 256 for the kernels that have a CU to themselves: single tokens of a batch,
  * chunks, trees, short prompts), or over contexts of very different lengths, is
  * split along the keys and keeps its parts there, for each part
- * 4 * (head_dim + 2) bytes a row of its tile (16 to 128 rows), at most 4 * 512 parts, and 8 KB of counters that every call
- * leaves at zero.  So make one eager call of each shape before a graph
- * capture (an attention call that counts, captured on a stream that has no
- * counters yet, is Q4K_ERR_ALLOC); and host threads that share a stream take
- * turns, and so do the replays of graphs captured on one stream.  Where they do
- * not, the rows of those calls hold unspecified values; later calls are right.
+ * 4 * (head_dim + 2) bytes a row of its tile (16 to 128 rows), at most 4 * 512
+ * parts, and 8 KB of counters that every call leaves at zero.  So make one eager
+ * call of each shape before a graph capture (an attention call that counts,
+ * captured on a stream that has no counters yet, is Q4K_ERR_ALLOC); and host
+ * threads that share a stream take turns, and so do the replays of graphs
+ * captured on one stream.  Where they do not, the rows of those calls hold
+ * unspecified values; later calls are right.
  */
 #ifndef Q4K_LAYER_H
 #define Q4K_LAYER_H
