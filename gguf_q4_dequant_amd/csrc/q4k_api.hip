@@ -72,11 +72,12 @@ struct Buffer {
 std::mutex g_ws_mutex;
 
 // What tells streams apart: the handle, and for hipStreamPerThread, one handle for a stream
-// of every thread, a number of the thread's own (odd, as no other handle is).
+// of every thread, a number of the thread's own (odd and above 1, as no other handle is:
+// hipStreamLegacy is 1, the rest are addresses).
 uintptr_t stream_key(hipStream_t stream) {
     if (stream != hipStreamPerThread) return reinterpret_cast<uintptr_t>(stream);
     static std::atomic<uintptr_t> threads{0};
-    thread_local const uintptr_t key = 2 * threads++ + 1;
+    thread_local const uintptr_t key = 2 * threads++ + 3;
     return key;
 }
 std::map<std::pair<std::pair<int, uintptr_t>, int>, Buffer> g_ws;

@@ -12,7 +12,7 @@ from tests.layer_reference import Paged, rng_of
 
 pytestmark = pytest.mark.gpu
 
-PER_THREAD = 2  # hipStreamPerThread
+LEGACY, PER_THREAD = 1, 2  # hipStreamLegacy, hipStreamPerThread
 
 
 def in_threads(work, repeats):
@@ -64,3 +64,21 @@ def test_products():
         work.append((lambda w=w, x=x, y=y: q4k.matmul(w, x, y, stream=PER_THREAD), y, want))
     torch.cuda.synchronize()
     in_threads(work, 30)
+
+
+def test_beside_the_null_streams_own_handle():
+    """One thread's calls on its stream, another's on hipStreamLegacy: two workspaces.  (The legacy stream
+    waits for blocking streams, and the per-thread stream is one, so they do not run at once here; the
+    results say that neither call takes the other's counters or parts.)"""
+    import torch
+    work = []
+    for n, handle in enumerate((PER_THREAD, LEGACY)):
+        rng = rng_of(111, n)
+        p = Paged(rng, [(2500 - 700 * n, 1), (50, 1)], 2, 64, 16, "f16")
+        cache, seqs = p.on_device()
+        q = to_dev(rng.standard_normal((p.T, 8, 64)).astype(np.float32))
+        want, out = q4k.attention(q, cache, seqs), torch.empty_like(q)
+        work.append((lambda q=q, c=cache, s=seqs, o=out, h=handle: (q4k.attention(q, c, s, out=o, stream=h),
+                                                                    torch.cuda.synchronize()), out, want))
+    torch.cuda.synchronize()
+    in_threads(work, 20)
