@@ -106,3 +106,50 @@ def test_uneven_batches_in_a_graph():
         with np.errstate(invalid="ignore"):
             exact, S, A = attention(p, q.cpu().numpy(), 0.125)
         assert (np.abs(want.cpu().numpy() - exact) <= tolerance(p, S, A, 6001)).all(), first
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("D", [48, 128, 256])
+def test_uneven_batches_of_every_kernel(D, kind):
+    """The kernels of few rows for other head sizes, with NaN keys over a stretch that one part has to itself."""
+    rng = rng_of(144, D, TYPES.index(kind))
+    sizes = [(int(c), 1 + b % 2) for b, c in enumerate(rng.integers(0, 50, 70))]
+    sizes[33] = (6000, 2)
+    sizes[50] = (4700, 1)
+    p = Paged(rng, sizes, 8, D, 32, kind)
+    q = rng.standard_normal((p.T, 16, D)).astype(np.float32)
+    cache, seqs = p.on_device()
+    got = q4k.attention(to_dev(q), cache, seqs).cpu().numpy()
+    keep = [33, 50, 0, 69]
+    rows = np.concatenate([np.arange(p.offsets[b], p.offsets[b + 1]) for b in keep])
+    few = Paged.__new__(Paged)
+    few.__dict__.update(p.__dict__)
+    few.sizes = [sizes[b] for b in keep]
+    few.table, few.lengths = p.table[keep], p.lengths[keep]
+    few.offsets = np.concatenate([[0], np.cumsum([n for _, n in few.sizes])])
+    want, S, A = attention(few, q[rows], D ** -0.5)
+    off, tol = np.abs(got[rows] - want), tolerance(few, S, A, 6002)
+    assert (off <= tol).all(), float((off / tol).max())
+    for page in p.table[50, :16]:
+        p.k[int(page), 3] = float("nan")
+    cache, seqs = p.on_device()
+    bad = q4k.attention(to_dev(q), cache, seqs).cpu().numpy()
+    hit = np.zeros(bad.shape, bool)
+    hit[p.offsets[50]:p.offsets[51], 6:8] = True
+    assert np.isnan(bad[hit]).all() and np.array_equal(bad[~hit], got[~hit])
+
+
+def test_uneven_batches_with_offsets_out_of_order():
+    """Rows hold anything, and nothing else is touched; the next call is right."""
+    import torch
+    rng = rng_of(145)
+    p = Paged(rng, [(6000, 1)] + [(int(c), 1) for c in rng.integers(0, 60, 79)], 8, 16, 16, "f16")
+    cache, seqs = p.on_device()
+    q = to_dev(rng.standard_normal((80, 16, 16)).astype(np.float32))
+    want = q4k.attention(q, cache, seqs)
+    guard = torch.full((3, *q.shape), 5.0, device="cuda")
+    for bad in (seqs.offsets.flip(0), seqs.offsets * 7 - 90, seqs.offsets[torch.randperm(81)], seqs.offsets % 9):
+        q4k.attention(q, cache, seqs._replace(offsets=bad.contiguous()), out=guard[1])
+        torch.cuda.synchronize()
+        assert (guard[0] == 5).all() and (guard[2] == 5).all()
+        assert torch.equal(q4k.attention(q, cache, seqs), want)
